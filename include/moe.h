@@ -56,7 +56,9 @@ extern "C" {
 enum moe_dtype {
   MOE_F32 = 0,  /* IEEE binary32 */
   MOE_BF16 = 1, /* bfloat16 */
-  MOE_E4M3 = 2  /* OCP FP8 E4M3 (max 448, no infinities), weights only, with fp32 scales */
+  MOE_E4M3 = 2, /* OCP FP8 E4M3 (max 448, no infinities), weights only, with fp32 scales */
+  MOE_MXFP4 = 3 /* OCP microscaled FP4: E2M1 codes, one power of two per 32 values of the reduction
+                   dimension; routed expert weights only, as images written by moe_mx_pack_weights */
 };
 
 /* Return codes. */
@@ -65,7 +67,8 @@ enum moe_status {
   MOE_ERR_NULL_ARG = -1,    /* a required pointer is NULL */
   MOE_ERR_BAD_DIMS = -2,    /* T < 0, D/E/I/top_k < 1, top_k > E, expert slice outside [0, E) */
   MOE_ERR_UNSUPPORTED = -3, /* dtype combination, D or I not a multiple of 64, E > 1024, top_k > 32,
-                               one expert's or the router's weight matrix of 2 GiB or more */
+                               one expert's or the router's weight matrix of 2 GiB or more; a call that
+                               does not take these dims (stated there) */
   MOE_ERR_WORKSPACE = -4,   /* ws_bytes smaller than moe_workspace_bytes(dims) */
   MOE_ERR_HIP = -5,         /* a kernel launch failed (see moe_last_hip_error) */
   MOE_ERR_SCRATCH_LIMIT = -6 /* moe_layer_forward_noalloc: the dims need more than MOE_STATIC_SCRATCH_BYTES */
@@ -95,7 +98,8 @@ typedef struct moe_dims {
   int32_t n_local;      /* local experts: ids expert_begin .. expert_begin + n_local - 1 */
   int32_t renormalize;  /* 1: kept weights sum to 1; 0: kept softmax entries as they are */
   int32_t act_dtype;    /* x, router weight, shared weights: MOE_F32 or MOE_BF16 */
-  int32_t w_dtype;      /* routed expert weights: MOE_F32 (with act F32), MOE_BF16 or MOE_E4M3 (with act BF16) */
+  int32_t w_dtype;      /* routed expert weights: MOE_F32 (with act F32), MOE_BF16, MOE_E4M3 or MOE_MXFP4 (with
+                           act BF16; MOE_MXFP4 with weight_layout MOE_LAYOUT_PACKED) */
   int32_t out_dtype;    /* y and expert outputs: MOE_F32 or MOE_BF16 */
   int32_t weight_layout;/* routed and shared expert weights: MOE_LAYOUT_ROWS or MOE_LAYOUT_PACKED */
 } moe_dims;
@@ -109,7 +113,7 @@ enum moe_layout {
 /* Weights of the layer (device pointers). */
 typedef struct moe_weights {
   const void* w_router;  /* [E][D] act_dtype; may be NULL when routing is given */
-  const void* w_gate;    /* [n_local][I][D] w_dtype */
+  const void* w_gate;    /* [n_local][I][D] w_dtype (MXFP4: n_local images, s_* unused) */
   const void* w_up;      /* [n_local][I][D] w_dtype */
   const void* w_down;    /* [n_local][D][I] w_dtype */
   const float* s_gate;   /* [n_local][I] per-output-channel scales (E4M3 only, else NULL) */
@@ -201,6 +205,9 @@ int moe_permute(const moe_dims* dims, const int32_t* packed, int32_t* counts, in
  *
  *   a_rows     if perm_token is NULL: grouped rows [N_a][D]; else x [T][D] and row r
  *              reads x[perm_token[r]].  act_dtype, or E4M3 codes when w_dtype is E4M3.
+ *              With w_dtype MXFP4 the bf16 rows are rounded to microscaled FP4 by the call (one
+ *              power of two per 32 values, see moe_mx_pack_weights), and so is h, from fp32:
+ *              both products are 4-bit by 4-bit with fp32 sums.
  *   a_scale    E4M3 only: fp32 scale per row of a_rows ([N_a], or [T] with perm_token)
  *   perm_token [N_a] int32 or NULL
  *   offsets    [n_local + 1] int32 (device)
@@ -313,6 +320,101 @@ int moe_pack_weights(int32_t dtype, int64_t n_mats, int32_t rows, int32_t cols, 
                      void* stream);
 
 /*
+ * Microscaled FP4 weights.  moe_mx_pack_weights rounds row-major matrices [rows][cols] to
+ * MOE_MXFP4 and writes each as an image of moe_mx_weight_bytes(1, rows, cols) bytes, the
+ * fragment-major order that the kernels stream with the scales beside their codes; a
+ * one-time transform at weight load time (17/32 byte per weight).  For each block of 32
+ * consecutive values of a row, with amax its largest magnitude:
+ *   e = floor(log2(amax)) - 2, at least -126 (0 for a zero block);
+ *   each value times 2^-e is rounded to the nearest of 0, .5, 1, 1.5, 2, 3, 4, 6 (ties to the
+ *   even code), magnitudes above 6 to 6.
+ * A block that holds a NaN or an infinity is stored as NaN.  moe_mx_unpack_weights writes the
+ * values the images stand for, exact in bf16 and fp32, e.g. to measure what the format costs
+ * with moe_audit on a bf16 layer.
+ *
+ *   src_dtype / dst_dtype  MOE_F32 or MOE_BF16
+ *   n_mats, rows, cols     as in moe_pack_weights: rows a multiple of 16, cols of 64
+ *   src, dst               device; images at 16-byte, rows at 16-byte aligned addresses
+ * moe_mx_weight_bytes returns 0 for sizes outside these rules.
+ */
+size_t moe_mx_weight_bytes(int64_t n_mats, int32_t rows, int32_t cols);
+int moe_mx_pack_weights(int32_t src_dtype, int64_t n_mats, int32_t rows, int32_t cols, const void* src, void* dst,
+                        void* stream);
+int moe_mx_unpack_weights(int32_t dst_dtype, int64_t n_mats, int32_t rows, int32_t cols, const void* src, void* dst,
+                          void* stream);
+
+/*
+ * moe_layer_forward for 1 to MOE_FEW_MAX_T tokens (a few requests' next tokens), in three
+ * launches, two with given routing: router logits; top-k and gate/up; down and combine.  The
+ * arguments, the result's definition, the error word and the workspace are
+ * moe_layer_forward's, for every w_dtype and layout it takes, with two differences:
+ *   - x and h are not quantised for MOE_E4M3 and MOE_MXFP4 weights (such a call is bound by the
+ *     weights' bytes, and the products run in bf16 on exact weight values), so y is closer to
+ *     the exact layer than moe_layer_forward's;
+ *   - a token that names one expert in several slots gets it once with the summed weight.
+ * The sum over experts is taken in another order than moe_layer_forward's; each call is
+ * deterministic.  Returns MOE_ERR_UNSUPPORTED for T > MOE_FEW_MAX_T.
+ */
+#define MOE_FEW_MAX_T 16
+int moe_layer_forward_few(const moe_dims* dims, const moe_weights* weights, const void* x, const int32_t* packed_in,
+                          const float* logit_bias, void* y, float* logits_out, int32_t* packed_out, void* ws,
+                          size_t ws_bytes, void* stream);
+
+/* How moe_norm's gate multiplies the block's output. */
+enum moe_gate {
+  MOE_GATE_NONE = 0,    /* not at all; gate is NULL */
+  MOE_GATE_TOKEN = 1,   /* gate [T] fp32 */
+  MOE_GATE_CHANNEL = 2, /* gate [D] act_dtype */
+  MOE_GATE_FULL = 3     /* gate [T][D] act_dtype */
+};
+
+/* Leaving a block and entering the next. */
+typedef struct moe_norm {
+  const void* w_post; /* [D] act_dtype: norm of the block's output, or NULL for none */
+  const void* gate;   /* see enum moe_gate */
+  const void* w_next; /* [D] act_dtype: pre-norm of the next block, or NULL for none */
+  int32_t gate_kind;
+  float res_scale;    /* factor of the residual stream */
+  float eps;          /* added to the mean square, at least 0 */
+} moe_norm;
+
+/*
+ * One pass over the residual stream between two blocks:
+ *   z = rms(y[t]) * w_post  (y[t] without w_post);   rms(v) = v / sqrt(mean(v^2) + eps)
+ *   r_out[t] = res_scale * r[t] + gate * z
+ *   x_next[t] = rms(r_out[t]) * w_next
+ * with fp32 statistics and products; x_next is taken from the unrounded r_out.  With y NULL
+ * the residual stream is only entered: x_next[t] = rms(r[t]) * w_next.
+ *
+ *   T, D       rows and width, any T >= 0 and 1 <= D <= 16384
+ *   act_dtype  of r, weights, gate (but the fp32 token gate), r_out, x_next: MOE_F32 or MOE_BF16
+ *   y_dtype    of y: MOE_F32, or MOE_BF16 with act_dtype BF16
+ *   y          [T][D] or NULL
+ *   r          [T][D];  r_out may be r itself, any other overlap of outputs with inputs is not allowed
+ *   r_out      [T][D] (NULL exactly if y is NULL)
+ *   x_next     [T][D] (NULL exactly if n->w_next is NULL)
+ */
+int moe_block_norm(int32_t T, int32_t D, int32_t act_dtype, int32_t y_dtype, const moe_norm* n, const void* y,
+                   const void* r, void* r_out, void* x_next, void* stream);
+
+/*
+ * A whole block around the residual stream r:
+ *   x = rms(r) * w_in (rounded to act_dtype), or x_in, the x_next of the block before;
+ *   y = the layer of x, routed by it: moe_layer_forward_few up to MOE_FEW_MAX_T tokens, else
+ *       moe_layer_forward, rounded to out_dtype;
+ *   r_out, x_next as moe_block_norm(n, y, r).
+ *
+ *   w_in, x_in   exactly one of them is given: w_in [D], x_in [T][D], act_dtype
+ *   r, r_out, x_next  act_dtype, as in moe_block_norm
+ *   ws           at least moe_block_workspace_bytes(dims) bytes (0 for invalid dims); the layer's
+ *                workspace, error word included, is its first part
+ */
+size_t moe_block_workspace_bytes(const moe_dims* dims);
+int moe_block_forward(const moe_dims* dims, const moe_weights* weights, const void* w_in, const void* x_in,
+                      const float* logit_bias, const moe_norm* n, const void* r, void* r_out, void* x_next, void* ws,
+                      size_t ws_bytes, void* stream);
+
+/*
  * Numerical audit: an fp32 shadow of the layer on sampled tokens, compared with the
  * layer's output.  For each sampled token t the reference is
  *   ref[t] = sum_j w[t][j] * W_down (silu(W_gate x_t) * (W_up x_t)) over the local slots
@@ -323,7 +425,8 @@ int moe_pack_weights(int32_t dtype, int64_t n_mats, int32_t rows, int32_t cols, 
  * of Playbook "Roofline Validation" checks low-precision results against a
  * high-precision evaluation.
  *
- *   dims, weights  as for moe_layer_forward (same layout, local slice and dtypes)
+ *   dims, weights  as for moe_layer_forward (same layout, local slice and dtypes; MOE_MXFP4 is not
+ *             taken: unpack the weights and audit them as MOE_BF16)
  *   x         [T][D] act_dtype: the hidden states the layer was run on
  *   packed    [T][2][top_k] int32: the routing the layer used (e.g. its packed_out)
  *   y         [T][D] out_dtype: the layer's output to audit

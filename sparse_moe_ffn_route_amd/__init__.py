@@ -20,8 +20,8 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libmoe_hip.so")
 
 # enum moe_dtype
-F32, BF16, E4M3 = 0, 1, 2
-_DTYPE_CODE = {"f32": F32, "bf16": BF16, "e4m3": E4M3}
+F32, BF16, E4M3, MXFP4 = 0, 1, 2, 3
+_DTYPE_CODE = {"f32": F32, "bf16": BF16, "e4m3": E4M3, "mxfp4": MXFP4}
 _TORCH_OF = {F32: torch.float32, BF16: torch.bfloat16, E4M3: torch.float8_e4m3fn}
 
 # enum moe_layout
@@ -33,12 +33,18 @@ OK, ERR_NULL_ARG, ERR_BAD_DIMS, ERR_UNSUPPORTED, ERR_WORKSPACE, ERR_HIP, ERR_SCR
 
 WS_ERROR_OFFSET = 0                     # MOE_WS_ERROR_OFFSET: byte offset of the workspace error word
 STATIC_SCRATCH_BYTES = 96 << 20         # MOE_STATIC_SCRATCH_BYTES
+FEW_MAX_T = 16                          # MOE_FEW_MAX_T
+
+# enum moe_gate
+GATE_NONE, GATE_TOKEN, GATE_CHANNEL, GATE_FULL = 0, 1, 2, 3
+_GATE_CODE = {"none": GATE_NONE, "token": GATE_TOKEN, "channel": GATE_CHANNEL, "full": GATE_FULL}
 
 # Symbols exported by the library (the entry points of include/moe.h).
 EXPORTS = (
     "moe_workspace_bytes", "moe_route", "moe_route_fused", "moe_permute", "moe_grouped_ffn",
     "moe_unpermute_combine", "moe_layer_forward", "moe_layer_forward_noalloc", "moe_audit_workspace_bytes", "moe_audit", "moe_pack_weights", "moe_hbm_read_probe", "moe_status_string", "moe_last_hip_error",
-    "moe_abi_version", "moe_mfma_peak_probe",
+    "moe_abi_version", "moe_mfma_peak_probe", "moe_mx_weight_bytes", "moe_mx_pack_weights", "moe_mx_unpack_weights",
+    "moe_layer_forward_few", "moe_block_norm", "moe_block_workspace_bytes", "moe_block_forward",
 )
 
 
@@ -57,6 +63,11 @@ class moe_dims(ctypes.Structure):
 class moe_weights(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in (
         "w_router", "w_gate", "w_up", "w_down", "s_gate", "s_up", "s_down", "sh_gate", "sh_up", "sh_down")]
+
+
+class moe_norm(ctypes.Structure):
+    _fields_ = [("w_post", ctypes.c_void_p), ("gate", ctypes.c_void_p), ("w_next", ctypes.c_void_p),
+                ("gate_kind", ctypes.c_int32), ("res_scale", ctypes.c_float), ("eps", ctypes.c_float)]
 
 
 _lib = None
@@ -101,6 +112,20 @@ def library() -> ctypes.CDLL:
     lib.moe_hbm_read_probe.restype = i32
     lib.moe_mfma_peak_probe.argtypes = [ctypes.c_int32, ctypes.c_int32, vp, vp]
     lib.moe_mfma_peak_probe.restype = i32
+    lib.moe_mx_weight_bytes.argtypes = [ctypes.c_int64, ctypes.c_int32, ctypes.c_int32]
+    lib.moe_mx_weight_bytes.restype = sz
+    for f in (lib.moe_mx_pack_weights, lib.moe_mx_unpack_weights):
+        f.argtypes = [ctypes.c_int32, ctypes.c_int64, ctypes.c_int32, ctypes.c_int32, vp, vp, vp]
+        f.restype = i32
+    np_ = ctypes.POINTER(moe_norm)
+    lib.moe_layer_forward_few.argtypes = [dp, wp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    lib.moe_layer_forward_few.restype = i32
+    lib.moe_block_norm.argtypes = [ctypes.c_int32] * 4 + [np_, vp, vp, vp, vp, vp]
+    lib.moe_block_norm.restype = i32
+    lib.moe_block_workspace_bytes.argtypes = [dp]
+    lib.moe_block_workspace_bytes.restype = sz
+    lib.moe_block_forward.argtypes = [dp, wp, vp, vp, vp, np_, vp, vp, vp, vp, sz, vp]
+    lib.moe_block_forward.restype = i32
     lib.moe_status_string.argtypes = [i32]
     lib.moe_status_string.restype = ctypes.c_char_p
     lib.moe_last_hip_error.argtypes = []
@@ -317,6 +342,122 @@ def moe_pack_weights(src: torch.Tensor, dst: Optional[torch.Tensor] = None, stre
     _check(library().moe_pack_weights(_CODE_OF_TORCH[src.dtype], n, rows, cols, _ptr(src), _ptr(dst),
                                       _stream(stream)), "moe_pack_weights")
     return dst
+
+
+def _mats(t: torch.Tensor):
+    if t.dim() == 2:
+        return (1, *t.shape)
+    if t.dim() == 3:
+        return tuple(t.shape)
+    raise ValueError("weights must be [rows][cols] or [n][rows][cols]")
+
+
+def moe_mx_weight_bytes(n_mats: int, rows: int, cols: int) -> int:
+    """Bytes of n_mats 4-bit images of [rows][cols] matrices."""
+    return int(library().moe_mx_weight_bytes(n_mats, rows, cols))
+
+
+def moe_mx_pack_weights(src: torch.Tensor, dst: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Round [n][rows][cols] (or [rows][cols]) fp32 or bf16 weights to microscaled FP4 images, uint8 [n][bytes]."""
+    n, rows, cols = _mats(src)
+    if src.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("weights must be float32 or bfloat16")
+    nbytes = moe_mx_weight_bytes(1, rows, cols)
+    if dst is None:
+        dst = torch.empty(n, nbytes, dtype=torch.uint8, device=src.device)
+    _need(dst, n * nbytes, "images")
+    _check(library().moe_mx_pack_weights(_CODE_OF_TORCH[src.dtype], n, rows, cols, _ptr(src), _ptr(dst),
+                                         _stream(stream)), "moe_mx_pack_weights")
+    return dst
+
+
+def moe_mx_unpack_weights(images: torch.Tensor, rows: int, cols: int, dtype: torch.dtype = torch.bfloat16,
+                          dst: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The values of n images (uint8 [n][bytes]) as [n][rows][cols] of float32 or bfloat16."""
+    nbytes = moe_mx_weight_bytes(1, rows, cols)
+    n = images.numel() // nbytes if nbytes else images.shape[0]
+    if dst is None:
+        dst = torch.empty(n, rows, cols, dtype=dtype, device=images.device)
+    if dst.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("values must be float32 or bfloat16")
+    if images.dtype != torch.uint8 or images.numel() != n * nbytes:
+        raise ValueError(f"images must be uint8, {nbytes} bytes each")
+    _need(dst, n * rows * cols * dst.element_size(), "values")
+    _check(library().moe_mx_unpack_weights(_CODE_OF_TORCH[dst.dtype], n, rows, cols, _ptr(images), _ptr(dst),
+                                           _stream(stream)), "moe_mx_unpack_weights")
+    return dst
+
+
+def moe_layer_forward_few(dims, weights: moe_weights, x, packed_in, logit_bias, y, logits_out=None, packed_out=None,
+                          ws=None, stream=None):
+    """moe_layer_forward for up to FEW_MAX_T tokens, in two launches after the router's."""
+    _check_io(dims, x=x, logits=logits_out, packed=packed_in, bias=logit_bias, y=y)
+    _need(packed_out, dims.T * 2 * dims.top_k * 4, "packed_out")
+    _check(library().moe_layer_forward_few(ctypes.byref(dims), ctypes.byref(weights), _ptr(x), _ptr(packed_in),
+                                           _ptr(logit_bias), _ptr(y), _ptr(logits_out), _ptr(packed_out), _ptr(ws),
+                                           ws.numel() if ws is not None else 0, _stream(stream)),
+           "moe_layer_forward_few")
+
+
+def _make_norm(T, D, act, w_post, gate, gate_kind, res_scale, eps, w_next) -> moe_norm:
+    """moe_norm after checks of its tensors' types and sizes."""
+    if gate_kind is None:
+        gate_kind = "none" if gate is None else "full" if gate.dim() == 2 else None
+        if gate_kind is None:
+            raise ValueError("a one-dimensional gate needs gate_kind 'token' or 'channel'")
+    kind = _GATE_CODE[gate_kind]
+    for t, what in ((w_post, "w_post"), (w_next, "w_next"), (gate if kind != GATE_TOKEN else None, "gate")):
+        if t is not None and t.dtype != act:
+            raise ValueError(f"{what}: {t.dtype}, the residual stream is {act}")
+    if kind == GATE_TOKEN and gate is not None and gate.dtype != torch.float32:
+        raise ValueError("a token gate is float32")
+    es = 4 if act == torch.float32 else 2
+    _need(w_post, D * es, "w_post")
+    _need(w_next, D * es, "w_next")
+    _need(gate, {GATE_NONE: 0, GATE_TOKEN: T * 4, GATE_CHANNEL: D * es, GATE_FULL: T * D * es}[kind], "gate")
+    return moe_norm(_ptr(w_post), _ptr(gate), _ptr(w_next), kind, res_scale, eps)
+
+
+def moe_block_norm(y, r, r_out=None, w_post=None, gate=None, gate_kind=None, res_scale=1.0, eps=1e-6, w_next=None,
+                   x_next=None, stream=None):
+    """Leave a block and enter the next on the residual stream r [T][D]; y None: only enter."""
+    if r.dim() != 2:
+        raise ValueError("r must be [T][D]")
+    T, D = r.shape
+    n = _make_norm(T, D, r.dtype, w_post, gate, gate_kind, res_scale, eps, w_next)
+    for t, what in ((r_out, "r_out"), (x_next, "x_next")):
+        if t is not None and t.dtype != r.dtype:
+            raise ValueError(f"{what}: {t.dtype}, the residual stream is {r.dtype}")
+        _need(t, T * D * r.element_size(), what)
+    _need(y, T * D * (y.element_size() if y is not None else 0), "y")
+    _check(library().moe_block_norm(T, D, _CODE_OF_TORCH.get(r.dtype, -1),
+                                    _CODE_OF_TORCH.get(y.dtype, -1) if y is not None else F32, ctypes.byref(n),
+                                    _ptr(y), _ptr(r), _ptr(r_out), _ptr(x_next), _stream(stream)), "moe_block_norm")
+
+
+def block_workspace(dims: moe_dims, device="cuda") -> torch.Tensor:
+    """A caller-owned scratch buffer of moe_block_workspace_bytes(dims) bytes."""
+    n = int(library().moe_block_workspace_bytes(ctypes.byref(dims)))
+    if n == 0:
+        raise MoeError(ERR_BAD_DIMS, "moe_block_workspace_bytes")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def moe_block_forward(dims, weights: moe_weights, r, r_out, w_in=None, x_in=None, logit_bias=None, w_post=None,
+                      gate=None, gate_kind=None, res_scale=1.0, eps=1e-6, w_next=None, x_next=None, ws=None,
+                      stream=None):
+    """Pre-norm (or x_in), the layer, and moe_block_norm on the residual stream r."""
+    act = _TORCH_OF.get(dims.act_dtype)
+    n = _make_norm(dims.T, dims.D, act, w_post, gate, gate_kind, res_scale, eps, w_next)
+    for t, what in ((r, "r"), (r_out, "r_out"), (x_next, "x_next"), (x_in, "x_in"), (w_in, "w_in")):
+        if t is not None and t.dtype != act:
+            raise ValueError(f"{what}: {t.dtype}, the layer's hidden states are {act}")
+        _need(t, (1 if what == "w_in" else dims.T) * dims.D * _ELEM_BYTES[dims.act_dtype], what)
+    _check_io(dims, bias=logit_bias)
+    _check(library().moe_block_forward(ctypes.byref(dims), ctypes.byref(weights), _ptr(w_in), _ptr(x_in),
+                                       _ptr(logit_bias), ctypes.byref(n), _ptr(r), _ptr(r_out), _ptr(x_next),
+                                       _ptr(ws), ws.numel() if ws is not None else 0, _stream(stream)),
+           "moe_block_forward")
 
 
 HBM_PROBE_SINK_WORDS = 16384

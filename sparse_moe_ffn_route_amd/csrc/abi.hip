@@ -10,6 +10,7 @@
 #include "moe.h"
 #include "common.hpp"
 #include "kernels.hpp"
+#include "mx.hpp"
 
 using namespace moe;
 
@@ -35,9 +36,10 @@ int check_dims(const moe_dims* d) {
   if (d->top_k > 32 || d->E > 1024 || d->n_local > kMaxLocalExperts) return MOE_ERR_UNSUPPORTED;
   if (d->D % 64 || d->I % 64 || d->I_shared % 64) return MOE_ERR_UNSUPPORTED;
   const bool f32 = d->act_dtype == MOE_F32 && d->w_dtype == MOE_F32 && d->out_dtype == MOE_F32;
-  const bool bf16 = d->act_dtype == MOE_BF16 && (d->w_dtype == MOE_BF16 || d->w_dtype == MOE_E4M3) &&
+  const bool bf16 = d->act_dtype == MOE_BF16 && (d->w_dtype == MOE_BF16 || d->w_dtype == MOE_E4M3 || d->w_dtype == MOE_MXFP4) &&
                     (d->out_dtype == MOE_BF16 || d->out_dtype == MOE_F32);
   if (!f32 && !bf16) return MOE_ERR_UNSUPPORTED;
+  if (d->w_dtype == MOE_MXFP4 && d->weight_layout != MOE_LAYOUT_PACKED) return MOE_ERR_UNSUPPORTED;
   // every row index and byte offset below fits the kernels' integer types
   const int64_t tk = static_cast<int64_t>(d->T) * d->top_k;
   if (tk > (1ll << 30) || static_cast<int64_t>(d->T) * d->E > (1ll << 31) - 1) return MOE_ERR_UNSUPPORTED;
@@ -84,8 +86,10 @@ int router_splits(const moe_dims& d) {
 struct Layout {
   size_t err, logits, logits_part, packed, hist, base, rank, bad, counts, offsets, tp_a, tp_b, perm_token, inv_pos;
   size_t cand_key, cand_id, cand_stats;
-  size_t xq, sx, h, h_sh, hq, sh, out_rows, total;
+  size_t xq, sx, h, h_sh, hq, sh, out_rows, few_h, few_h_sh, total;
 };
+
+bool is_few(const moe_dims& d) { return d.T <= kFewMaxT; }
 
 Layout layout(const moe_dims& d) {
   Layout L{};
@@ -97,7 +101,7 @@ Layout layout(const moe_dims& d) {
   };
   const size_t T = d.T, tk = static_cast<size_t>(d.T) * d.top_k, nl = d.n_local;
   const size_t U = perm_units(d.T, d.top_k);
-  const bool fp8 = d.w_dtype == MOE_E4M3;
+  const bool fp8 = d.w_dtype == MOE_E4M3, mx = d.w_dtype == MOE_MXFP4;
   const size_t hs = act_size(d.act_dtype), os = out_size(d.out_dtype);
   L.err = take(4);  // MOE_WS_ERROR_OFFSET: first word of the workspace
   L.logits = take(T * d.E * 4);
@@ -118,13 +122,17 @@ Layout layout(const moe_dims& d) {
   L.tp_b = take((nl + 1) * 4);
   L.perm_token = take(tk * 4);
   L.inv_pos = take(tk * 4);
-  L.xq = take(fp8 ? T * d.D : 0);
+  // 4-bit: records of x (moe_grouped_ffn may be given T * top_k grouped rows) and of h
+  L.xq = take(fp8 ? T * d.D : mx ? tk * mx_row_bytes(d.D) : 0);
   L.sx = take(fp8 ? T * 4 : 0);
-  L.h = take(tk * d.I * hs);
+  L.h = take(mx ? tk * mx_row_bytes(d.I) : tk * d.I * hs);
   L.h_sh = take(T * d.I_shared * hs);
   L.hq = take(fp8 ? tk * d.I : 0);
   L.sh = take(fp8 ? tk * 4 : 0);
   L.out_rows = take(tk * d.D * os);
+  // h of the few-token layer: fp32, or two bf16 planes
+  L.few_h = take(is_few(d) ? tk * d.I * 4 : 0);
+  L.few_h_sh = take(is_few(d) ? T * d.I_shared * 4 : 0);
   L.total = off;
   return L;
 }
@@ -210,6 +218,42 @@ int route_tokens(const moe_dims& d, const void* x, const void* w_router, float* 
   return hip_status(launch_route(nullptr, 1, logits, bias, d.T, d.E, d.top_k, d.renormalize, packed, s));
 }
 
+// M-tile height of the 4-bit grouped GEMMs, by the average routed rows per expert: one tile of
+// 16 or 32 rows reads each weight byte once; above, 128-row tiles reuse it.
+int mx_bm(const moe_dims& d) {
+  const double avg = static_cast<double>(d.T) * d.top_k / d.E;
+  return avg <= 16.0 ? 16 : avg <= 32.0 ? 32 : 128;
+}
+
+// M-tile height of the routed grouped GEMMs of these dims.
+int routed_bm(const moe_dims& d, bool gathered) {
+  return d.w_dtype == MOE_MXFP4 ? mx_bm(d) : gemm_bm(expert_shape(d, gathered));
+}
+
+// The routed groups on 4-bit weights: rows of x (or grouped rows) to records, gate/up to
+// records of h, down to out_rows.
+int mx_experts(const moe_dims& d, void* ws, const Layout& L, const void* a_rows, const int32_t* perm,
+               const int32_t* offsets, const void* w_gate, const void* w_up, const void* w_down, void* out_rows,
+               hipEvent_t ev_gate_up, hipEvent_t ev_down, hipStream_t s) {
+  const int bm = mx_bm(d);
+  const int tk = d.T * d.top_k;
+  void* xm = at<void>(ws, L.xq);
+  void* hm = at<void>(ws, L.h);
+  MOE_TRY(launch_mx_rows(a_rows, perm ? d.T : tk, perm ? nullptr : offsets + d.n_local, d.D, xm, s));
+  MxGemm p{};
+  p.a = xm; p.perm = perm; p.offsets = offsets; p.tile_prefix = at<int32_t>(ws, L.tp_a); p.n_groups = d.n_local;
+  p.w0 = w_gate; p.w1 = w_up; p.w_stride = d.I / 16 * mx_fragment_bytes(d.D);
+  p.out = hm; p.N = d.I; p.K = d.D;
+  MOE_TRY(launch_mx_gemm(true, EL_BF16, bm, p, routed_tile_bound(tk, d.n_local, bm, d.I, mx_gemm_bn(true)), s));
+  if (ev_gate_up) MOE_TRY(hipEventRecord(ev_gate_up, s));
+  p.a = hm; p.perm = nullptr; p.tile_prefix = at<int32_t>(ws, L.tp_b);
+  p.w0 = w_down; p.w1 = nullptr; p.w_stride = d.D / 16 * mx_fragment_bytes(d.I);
+  p.out = out_rows; p.N = d.D; p.K = d.I;
+  MOE_TRY(launch_mx_gemm(false, d.out_dtype, bm, p, routed_tile_bound(tk, d.n_local, bm, d.D, mx_gemm_bn(false)), s));
+  if (ev_down) MOE_TRY(hipEventRecord(ev_down, s));
+  return MOE_OK;
+}
+
 // gate/up -> h (+ quantise) -> down for the routed groups, then the optional shared
 // expert in launches of its own, whose down projection also does the unpermute-combine:
 // y[t] = sum_j w[t][j] * out_rows[inv[t][j]] + shared(x_t).
@@ -221,8 +265,7 @@ int experts_forward(const moe_dims& d, void* ws, const Layout& L, const void* a_
                     bool have_tile_prefix, hipEvent_t ev_gate_up, hipEvent_t ev_down, hipStream_t s) {
   const int shape = expert_shape(d, perm != nullptr);
   const bool packed = d.weight_layout == MOE_LAYOUT_PACKED;
-  const int bm = gemm_bm(shape);
-  const int bn_gu = gemm_bn(true, shape, w_el(d), packed), bn_dn = gemm_bn(false, shape, w_el(d), packed);
+  const int bm = routed_bm(d, perm != nullptr);
   const int tk = d.T * d.top_k;
   const bool fp8 = d.w_dtype == MOE_E4M3;
   int32_t* tp_a = at<int32_t>(ws, L.tp_a);
@@ -235,29 +278,35 @@ int experts_forward(const moe_dims& d, void* ws, const Layout& L, const void* a_
 
   if (!have_tile_prefix) MOE_TRY(launch_tile_prefix(offsets, d.n_local, bm, bm, tp_a, tp_b, s));
 
-  // gate/up with the fused SwiGLU epilogue
-  const GemmProblem g0 = problem(a_rows, perm, a_scale, d.D, offsets, tp_a, d.n_local, 0, w_gate, w_up, s_gate, s_up,
-                                 static_cast<long long>(d.I) * d.D, h, d.I, d.I, d.D);
-  const int tiles_gu = routed_tile_bound(tk, d.n_local, bm, d.I, bn_gu);
-  MOE_TRY(launch_gemm(w_el(d), hel, true, shape, packed, g0, tiles_gu, s));
-  if (ev_gate_up) MOE_TRY(hipEventRecord(ev_gate_up, s));
+  if (d.w_dtype == MOE_MXFP4) {
+    const int st = mx_experts(d, ws, L, a_rows, perm, offsets, w_gate, w_up, w_down, out_rows, ev_gate_up, ev_down, s);
+    if (st != MOE_OK) return st;
+  } else {
+    const int bn_gu = gemm_bn(true, shape, w_el(d), packed), bn_dn = gemm_bn(false, shape, w_el(d), packed);
+    // gate/up with the fused SwiGLU epilogue
+    const GemmProblem g0 = problem(a_rows, perm, a_scale, d.D, offsets, tp_a, d.n_local, 0, w_gate, w_up, s_gate, s_up,
+                                   static_cast<long long>(d.I) * d.D, h, d.I, d.I, d.D);
+    const int tiles_gu = routed_tile_bound(tk, d.n_local, bm, d.I, bn_gu);
+    MOE_TRY(launch_gemm(w_el(d), hel, true, shape, packed, g0, tiles_gu, s));
+    if (ev_gate_up) MOE_TRY(hipEventRecord(ev_gate_up, s));
 
-  // down projection of every grouped row
-  const void* h_in = h;
-  const float* h_scale = nullptr;
-  if (fp8) {
-    void* hq = at<void>(ws, L.hq);
-    float* sh = at<float>(ws, L.sh);
-    MOE_TRY(launch_quant_rows(EL_BF16, h, tk, n_rows_dev, d.I, hq, sh, s));
-    h_in = hq;
-    h_scale = sh;
+    // down projection of every grouped row
+    const void* h_in = h;
+    const float* h_scale = nullptr;
+    if (fp8) {
+      void* hq = at<void>(ws, L.hq);
+      float* sh = at<float>(ws, L.sh);
+      MOE_TRY(launch_quant_rows(EL_BF16, h, tk, n_rows_dev, d.I, hq, sh, s));
+      h_in = hq;
+      h_scale = sh;
+    }
+    const GemmProblem d0 = problem(h_in, nullptr, h_scale, d.I, offsets, tp_b, d.n_local, 0, w_down, nullptr, s_down,
+                                   nullptr, static_cast<long long>(d.D) * d.I, out_rows, d.D, d.D, d.I);
+    const int tiles_dn = routed_tile_bound(tk, d.n_local, bm, d.D, bn_dn);
+    MOE_TRY(launch_gemm(w_el(d), d.out_dtype, false, shape, packed, d0, tiles_dn, s));
+    if (ev_down) MOE_TRY(hipEventRecord(ev_down, s));
   }
-  const GemmProblem d0 = problem(h_in, nullptr, h_scale, d.I, offsets, tp_b, d.n_local, 0, w_down, nullptr, s_down,
-                                 nullptr, static_cast<long long>(d.D) * d.I, out_rows, d.D, d.D, d.I);
-  const int tiles_dn = routed_tile_bound(tk, d.n_local, bm, d.D, bn_dn);
   const int oel = d.out_dtype;
-  MOE_TRY(launch_gemm(w_el(d), oel, false, shape, packed, d0, tiles_dn, s));
-  if (ev_down) MOE_TRY(hipEventRecord(ev_down, s));
 
   // The shared expert runs in launches of its own: as a second problem of the routed
   // launches its tiles (all full, and last in the launch order) landed on one XCD.  Where
@@ -282,6 +331,55 @@ int experts_forward(const moe_dims& d, void* ws, const Layout& L, const void* a_
                                 ((d.T + sh_bm - 1) / sh_bm) * ((d.D + bn_d - 1) / bn_d), s));
   }
   return MOE_OK;
+}
+
+// Pointers that a call of the whole layer needs.
+int check_layer_args(const moe_dims& d, const moe_weights* w, const void* x, const int32_t* packed_in, const void* y,
+                     const void* ws) {
+  if (!w || !x || !y || !ws) return MOE_ERR_NULL_ARG;
+  if (!w->w_gate || !w->w_up || !w->w_down) return MOE_ERR_NULL_ARG;
+  if (!packed_in && !w->w_router) return MOE_ERR_NULL_ARG;
+  if (d.w_dtype == MOE_E4M3 && (!w->s_gate || !w->s_up || !w->s_down)) return MOE_ERR_NULL_ARG;
+  if (d.I_shared > 0 && (!w->sh_gate || !w->sh_up || !w->sh_down)) return MOE_ERR_NULL_ARG;
+  return MOE_OK;
+}
+
+// Sizes of 4-bit weight matrices: the kernels address one matrix with 32-bit offsets, and a launch
+// has one workgroup per four (16-row, 512-value) pieces.
+int mx_check(int64_t n_mats, int32_t rows, int32_t cols) {
+  if (n_mats < 0 || rows < 0 || cols < 0) return MOE_ERR_BAD_DIMS;
+  if (rows % 16 || cols % 64) return MOE_ERR_UNSUPPORTED;
+  const int64_t per = static_cast<int64_t>(rows / 16) * mx_groups(cols);
+  if (static_cast<int64_t>(rows) * cols >= (1ll << 32) || (per > 0 && n_mats > (1ll << 32) / per))
+    return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+int check_norm(int32_t T, int32_t D, int32_t act, int32_t y_dtype, const moe_norm* n, bool leave, const void* r_out,
+               const void* x_next) {
+  if (!n) return MOE_ERR_NULL_ARG;
+  if (T < 0 || D < 1 || n->gate_kind < MOE_GATE_NONE || n->gate_kind > MOE_GATE_FULL || !(n->eps >= 0.0f))
+    return MOE_ERR_BAD_DIMS;
+  if (D > kNormMaxD || (act != MOE_F32 && act != MOE_BF16)) return MOE_ERR_UNSUPPORTED;
+  if (leave && y_dtype != MOE_F32 && !(y_dtype == MOE_BF16 && act == MOE_BF16)) return MOE_ERR_UNSUPPORTED;
+  if ((n->gate == nullptr) != (n->gate_kind == MOE_GATE_NONE)) return MOE_ERR_NULL_ARG;
+  if ((r_out != nullptr) != leave || (x_next == nullptr) != (n->w_next == nullptr)) return MOE_ERR_NULL_ARG;
+  if (!leave && !x_next) return MOE_ERR_NULL_ARG;
+  return MOE_OK;
+}
+
+// Workspace of a block: the layer's, then its input and output.
+struct BlockLayout {
+  size_t y, x, total;
+};
+
+BlockLayout block_layout(const moe_dims& d) {
+  const size_t v = static_cast<size_t>(d.T) * d.D;
+  BlockLayout B{};
+  B.y = layout(d).total;
+  B.x = B.y + align_up(v * out_size(d.out_dtype));
+  B.total = B.x + align_up(v * act_size(d.act_dtype));
+  return B;
 }
 
 // Static scratch of moe_layer_forward_noalloc.  In host code `scratch` names a host-side
@@ -358,7 +456,7 @@ int moe_permute(const moe_dims* dims, const int32_t* packed, int32_t* counts, in
   if (ws_bytes < L.total) return MOE_ERR_WORKSPACE;
   hipStream_t s = static_cast<hipStream_t>(stream);
   if (d.T == 0) return MOE_OK;
-  const int bm = gemm_bm(expert_shape(d, true));
+  const int bm = routed_bm(d, true);
   // e4m3: x is quantised per token by the grouping launches, as in the layer call
   const bool quant = x && fp8;
   MOE_TRY(launch_permute(packed, d.T, d.top_k, d.E, d.expert_begin, d.n_local, at<int32_t>(ws, L.hist),
@@ -414,12 +512,9 @@ int moe_layer_forward(const moe_dims* dims, const moe_weights* w, const void* x,
   int st = check_dims(dims);
   if (st != MOE_OK) return st;
   const moe_dims& d = *dims;
-  if (!w || !x || !y || !ws) return MOE_ERR_NULL_ARG;
-  if (!w->w_gate || !w->w_up || !w->w_down) return MOE_ERR_NULL_ARG;
-  if (!packed_in && !w->w_router) return MOE_ERR_NULL_ARG;
+  st = check_layer_args(d, w, x, packed_in, y, ws);
+  if (st != MOE_OK) return st;
   const bool fp8 = d.w_dtype == MOE_E4M3;
-  if (fp8 && (!w->s_gate || !w->s_up || !w->s_down)) return MOE_ERR_NULL_ARG;
-  if (d.I_shared > 0 && (!w->sh_gate || !w->sh_up || !w->sh_down)) return MOE_ERR_NULL_ARG;
   const Layout L = layout(d);
   if (ws_bytes < L.total) return MOE_ERR_WORKSPACE;
   if (d.T == 0) return MOE_OK;
@@ -449,7 +544,7 @@ int moe_layer_forward(const moe_dims* dims, const moe_weights* w, const void* x,
   int32_t* offsets = at<int32_t>(ws, L.offsets);
   int32_t* perm = at<int32_t>(ws, L.perm_token);
   int32_t* inv = at<int32_t>(ws, L.inv_pos);
-  const int bm = gemm_bm(expert_shape(d, true));
+  const int bm = routed_bm(d, true);
   // with e4m3 experts the grouping launches also quantise x per token
   MOE_TRY(launch_permute(packed, d.T, d.top_k, d.E, d.expert_begin, d.n_local, at<int32_t>(ws, L.hist),
                          at<int32_t>(ws, L.base), at<int32_t>(ws, L.rank), at<int32_t>(ws, L.bad), counts, offsets,
@@ -494,8 +589,111 @@ int moe_layer_forward_noalloc(const moe_dims* dims, const moe_weights* w, const 
                                    hipMemcpyDeviceToDevice, static_cast<hipStream_t>(stream)));
 }
 
+size_t moe_mx_weight_bytes(int64_t n_mats, int32_t rows, int32_t cols) {
+  if (mx_check(n_mats, rows, cols) != MOE_OK) return 0;
+  return static_cast<size_t>(n_mats) * (rows / 16) * mx_fragment_bytes(cols);
+}
+
+int moe_mx_pack_weights(int32_t src_dtype, int64_t n_mats, int32_t rows, int32_t cols, const void* src, void* dst,
+                        void* stream) {
+  if (src_dtype != MOE_F32 && src_dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED;
+  const int st = mx_check(n_mats, rows, cols);
+  if (st != MOE_OK) return st;
+  if (n_mats == 0 || rows == 0 || cols == 0) return MOE_OK;
+  if (!src || !dst) return MOE_ERR_NULL_ARG;
+  return hip_status(launch_mx_pack(src_dtype, src, n_mats, rows, cols, dst, static_cast<hipStream_t>(stream)));
+}
+
+int moe_mx_unpack_weights(int32_t dst_dtype, int64_t n_mats, int32_t rows, int32_t cols, const void* src, void* dst,
+                          void* stream) {
+  if (dst_dtype != MOE_F32 && dst_dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED;
+  const int st = mx_check(n_mats, rows, cols);
+  if (st != MOE_OK) return st;
+  if (n_mats == 0 || rows == 0 || cols == 0) return MOE_OK;
+  if (!src || !dst) return MOE_ERR_NULL_ARG;
+  return hip_status(launch_mx_unpack(dst_dtype, src, n_mats, rows, cols, dst, static_cast<hipStream_t>(stream)));
+}
+
+int moe_layer_forward_few(const moe_dims* dims, const moe_weights* w, const void* x, const int32_t* packed_in,
+                          const float* logit_bias, void* y, float* logits_out, int32_t* packed_out, void* ws,
+                          size_t ws_bytes, void* stream) {
+  int st = check_dims(dims);
+  if (st != MOE_OK) return st;
+  const moe_dims& d = *dims;
+  if (!is_few(d)) return MOE_ERR_UNSUPPORTED;
+  st = check_layer_args(d, w, x, packed_in, y, ws);
+  if (st != MOE_OK) return st;
+  const Layout L = layout(d);
+  if (ws_bytes < L.total) return MOE_ERR_WORKSPACE;
+  if (d.T == 0) return MOE_OK;
+  const bool mx = d.w_dtype == MOE_MXFP4;
+  const int64_t es = d.w_dtype == MOE_F32 ? 4 : d.w_dtype == MOE_BF16 ? 2 : 1;
+  FewLayer p{};
+  p.x = x; p.w_router = w->w_router; p.bias = logit_bias; p.packed_in = packed_in;
+  p.logits = logits_out ? logits_out : at<float>(ws, L.logits);
+  p.packed = at<int32_t>(ws, L.packed); p.packed_out = packed_out; p.err = at<int32_t>(ws, L.err);
+  p.w_gate = w->w_gate; p.w_up = w->w_up; p.w_down = w->w_down;
+  p.s_gate = w->s_gate; p.s_up = w->s_up; p.s_down = w->s_down;
+  p.sh_gate = w->sh_gate; p.sh_up = w->sh_up; p.sh_down = w->sh_down;
+  p.gu_stride = mx ? d.I / 16 * mx_fragment_bytes(d.D) : static_cast<int64_t>(d.I) * d.D * es;
+  p.dn_stride = mx ? d.D / 16 * mx_fragment_bytes(d.I) : static_cast<int64_t>(d.I) * d.D * es;
+  p.h = at<void>(ws, L.few_h); p.h_sh = at<void>(ws, L.few_h_sh); p.y = y;
+  p.T = d.T; p.D = d.D; p.E = d.E; p.k = d.top_k; p.I = d.I; p.I_shared = d.I_shared; p.e_begin = d.expert_begin;
+  p.n_local = d.n_local; p.renormalize = d.renormalize; p.out_el = d.out_dtype;
+  return hip_status(launch_few_layer(d.w_dtype, d.weight_layout == MOE_LAYOUT_PACKED, p,
+                                     static_cast<hipStream_t>(stream)));
+}
+
+int moe_block_norm(int32_t T, int32_t D, int32_t act_dtype, int32_t y_dtype, const moe_norm* n, const void* y,
+                   const void* r, void* r_out, void* x_next, void* stream) {
+  const int st = check_norm(T, D, act_dtype, y_dtype, n, y != nullptr, r_out, x_next);
+  if (st != MOE_OK) return st;
+  if (!r) return MOE_ERR_NULL_ARG;
+  if (T == 0) return MOE_OK;
+  BlockNorm p{};
+  p.y = y; p.r = r; p.w_post = n->w_post; p.gate = n->gate; p.r_out = r_out; p.w_next = n->w_next; p.x_next = x_next;
+  p.T = T; p.D = D; p.gate_kind = n->gate_kind; p.res_scale = n->res_scale; p.eps = n->eps;
+  return hip_status(launch_block_norm(act_dtype, y ? y_dtype : act_dtype, p, static_cast<hipStream_t>(stream)));
+}
+
+size_t moe_block_workspace_bytes(const moe_dims* dims) {
+  if (check_dims(dims) != MOE_OK) return 0;
+  return block_layout(*dims).total;
+}
+
+int moe_block_forward(const moe_dims* dims, const moe_weights* weights, const void* w_in, const void* x_in,
+                      const float* logit_bias, const moe_norm* n, const void* r, void* r_out, void* x_next, void* ws,
+                      size_t ws_bytes, void* stream) {
+  int st = check_dims(dims);
+  if (st != MOE_OK) return st;
+  const moe_dims& d = *dims;
+  if (!r || !ws || (w_in == nullptr) == (x_in == nullptr)) return MOE_ERR_NULL_ARG;
+  st = check_norm(d.T, d.D, d.act_dtype, d.out_dtype, n, true, r_out, x_next);
+  if (st != MOE_OK) return st;
+  const BlockLayout B = block_layout(d);
+  void* y = at<void>(ws, B.y);
+  st = check_layer_args(d, weights, r, nullptr, y, ws);
+  if (st != MOE_OK) return st;
+  if (ws_bytes < B.total) return MOE_ERR_WORKSPACE;
+  if (d.T == 0) return MOE_OK;
+  const void* x = x_in;
+  if (w_in) {
+    moe_norm enter{};
+    enter.w_next = w_in;
+    enter.eps = n->eps;
+    x = at<void>(ws, B.x);
+    st = moe_block_norm(d.T, d.D, d.act_dtype, d.act_dtype, &enter, nullptr, r, nullptr, at<void>(ws, B.x), stream);
+    if (st != MOE_OK) return st;
+  }
+  st = is_few(d) ? moe_layer_forward_few(dims, weights, x, nullptr, logit_bias, y, nullptr, nullptr, ws, B.y, stream)
+                 : moe_layer_forward(dims, weights, x, nullptr, logit_bias, y, nullptr, nullptr, ws, B.y, nullptr,
+                                     stream);
+  if (st != MOE_OK) return st;
+  return moe_block_norm(d.T, d.D, d.act_dtype, d.out_dtype, n, y, r, r_out, x_next, stream);
+}
+
 size_t moe_audit_workspace_bytes(const moe_dims* dims, int32_t n_sample) {
-  if (check_dims(dims) != MOE_OK || n_sample < 1 || n_sample > kAuditMaxSamples) return 0;
+  if (check_dims(dims) != MOE_OK || dims->w_dtype == MOE_MXFP4 || n_sample < 1 || n_sample > kAuditMaxSamples) return 0;
   return audit_workspace_bytes(n_sample, dims->top_k, dims->D, std::max(dims->I, dims->I_shared));
 }
 
@@ -506,6 +704,7 @@ int moe_audit(const moe_dims* dims, const moe_weights* w, const void* x, const i
   if (st != MOE_OK) return st;
   const moe_dims& d = *dims;
   if (n_sample < 1 || n_sample > kAuditMaxSamples) return MOE_ERR_BAD_DIMS;
+  if (d.w_dtype == MOE_MXFP4) return MOE_ERR_UNSUPPORTED;
   if (d.D > kAuditMaxWidth || d.I > kAuditMaxWidth || d.I_shared > kAuditMaxWidth) return MOE_ERR_UNSUPPORTED;
   if (!w || !x || !packed || !y || !sample || !result || !ws || !w->w_gate || !w->w_up || !w->w_down)
     return MOE_ERR_NULL_ARG;

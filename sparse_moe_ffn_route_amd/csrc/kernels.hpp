@@ -101,4 +101,76 @@ hipError_t launch_pack(const void* src, void* dst, int64_t n_mats, int rows, int
 hipError_t launch_combine(int out_el, const void* out_rows, const int32_t* packed, const int32_t* inv_pos,
                           const void* shared_out, int T, int D, int k, void* y, hipStream_t stream);
 
+// Microscaled 4-bit storage (formats in mx.hpp).  Weights [n_mats][rows][cols] of src_el
+// (EL_F32 / EL_BF16) to the packed image and back; bf16 rows [rows][cols] (n_rows_dev: rows in
+// use, or NULL for all) to activation records.
+hipError_t launch_mx_pack(int src_el, const void* src, int64_t n_mats, int rows, int cols, void* dst,
+                          hipStream_t stream);
+hipError_t launch_mx_unpack(int dst_el, const void* src, int64_t n_mats, int rows, int cols, void* dst,
+                            hipStream_t stream);
+hipError_t launch_mx_rows(const void* src, int rows, const int32_t* n_rows_dev, int cols, void* dst,
+                          hipStream_t stream);
+
+// Grouped GEMM on 4-bit rows and weights.  Rows of group g are [offsets[g], offsets[g + 1]); row r
+// reads record row perm[r] (or r).  tile_prefix: M-tile prefix for height bm (16, 32 or 128).
+struct MxGemm {
+  const void* a;               // records of width K
+  const int32_t* perm;
+  const int32_t* offsets;      // [n_groups + 1]
+  const int32_t* tile_prefix;  // [n_groups + 1]
+  int n_groups;
+  const void* w0;              // gate (SwiGLU) or the only weights: images of [N][K]
+  const void* w1;              // up (SwiGLU)
+  int64_t w_stride;            // bytes between consecutive groups' images
+  void* out;                   // SwiGLU: records of width N; else [rows][N] of the output type
+  int N, K;
+};
+int mx_gemm_bn(bool swiglu);  // channels per workgroup
+hipError_t launch_mx_gemm(bool swiglu, int out_el, int bm, const MxGemm& p, int max_tiles, hipStream_t stream);
+
+// The whole layer for up to kFewMaxT tokens.  w_el: EL_F32, EL_BF16, EL_E4M3 or 3 (4-bit images,
+// MOE_MXFP4); x, router and shared weights are F32 with F32 experts, else BF16.
+constexpr int kFewMaxT = 16;
+struct FewLayer {
+  const void* x;             // [T][D]
+  const void* w_router;      // [E][D]
+  const float* bias;         // [E] or NULL
+  const int32_t* packed_in;  // given routing, or NULL
+  float* logits;             // [T][E], written unless packed_in
+  int32_t* packed;           // [T][2][k] scratch, written
+  int32_t* packed_out;       // copy, or NULL
+  int32_t* err;              // ids outside [0, E)
+  const void* w_gate;
+  const void* w_up;
+  const void* w_down;
+  const float* s_gate;
+  const float* s_up;
+  const float* s_down;
+  const void* sh_gate;
+  const void* sh_up;
+  const void* sh_down;
+  int64_t gu_stride, dn_stride;  // bytes between experts
+  void* h;                   // [T][k][I] fp32, or two bf16 planes of it
+  void* h_sh;                // [T][I_shared] likewise
+  void* y;                   // [T][D] of out_el
+  int T, D, E, k, I, I_shared, e_begin, n_local, renormalize, out_el;
+};
+hipError_t launch_few_layer(int w_el, bool packed, const FewLayer& p, hipStream_t stream);
+
+// Post-norm, gate, residual scale and add, next pre-norm (see block_norm.hip).
+constexpr int kNormMaxD = 16384;
+enum : int { kGateNone = 0, kGateToken = 1, kGateChannel = 2, kGateFull = 3 };  // as enum moe_gate
+struct BlockNorm {
+  const void* y;       // [T][D] or NULL
+  const void* r;       // [T][D]
+  const void* w_post;  // [D] or NULL
+  const void* gate;    // by gate_kind: - / [T] fp32 / [D] / [T][D]
+  void* r_out;         // [T][D] (with y)
+  const void* w_next;  // [D] or NULL
+  void* x_next;        // [T][D] (with w_next)
+  int T, D, gate_kind;
+  float res_scale, eps;
+};
+hipError_t launch_block_norm(int el, int y_el, const BlockNorm& p, hipStream_t stream);
+
 }  // namespace moe

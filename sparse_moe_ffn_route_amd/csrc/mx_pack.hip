@@ -1,0 +1,194 @@
+// Microscaled 4-bit storage: weights to the packed image and back, activation rows to
+// records (formats in mx.hpp).
+//
+// All three are streams: pack reads 2 (bf16) or 4 (fp32) bytes and writes 17/32 byte per
+// value, unpack the reverse.
+#include <type_traits>
+
+#include "common.hpp"
+#include "kernels.hpp"
+#include "mx.hpp"
+
+namespace moe {
+
+namespace {
+
+typedef uint32_t u32;
+
+// 8 consecutive values as float.
+template <int EL>
+__device__ __forceinline__ void load8(const void* base, size_t idx, float (&v)[8]) {
+  if constexpr (EL == EL_F32) {
+    const u32x4* p = reinterpret_cast<const u32x4*>(static_cast<const float*>(base) + idx);
+    const u32x4 a = p[0], b = p[1];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[i] = __uint_as_float(a[i]);
+      v[4 + i] = __uint_as_float(b[i]);
+    }
+  } else {
+    const u32x4 a = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(base) + idx);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = bf16_bits_to_f32(a[i] & 0xFFFFu);
+      v[2 * i + 1] = __uint_as_float(a[i] & 0xFFFF0000u);
+    }
+  }
+}
+
+// One wave per (matrix, 16 rows, group): lane l encodes one block per step, so the codes go
+// out as whole 1 KB runs and the scales as one 256-byte store.
+template <int EL>
+__global__ __launch_bounds__(256) void mx_pack_kernel(const void* __restrict__ src, uint8_t* __restrict__ dst,
+                                                      int64_t units, int frags, int cols) {
+  const int64_t u = static_cast<int64_t>(blockIdx.x) * 4 + threadIdx.x / kWave;
+  if (u >= units) return;
+  const int lane = threadIdx.x % kWave;
+  const int groups = mx_groups(cols);
+  const int g = static_cast<int>(u % groups);
+  const int64_t fr = u / groups;  // fragment over all matrices
+  const int steps = min(4, mx_steps(cols) - g * 4);
+  uint8_t* out = dst + fr * mx_fragment_bytes(cols) + static_cast<int64_t>(g) * kMxGroupBytes;
+  const size_t row = static_cast<size_t>(fr) * 16 + (lane & 15);
+  u32 scales = 0x7F7F7F7Fu;
+  for (int s = 0; s < steps; ++s) {
+    const int k0 = g * kMxGroup + s * kMxStep + (lane >> 4) * kMxBlock;
+    u32x4 codes = {0u, 0u, 0u, 0u};
+    if (k0 < cols) {
+      float v[4][8];
+      u32 m = 0;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        load8<EL>(src, row * cols + k0 + c * 8, v[c]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = max(m, mx_abs_bits(v[c][i]));
+      }
+      const u32 b = mx_scale_byte(m);
+      scales = (scales & ~(0xFFu << (8 * s))) | (b << (8 * s));
+      if (b != 255u) {
+        const float inv = mx_inverse_scale(b);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) codes[c] = mx_codes8(v[c], inv);
+      }
+    }
+    *reinterpret_cast<u32x4*>(out + s * kMxRun + lane * 16) = codes;
+  }
+  *reinterpret_cast<u32*>(out + steps * kMxRun + lane * 4) = scales;
+}
+
+// The value of a code (nibble i of w) times the block's scale; scale byte 255 is NaN.
+__device__ __forceinline__ float mx_value(u32 w, int i, float scale) {
+  const u32 c = (w >> (4 * i)) & 15u, m = c & 7u;
+  const float a = m < 2 ? 0.5f * m : static_cast<float>((2u | (m & 1u)) << (m >> 1)) * 0.25f;
+  const float v = a * scale;
+  return c & 8u ? -v : v;
+}
+
+template <int EL>
+__global__ __launch_bounds__(256) void mx_unpack_kernel(const uint8_t* __restrict__ src, void* __restrict__ dst,
+                                                        int64_t units, int frags, int cols) {
+  const int64_t u = static_cast<int64_t>(blockIdx.x) * 4 + threadIdx.x / kWave;
+  if (u >= units) return;
+  const int lane = threadIdx.x % kWave;
+  const int groups = mx_groups(cols);
+  const int g = static_cast<int>(u % groups);
+  const int64_t fr = u / groups;
+  const int steps = min(4, mx_steps(cols) - g * 4);
+  const uint8_t* in = src + fr * mx_fragment_bytes(cols) + static_cast<int64_t>(g) * kMxGroupBytes;
+  const size_t row = static_cast<size_t>(fr) * 16 + (lane & 15);
+  const u32 scales = *reinterpret_cast<const u32*>(in + steps * kMxRun + lane * 4);
+  for (int s = 0; s < steps; ++s) {
+    const int k0 = g * kMxGroup + s * kMxStep + (lane >> 4) * kMxBlock;
+    if (k0 >= cols) continue;
+    const u32x4 codes = *reinterpret_cast<const u32x4*>(in + s * kMxRun + lane * 16);
+    const u32 b = (scales >> (8 * s)) & 255u;
+    const float scale = b == 255u ? __uint_as_float(0x7FC00000u) : ldexpf(1.0f, static_cast<int>(b) - 127);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = mx_value(codes[c], i, scale);
+      const size_t idx = row * cols + k0 + c * 8;
+      if constexpr (EL == EL_F32) {
+        float4* p = reinterpret_cast<float4*>(static_cast<float*>(dst) + idx);
+        p[0] = make_float4(v[0], v[1], v[2], v[3]);
+        p[1] = make_float4(v[4], v[5], v[6], v[7]);
+      } else {
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(dst) + idx) =
+            make_uint4(bf16x2_bits(v[0], v[1]), bf16x2_bits(v[2], v[3]), bf16x2_bits(v[4], v[5]),
+                       bf16x2_bits(v[6], v[7]));
+      }
+    }
+  }
+}
+
+// bf16 rows -> records.  Four lanes share a block (8 values each): loads of 16 bytes and
+// stores of 4 bytes per lane are contiguous over the wave, one wave per record.
+__global__ __launch_bounds__(256) void mx_rows_kernel(const uint16_t* __restrict__ src, int rows,
+                                                      const int32_t* __restrict__ n_rows_dev, int cols,
+                                                      uint8_t* __restrict__ dst) {
+  const int groups = mx_groups(cols);
+  const int64_t u = static_cast<int64_t>(blockIdx.x) * 4 + threadIdx.x / kWave;
+  const int64_t row = u / groups;
+  const int g = static_cast<int>(u - row * groups);
+  const int n = n_rows_dev ? min(rows, ld_scalar(n_rows_dev)) : rows;
+  if (row >= n) return;
+  const int lane = threadIdx.x % kWave;
+  const int k0 = g * kMxGroup + lane * 8;
+  float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  if (k0 < cols) load8<EL_BF16>(src, static_cast<size_t>(row) * cols + k0, v);
+  u32 m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, mx_abs_bits(v[i]));
+  m = max(m, static_cast<u32>(__shfl_xor(static_cast<int>(m), 1, kWave)));
+  m = max(m, static_cast<u32>(__shfl_xor(static_cast<int>(m), 2, kWave)));
+  const u32 b = mx_scale_byte(m);
+  const u32 codes = b == 255u ? 0u : mx_codes8(v, mx_inverse_scale(b));
+  uint8_t* out = dst + row * mx_row_bytes(cols) + static_cast<int64_t>(g) * kMxRecord;
+  *reinterpret_cast<u32*>(out + lane * 4) = codes;
+  const int blk = lane >> 2;  // block of the group: step blk / 4, lane group blk % 4
+  if ((lane & 3) == 0) out[256 + (blk & 3) * 4 + (blk >> 2)] = static_cast<uint8_t>(b);
+}
+
+}  // namespace
+
+hipError_t launch_mx_pack(int src_el, const void* src, int64_t n_mats, int rows, int cols, void* dst,
+                          hipStream_t stream) {
+  const int frags = rows / 16;
+  const int64_t units = n_mats * frags * mx_groups(cols);
+  if (units == 0) return hipSuccess;
+  const dim3 grid(static_cast<uint32_t>((units + 3) / 4));
+  if (src_el == EL_F32)
+    hipLaunchKernelGGL((mx_pack_kernel<EL_F32>), grid, dim3(256), 0, stream, src, static_cast<uint8_t*>(dst), units,
+                       frags, cols);
+  else
+    hipLaunchKernelGGL((mx_pack_kernel<EL_BF16>), grid, dim3(256), 0, stream, src, static_cast<uint8_t*>(dst), units,
+                       frags, cols);
+  return hipGetLastError();
+}
+
+hipError_t launch_mx_unpack(int dst_el, const void* src, int64_t n_mats, int rows, int cols, void* dst,
+                            hipStream_t stream) {
+  const int frags = rows / 16;
+  const int64_t units = n_mats * frags * mx_groups(cols);
+  if (units == 0) return hipSuccess;
+  const dim3 grid(static_cast<uint32_t>((units + 3) / 4));
+  if (dst_el == EL_F32)
+    hipLaunchKernelGGL((mx_unpack_kernel<EL_F32>), grid, dim3(256), 0, stream, static_cast<const uint8_t*>(src), dst,
+                       units, frags, cols);
+  else
+    hipLaunchKernelGGL((mx_unpack_kernel<EL_BF16>), grid, dim3(256), 0, stream, static_cast<const uint8_t*>(src), dst,
+                       units, frags, cols);
+  return hipGetLastError();
+}
+
+hipError_t launch_mx_rows(const void* src, int rows, const int32_t* n_rows_dev, int cols, void* dst,
+                          hipStream_t stream) {
+  const int64_t units = static_cast<int64_t>(rows) * mx_groups(cols);
+  if (units == 0) return hipSuccess;
+  hipLaunchKernelGGL(mx_rows_kernel, dim3(static_cast<uint32_t>((units + 3) / 4)), dim3(256), 0, stream,
+                     static_cast<const uint16_t*>(src), rows, n_rows_dev, cols, static_cast<uint8_t*>(dst));
+  return hipGetLastError();
+}
+
+}  // namespace moe

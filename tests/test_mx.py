@@ -1,0 +1,255 @@
+"""Microscaled FP4 weights: the packed images, the grouped experts on them, and the whole layer.
+
+Bars.  Images and unpacked values: bit-exact.  Grouped experts: |out - ref| <= half a step of the output type
+times |ref| (2^-8 bf16, 2^-24 fp32), plus 1e-4 of the row's largest value for the fp32 sums (the bar of the fp32
+layer), plus the slack of values of h that lie on a rounding border (mx_reference.grouped_ffn).
+"""
+
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import mx_reference as mx
+import oracle
+import sparse_moe_ffn_route_amd as moe
+from harness import to_np
+
+
+# ---------------------------------------------------------------------------
+# Host
+# ---------------------------------------------------------------------------
+
+def test_weight_bytes():
+    # one 16-row fragment: whole groups of 512 are 4 KB of codes and 256 bytes of scales
+    assert moe.moe_mx_weight_bytes(1, 16, 512) == 4096 + 256
+    assert moe.moe_mx_weight_bytes(3, 32, 1024) == 3 * 2 * 2 * 4352
+    assert moe.moe_mx_weight_bytes(1, 16, 64) == 1024 + 256
+    assert moe.moe_mx_weight_bytes(1, 16, 704) == 6 * 1024 + 2 * 256
+    assert moe.moe_mx_weight_bytes(0, 16, 64) == 0
+    for bad in ((1, 24, 64), (1, 16, 96), (-1, 16, 64), (1, -16, 64), (1, 65536, 65536)):
+        assert moe.moe_mx_weight_bytes(*bad) == 0
+
+
+def test_pack_and_unpack_argument_checks():
+    lib = moe.library()
+    fake = ctypes.c_void_p(256)
+    for f in (lib.moe_mx_pack_weights, lib.moe_mx_unpack_weights):
+        assert f(moe.E4M3, 1, 16, 64, fake, fake, None) == moe.ERR_UNSUPPORTED
+        assert f(moe.MXFP4, 1, 16, 64, fake, fake, None) == moe.ERR_UNSUPPORTED
+        assert f(moe.BF16, 1, 8, 64, fake, fake, None) == moe.ERR_UNSUPPORTED
+        assert f(moe.BF16, 1, 16, 32, fake, fake, None) == moe.ERR_UNSUPPORTED
+        assert f(moe.BF16, -1, 16, 64, fake, fake, None) == moe.ERR_BAD_DIMS
+        assert f(moe.BF16, 1 << 62, 16, 64, fake, fake, None) == moe.ERR_UNSUPPORTED
+        assert f(moe.BF16, 1, 16, 64, None, fake, None) == moe.ERR_NULL_ARG
+        assert f(moe.BF16, 1, 16, 64, fake, None, None) == moe.ERR_NULL_ARG
+        assert f(moe.BF16, 0, 16, 64, None, None, None) == moe.OK
+    with pytest.raises(ValueError, match="float32 or bfloat16"):
+        moe.moe_mx_pack_weights(torch.zeros(16, 64, dtype=torch.float16))
+    with pytest.raises(ValueError, match="images"):
+        moe.moe_mx_pack_weights(torch.zeros(16, 64), dst=torch.zeros(10, dtype=torch.uint8))
+    with pytest.raises(ValueError, match="images"):
+        moe.moe_mx_unpack_weights(torch.zeros(1281, dtype=torch.uint8), 16, 64)
+
+
+def test_dims_take_mxfp4_with_packed_bf16_only():
+    ok = dict(T=8, D=64, E=8, top_k=2, I=64, act="bf16", w="mxfp4", out="bf16", layout="packed")
+    assert moe.moe_workspace_bytes(moe.make_dims(**ok)) > 0
+    assert moe.moe_workspace_bytes(moe.make_dims(**{**ok, "out": "f32"})) > 0
+    for bad in (dict(layout="rows"), dict(act="f32"), dict(act="f32", out="f32"), dict(D=96)):
+        assert moe.moe_workspace_bytes(moe.make_dims(**{**ok, **bad})) == 0
+    lib = moe.library()
+    d, fake = moe.make_dims(**ok), ctypes.c_void_p(256)
+    w = moe.moe_weights(fake, fake, fake, fake, None, None, None, None, None, None)
+    assert lib.moe_audit_workspace_bytes(ctypes.byref(d), 4) == 0
+    assert lib.moe_audit(ctypes.byref(d), ctypes.byref(w), fake, fake, fake, fake, 4, None, fake, fake, 1 << 30,
+                         None) == moe.ERR_UNSUPPORTED
+
+
+def test_reference_rounding():
+    """The reference itself, on values whose answers are known."""
+    v = np.zeros(64)
+    v[:12] = [6.0, 0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0, -0.25, -0.76, 7.9, 0.1]
+    v[32:34] = [1.0, 0.0625]
+    q = mx.quantise(v)
+    np.testing.assert_array_equal(q[:12], [6.0, 0.0, 1.0, 1.0, 2.0, 2.0, 4.0, 4.0, -0.0, -1.0, 6.0, 0.0])
+    np.testing.assert_array_equal(q[32:34], [1.0, 0.0])   # scale 1/4: 1/16 lies on the tie between 0 and 1/8
+
+
+# ---------------------------------------------------------------------------
+# Images
+# ---------------------------------------------------------------------------
+
+def _source(rng, shape, dtype):
+    v = rng.standard_normal(shape).astype(np.float32)
+    v.reshape(-1, 32)[1::7] *= 2.0 ** rng.integers(-40, 40, (len(v.reshape(-1, 32)[1::7]), 1))
+    v.reshape(-1, 32)[2::11] = 0.0                                   # zero blocks
+    v.reshape(-1, 32)[3::13] = rng.choice([6.0, 0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0, 7.0, -5.0],
+                                          (len(v.reshape(-1, 32)[3::13]), 32))   # ties
+    v.reshape(-1, 32)[4::17] *= 2.0 ** -130                          # subnormal magnitudes
+    return torch.from_numpy(v).to(dtype)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("n,rows,cols", [(1, 16, 64), (2, 48, 512), (3, 32, 704), (1, 16, 1088), (5, 64, 128)])
+def test_pack_weights_image_and_values(n, rows, cols, dtype):
+    src = _source(np.random.default_rng(cols + n), (n, rows, cols), dtype)
+    codes, exps = mx.encode(src.to(torch.float64).numpy())
+    guard = torch.full((n * moe.moe_mx_weight_bytes(1, rows, cols) + 64,), 0xA5, dtype=torch.uint8, device="cuda")
+    moe.moe_mx_pack_weights(src.cuda(), guard)
+    np.testing.assert_array_equal(guard[:-64].cpu().numpy().reshape(n, -1), mx.image(codes, exps))
+    assert (guard[-64:] == 0xA5).all()
+    for out in (torch.bfloat16, torch.float32):
+        got = moe.moe_mx_unpack_weights(guard[:-64], rows, cols, out)
+        # bf16's smallest subnormal is 2^-133: a value below half of it is out of bf16's reach
+        want = mx.decode(codes, exps)
+        if out == torch.bfloat16:
+            want = torch.from_numpy(want).to(torch.float32).to(torch.bfloat16).to(torch.float64).numpy()
+        np.testing.assert_array_equal(to_np(got), want)
+
+
+@pytest.mark.gpu
+def test_pack_weights_non_finite_blocks():
+    """A NaN or an infinity makes its block NaN and no other."""
+    src = torch.randn(1, 16, 128)
+    src[0, 3, 40], src[0, 5, 0], src[0, 7, 127] = float("nan"), float("inf"), float("-inf")
+    got = to_np(moe.moe_mx_unpack_weights(moe.moe_mx_pack_weights(src.cuda()), 16, 128))[0]
+    want = mx.quantise(src[0].numpy())
+    np.testing.assert_array_equal(got, want)
+    assert np.isnan(got[3, 32:64]).all() and np.isnan(got[5, :32]).all() and np.isnan(got[7, 96:]).all()
+    assert np.isnan(got).sum() == 96
+
+
+# ---------------------------------------------------------------------------
+# Grouped experts
+# ---------------------------------------------------------------------------
+
+def _weights(rng, n, D, I):
+    """(bf16 source tensors, images, decoded values) of gate, up, down."""
+    src = [torch.from_numpy((rng.standard_normal(s) / np.sqrt(s[-1])).astype(np.float32)).to(torch.bfloat16)
+           for s in ((n, I, D), (n, I, D), (n, D, I))]
+    img = [moe.moe_mx_pack_weights(s.cuda()) for s in src]
+    val = [mx.quantise(to_np(s)) for s in src]
+    return src, img, val
+
+
+def _check_rows(got, ref, slack, half_step):
+    lim = half_step * np.abs(ref) + 1e-4 * np.abs(ref).max(1, keepdims=True) + slack * (1 + half_step)
+    assert (np.abs(got - ref) <= lim).all(), float((np.abs(got - ref) - lim).max())
+
+
+FFN = [
+    # (rows of each group, D, I, out): heights of 16, 32 and 128 rows come from the average
+    ([1], 64, 64, "bf16"),
+    ([5, 0, 16, 17, 1, 0, 3], 256, 128, "f32"),
+    ([20, 31, 33, 0, 16], 704, 320, "bf16"),
+    ([130, 1, 128, 0, 300, 64, 97], 576, 192, "bf16"),
+    ([260, 40], 1088, 576, "f32"),
+    ([0, 0, 40, 0], 128, 64, "bf16"),
+    ([70], 4224, 64, "bf16"),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("gathered", [True, False])
+@pytest.mark.parametrize("counts,D,I,out", FFN)
+def test_grouped_ffn(counts, D, I, out, gathered):
+    rng = np.random.default_rng(D + I + len(counts))
+    n, N = len(counts), int(sum(counts))
+    _, img, val = _weights(rng, n, D, I)
+    T = N if not gathered else max(1, N // 2)
+    k = 1 if not gathered else -(-N // T)      # T * k bounds the grouped rows
+    k = min(k, n)
+    T = max(T, -(-N // k))
+    x = torch.from_numpy(rng.standard_normal((T, D)).astype(np.float32)).to(torch.bfloat16)
+    perm = rng.integers(0, T, N).astype(np.int32) if gathered else np.arange(N, dtype=np.int32)
+    offsets = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    d = moe.make_dims(T, D, n, k, I, act="bf16", w="mxfp4", out=out, layout="packed")
+    dt = torch.float32 if out == "f32" else torch.bfloat16
+    rows = torch.full((T * k, D), 7.0, dtype=dt, device="cuda")
+    ws = moe.workspace(d)
+    ws.fill_(0xFF)                              # scale bytes left unwritten would be NaN
+    moe.moe_grouped_ffn(d, x.cuda(), None, torch.from_numpy(perm).cuda() if gathered else None,
+                        torch.from_numpy(offsets).cuda(), *img, None, None, None, rows, ws)
+    got = to_np(rows)
+    assert (got[N:] == 7.0).all()               # rows behind the last group
+    ref, slack = mx.grouped_ffn(to_np(x), perm, offsets, *val)
+    _check_rows(got[:N], ref, slack, 2.0 ** -24 if out == "f32" else 2.0 ** -8)
+
+
+@pytest.mark.gpu
+def test_grouped_ffn_keeps_nan_to_its_row_and_expert():
+    """A NaN in a token reaches that token's rows only; a NaN weight block reaches that expert's rows only."""
+    rng = np.random.default_rng(5)
+    counts, D, I = [20, 18, 25], 256, 128
+    src, img, _ = _weights(rng, 3, D, I)
+    bad = src[0].clone()
+    bad[1, 3, 7] = float("nan")
+    img_bad = moe.moe_mx_pack_weights(bad.cuda())
+    T = sum(counts)
+    x = torch.from_numpy(rng.standard_normal((T, D)).astype(np.float32)).to(torch.bfloat16)
+    x_bad = x.clone()
+    x_bad[4, 100] = float("inf")
+    offsets = torch.tensor([0, 20, 38, 63], dtype=torch.int32, device="cuda")
+    d = moe.make_dims(T, D, 3, 1, I, act="bf16", w="mxfp4", out="bf16", layout="packed")
+    ws = moe.workspace(d)
+    outs = []
+    for xx, wg in ((x, img[0]), (x_bad, img[0]), (x, img_bad)):
+        o = torch.empty(T, D, dtype=torch.bfloat16, device="cuda")
+        moe.moe_grouped_ffn(d, xx.cuda(), None, None, offsets, wg, img[1], img[2], None, None, None, o, ws)
+        outs.append(to_np(o))
+    clean, by_x, by_w = outs
+    assert np.isnan(by_x[4]).all()
+    np.testing.assert_array_equal(np.delete(by_x, 4, 0), np.delete(clean, 4, 0))
+    assert np.isnan(by_w[20:38]).all()
+    np.testing.assert_array_equal(by_w[:20], clean[:20])
+    np.testing.assert_array_equal(by_w[38:], clean[38:])
+
+
+# ---------------------------------------------------------------------------
+# The layer
+# ---------------------------------------------------------------------------
+
+LAYERS = [
+    # (T, D, E, k, I, I_shared, begin, n_local, given)
+    (40, 256, 16, 3, 128, 64, 0, 16, False),
+    (300, 448, 24, 4, 192, 128, 0, 24, False),
+    (700, 320, 8, 2, 64, 0, 2, 5, True),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,D,E,k,I,Is,begin,nl,given", LAYERS)
+def test_layer_forward(T, D, E, k, I, Is, begin, nl, given):
+    rng = np.random.default_rng(T)
+    bf = lambda a: torch.from_numpy(a.astype(np.float32)).to(torch.bfloat16)  # noqa: E731
+    x, wr = bf(rng.standard_normal((T, D))), bf(rng.standard_normal((E, D)) / np.sqrt(D))
+    _, img, val = _weights(rng, nl, D, I)
+    sh = [bf(rng.standard_normal(s) / np.sqrt(s[-1])) for s in ((Is, D), (Is, D), (D, Is))] if Is else [None] * 3
+    d = moe.make_dims(T, D, E, k, I, Is, begin, nl, True, "bf16", "mxfp4", "f32", "packed")
+    w = [None if s is None else moe.moe_pack_weights(s.cuda()) for s in sh]
+    wts = moe.make_weights(wr.cuda(), *img, None, None, None, *w)
+    packed_in = None
+    if given:
+        ids = np.argsort(rng.random((T, E)), axis=1)[:, :k].astype(np.int32)
+        packed_in = torch.from_numpy(oracle.pack_routing(ids, rng.random((T, k)).astype(np.float32))).cuda()
+    y = torch.empty(T, D, dtype=torch.float32, device="cuda")
+    blob = torch.empty(T, 2, k, dtype=torch.int32, device="cuda")
+    moe.moe_layer_forward(d, wts, x.cuda(), packed_in, None, y, None, blob, moe.workspace(d))
+    ids, wt = oracle.unpack_routing(blob.cpu().numpy())
+    x64 = to_np(x)
+    ref, lim = np.zeros((T, D)), np.zeros((T, D))
+    for e in range(nl):
+        t, j = np.nonzero(ids == begin + e)
+        rows, slack = mx.grouped_ffn(x64, t, [0, len(t)], *(v[e:e + 1] for v in val))
+        np.add.at(ref, t, wt[t, j][:, None] * rows)
+        np.add.at(lim, t, wt[t, j][:, None] * slack)
+    if Is:
+        g, u, dn = (to_np(s) for s in sh)
+        h = mx.silu(x64 @ g.T) * (x64 @ u.T)
+        ref += h @ dn.T
+        lim += 2.0 ** -8 * (np.abs(h) @ np.abs(dn).T)       # the shared h is stored in bf16
+    lim += 1e-4 * np.abs(ref).max(1, keepdims=True)
+    assert (np.abs(to_np(y) - ref) <= lim).all(), float((np.abs(to_np(y) - ref) - lim).max())
