@@ -353,7 +353,8 @@ int moe_mx_unpack_weights(int32_t dst_dtype, int64_t n_mats, int32_t rows, int32
  *     the exact layer than moe_layer_forward's;
  *   - a token that names one expert in several slots gets it once with the summed weight.
  * The sum over experts is taken in another order than moe_layer_forward's; each call is
- * deterministic.  Returns MOE_ERR_UNSUPPORTED for T > MOE_FEW_MAX_T.
+ * deterministic.  Returns MOE_ERR_UNSUPPORTED for T > MOE_FEW_MAX_T and where T * top_k * I or
+ * T * I_shared reaches 2^28.
  */
 #define MOE_FEW_MAX_T 16
 int moe_layer_forward_few(const moe_dims* dims, const moe_weights* weights, const void* x, const int32_t* packed_in,
@@ -400,8 +401,8 @@ int moe_block_norm(int32_t T, int32_t D, int32_t act_dtype, int32_t y_dtype, con
 /*
  * A whole block around the residual stream r:
  *   x = rms(r) * w_in (rounded to act_dtype), or x_in, the x_next of the block before;
- *   y = the layer of x, routed by it: moe_layer_forward_few up to MOE_FEW_MAX_T tokens, else
- *       moe_layer_forward, rounded to out_dtype;
+ *   y = the layer of x, routed by it: moe_layer_forward_few where it takes the dims (up to
+ *       MOE_FEW_MAX_T tokens), else moe_layer_forward, rounded to out_dtype;
  *   r_out, x_next as moe_block_norm(n, y, r).
  *
  *   w_in, x_in   exactly one of them is given: w_in [D], x_in [T][D], act_dtype

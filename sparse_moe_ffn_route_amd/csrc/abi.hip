@@ -86,10 +86,14 @@ int router_splits(const moe_dims& d) {
 struct Layout {
   size_t err, logits, logits_part, packed, hist, base, rank, bad, counts, offsets, tp_a, tp_b, perm_token, inv_pos;
   size_t cand_key, cand_id, cand_stats;
-  size_t xq, sx, h, h_sh, hq, sh, out_rows, few_h, few_h_sh, total;
+  size_t xq, sx, h, h_sh, hq, sh, out_rows, few_h, few_h_sh, few_list, few_rows, few_xt, total;
 };
 
-bool is_few(const moe_dims& d) { return d.T <= kFewMaxT; }
+// Whether the few-token layer takes these dims: it addresses h (4 bytes per value) with 32-bit offsets.
+bool is_few(const moe_dims& d) {
+  return d.T <= kFewMaxT && static_cast<int64_t>(d.T) * d.top_k * d.I * 4 < (1ll << 30) &&
+         static_cast<int64_t>(d.T) * d.I_shared * 4 < (1ll << 30);
+}
 
 Layout layout(const moe_dims& d) {
   Layout L{};
@@ -130,9 +134,12 @@ Layout layout(const moe_dims& d) {
   L.hq = take(fp8 ? tk * d.I : 0);
   L.sh = take(fp8 ? tk * 4 : 0);
   L.out_rows = take(tk * d.D * os);
-  // h of the few-token layer: fp32, or two bf16 planes
-  L.few_h = take(is_few(d) ? tk * d.I * 4 : 0);
+  // h of the few-token layer: fp32, two bf16 planes, or the terms of the 4-bit kernels
+  L.few_h = take(!is_few(d) ? 0 : mx ? few_mx_h_bytes(d.T, d.top_k, d.I) : tk * d.I * 4);
+  L.few_xt = take(is_few(d) && mx ? few_mx_x_bytes(d.T, d.D) : 0);
   L.few_h_sh = take(is_few(d) ? T * d.I_shared * 4 : 0);
+  L.few_list = take(is_few(d) ? (1 + tk) * 4 : 0);
+  L.few_rows = take(is_few(d) ? tk * 16 * 2 : 0);
   L.total = off;
   return L;
 }
@@ -631,7 +638,9 @@ int moe_layer_forward_few(const moe_dims* dims, const moe_weights* w, const void
   FewLayer p{};
   p.x = x; p.w_router = w->w_router; p.bias = logit_bias; p.packed_in = packed_in;
   p.logits = logits_out ? logits_out : at<float>(ws, L.logits);
-  p.packed = at<int32_t>(ws, L.packed); p.packed_out = packed_out; p.err = at<int32_t>(ws, L.err);
+  p.packed_out = packed_out; p.err = at<int32_t>(ws, L.err);
+  p.count = at<int32_t>(ws, L.few_list); p.list = p.count + 1; p.rows = at<int16_t>(ws, L.few_rows);
+  p.x_terms = at<void>(ws, L.few_xt);
   p.w_gate = w->w_gate; p.w_up = w->w_up; p.w_down = w->w_down;
   p.s_gate = w->s_gate; p.s_up = w->s_up; p.s_down = w->s_down;
   p.sh_gate = w->sh_gate; p.sh_up = w->sh_up; p.sh_down = w->sh_down;

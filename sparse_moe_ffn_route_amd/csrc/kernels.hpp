@@ -137,9 +137,11 @@ struct FewLayer {
   const float* bias;         // [E] or NULL
   const int32_t* packed_in;  // given routing, or NULL
   float* logits;             // [T][E], written unless packed_in
-  int32_t* packed;           // [T][2][k] scratch, written
-  int32_t* packed_out;       // copy, or NULL
+  int32_t* packed_out;       // the routing blob, or NULL
   int32_t* err;              // ids outside [0, E)
+  int32_t* count;            // scratch: local experts with a token,
+  int32_t* list;             // [T * k] which, ascending,
+  int16_t* rows;             // [T * k][16] and each token's row of h (t * k + slot), or -1
   const void* w_gate;
   const void* w_up;
   const void* w_down;
@@ -154,7 +156,11 @@ struct FewLayer {
   void* h_sh;                // [T][I_shared] likewise
   void* y;                   // [T][D] of out_el
   int T, D, E, k, I, I_shared, e_begin, n_local, renormalize, out_el;
+  void* x_terms;             // 4-bit weights: scratch of few_mx_x_bytes(T, D); h: few_mx_h_bytes(T, k, I)
+  int shared_blocks, shared_waves, red_bufs, shared_red_bufs;  // set by the launchers
 };
+size_t few_mx_x_bytes(int T, int D);
+size_t few_mx_h_bytes(int T, int k, int I);
 hipError_t launch_few_layer(int w_el, bool packed, const FewLayer& p, hipStream_t stream);
 
 // Post-norm, gate, residual scale and add, next pre-norm (see block_norm.hip).

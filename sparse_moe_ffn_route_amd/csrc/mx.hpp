@@ -25,6 +25,7 @@
 
 namespace moe {
 
+constexpr int EL_MXFP4 = 3;            // as MOE_MXFP4
 constexpr int kMxBlock = 32;
 constexpr int kMxStep = 128;           // values per MFMA
 constexpr int kMxGroup = 512;          // values per group of four steps
