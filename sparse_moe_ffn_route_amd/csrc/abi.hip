@@ -86,7 +86,7 @@ int router_splits(const moe_dims& d) {
 struct Layout {
   size_t err, logits, logits_part, packed, hist, base, rank, bad, counts, offsets, tp_a, tp_b, perm_token, inv_pos;
   size_t cand_key, cand_id, cand_stats;
-  size_t xq, sx, h, h_sh, hq, sh, out_rows, few_h, few_h_sh, few_list, few_rows, few_xt, total;
+  size_t xq, sx, h, h_sh, hq, sh, out_rows, few_h, few_h_sh, few_entries, few_xt, total;
 };
 
 // Whether the few-token layer takes these dims: it addresses h (4 bytes per value) with 32-bit offsets.
@@ -138,8 +138,7 @@ Layout layout(const moe_dims& d) {
   L.few_h = take(!is_few(d) ? 0 : mx ? few_mx_h_bytes(d.T, d.top_k, d.I) : tk * d.I * 4);
   L.few_xt = take(is_few(d) && mx ? few_mx_x_bytes(d.T, d.D) : 0);
   L.few_h_sh = take(is_few(d) ? T * d.I_shared * 4 : 0);
-  L.few_list = take(is_few(d) ? (1 + tk) * 4 : 0);
-  L.few_rows = take(is_few(d) ? tk * 16 * 2 : 0);
+  L.few_entries = take(is_few(d) ? (1 + tk) * 8 : 0);
   L.total = off;
   return L;
 }
@@ -639,7 +638,7 @@ int moe_layer_forward_few(const moe_dims* dims, const moe_weights* w, const void
   p.x = x; p.w_router = w->w_router; p.bias = logit_bias; p.packed_in = packed_in;
   p.logits = logits_out ? logits_out : at<float>(ws, L.logits);
   p.packed_out = packed_out; p.err = at<int32_t>(ws, L.err);
-  p.count = at<int32_t>(ws, L.few_list); p.list = p.count + 1; p.rows = at<int16_t>(ws, L.few_rows);
+  p.entries = at<int32_t>(ws, L.few_entries); p.entry = at<int2>(ws, L.few_entries) + 1;
   p.x_terms = at<void>(ws, L.few_xt);
   p.w_gate = w->w_gate; p.w_up = w->w_up; p.w_down = w->w_down;
   p.s_gate = w->s_gate; p.s_up = w->s_up; p.s_down = w->s_down;

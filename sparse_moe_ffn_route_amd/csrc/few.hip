@@ -8,14 +8,13 @@
 //                    output channels, which therefore owns their whole sum
 // With given routing the first launch is not needed.
 //
-// All tokens of the call are the columns of one 16-column MFMA tile, so each weight byte of a
-// chosen expert is read once whichever tokens chose it, and there is no grouping step.
-// Columns of tokens that did not choose the expert are computed and dropped by a select
-// (not by a zero weight: an expert's NaN must not reach another expert's token).  Weights
+// The tokens that chose an expert are columns of one 16-column MFMA tile, so each weight byte is
+// read once whichever tokens chose it; the grouping is a few hundred pairs that every
+// workgroup sorts out for itself.  Weights
 // are turned into bf16 in registers (exact for e4m3 codes) and x is
 // never quantised; h, scaled by the routing weight, is carried as a pair of bf16 (value and
-// remainder, 16 significant bits), which keeps the rounding of h out of y.  Up to 8 tokens
-// the remainders are columns 8 to 15 of the same MFMA.  4-bit weights have kernels of their
+// remainder, 16 significant bits), which keeps the rounding of h out of y: the remainders are
+// columns 8 to 15 of the same MFMA.  4-bit weights have kernels of their
 // own (few_mx.hip).
 //
 // The weights' bytes bound all of it, so both large kernels are built as streams: each wave
@@ -34,22 +33,26 @@ using namespace few;
 // logits
 // ---------------------------------------------------------------------------
 
+// 16 waves split the width: at D = 4096 each has all its loads (8 steps of 16 experts) in flight at
+// once, so the launch is a few memory latencies long.
+constexpr int kLogitWaves = 16;
+
 template <int EL>
-__global__ __launch_bounds__(kThreads) void few_logits_kernel(const void* __restrict__ x, const void* __restrict__ wr,
+__global__ __launch_bounds__(kLogitWaves * kWave) void few_logits_kernel(const void* __restrict__ x, const void* __restrict__ wr,
                                                               int T, int D, int E, float* __restrict__ logits) {
-  __shared__ f32x4 red[kWaves][kWave];
+  __shared__ f32x4 red[kLogitWaves][kWave];
   const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
   const int lrow = lane & 15, lgrp = lane >> 4;
   const int e0 = blockIdx.x * 16;
   constexpr int es = EL == EL_F32 ? 4 : 2;
   const int S = D * es / 64;
-  const int s0 = S * wave / kWaves, s1 = S * (wave + 1) / kWaves;
+  const int s0 = S * wave / kLogitWaves, s1 = S * (wave + 1) / kLogitWaves;
   const int e = min(e0 + lrow, E - 1);
   const uint8_t* wp = static_cast<const uint8_t*>(wr) + static_cast<int64_t>(e) * D * es + lgrp * 16;
   const uint8_t* xp = static_cast<const uint8_t*>(x) + static_cast<int64_t>(min(lrow, T - 1)) * D * es + lgrp * 16;
   const u32x4 z = {0u, 0u, 0u, 0u};
   f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-  constexpr int U = 16;
+  constexpr int U = 8;
   for (int s = s0; s < s1; s += U) {
     u32x4 a[U], b[U];
 #pragma unroll
@@ -68,7 +71,7 @@ __global__ __launch_bounds__(kThreads) void few_logits_kernel(const void* __rest
     const int l = threadIdx.x & 63, r = threadIdx.x >> 6;
     float v = 0.f;
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) v += red[w][l][r];
+    for (int w = 0; w < kLogitWaves; ++w) v += red[w][l][r];
     const int t = l & 15, ee = e0 + (l >> 4) * 4 + r;
     if (t < T && ee < E) logits[static_cast<int64_t>(t) * E + ee] = v;
   }
@@ -80,9 +83,9 @@ template <int W, bool PACKED, bool XLDS>
 __global__ __launch_bounds__(kThreads, 2) void few_gate_up_kernel(FewLayer p) {
   constexpr int SH = W == EL_F32 ? EL_F32 : EL_BF16;
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
-  __shared__ Pairs q;
+  __shared__ Route q;
   float* red = reinterpret_cast<float*>(lds);
-  uint8_t* xs = lds + p.red_bufs * 2 * kWaves * p.T * 16 * sizeof(float);
+  uint8_t* xs = lds + p.red_bytes;
   if (static_cast<int>(blockIdx.x) < p.shared_blocks) {
     if constexpr (XLDS) {
       stage_x<SH>(p, xs);
@@ -94,55 +97,30 @@ __global__ __launch_bounds__(kThreads, 2) void few_gate_up_kernel(FewLayer p) {
     return;
   }
   if constexpr (XLDS) stage_x<W>(p, xs);
-  route_call(q, p);
   const int b = blockIdx.x - p.shared_blocks, blocks = gridDim.x - p.shared_blocks;
-  if (b == blocks - 1) write_tables(q, p);
-  const int units = __builtin_amdgcn_readfirstlane(q.count) * (p.I / 16);
+  route_call<16, kDownMembers>(q, lds, p, b == blocks - 1);
+  const int units = __builtin_amdgcn_readfirstlane(q.entries) * (p.I / 16);
   gate_up_units<W, PACKED, XLDS, false>(p, q, xs, red, static_cast<int>(static_cast<int64_t>(units) * b / blocks),
                                         static_cast<int>(static_cast<int64_t>(units) * (b + 1) / blocks));
 }
 
 // The last shared_waves waves take the shared expert, the others the routed ones.
-template <int W, bool PACKED, bool TWO, int OUT>
+template <int W, bool PACKED, int OUT>
 __global__ __launch_bounds__(kThreads, 2) void few_down_kernel(FewLayer p) {
-  constexpr bool F32 = W == EL_F32;
-  constexpr int SH = F32 ? EL_F32 : EL_BF16;
-  __shared__ int16_t rows[kMaxPairs * 16];
+  constexpr int SH = W == EL_F32 ? EL_F32 : EL_BF16;
   __shared__ f32x4 red[kWaves][kWave];
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), lane = threadIdx.x % kWave;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int frag = blockIdx.x, routed = kWaves - p.shared_waves;
-  const int count = ld_scalar(p.count);
-  for (int i = threadIdx.x; i < count * 16; i += kThreads) rows[i] = p.rows[i];
-  __syncthreads();
-  red[wave][lane] = wave < routed ? down_blocks<W, PACKED, TWO, false>(p, rows, count, frag, wave, routed)
-                                  : down_blocks<SH, PACKED, TWO, true>(p, rows, 1, frag, wave - routed, p.shared_waves);
-  __syncthreads();
-  if (static_cast<int>(threadIdx.x) < p.T * 16) {
-    const int tt = threadIdx.x / 16, ch = threadIdx.x % 16;
-    const int l = (ch / 4) * 16 + tt;
-    float v = 0.f;
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) {
-      v += red[w][l][ch % 4];
-      if constexpr (!F32 && !TWO) v += red[w][l + 8][ch % 4];
-    }
-    const int64_t idx = static_cast<int64_t>(tt) * p.D + frag * 16 + ch;
-    if constexpr (OUT == EL_F32) static_cast<float*>(p.y)[idx] = v;
-    else static_cast<uint16_t*>(p.y)[idx] = static_cast<uint16_t>(bf16x2_bits(v, 0.f));
-  }
+  const f32x4 acc = wave < routed
+                        ? down_blocks<W, PACKED, false>(p, ld_scalar(p.entries), frag, wave, routed)
+                        : down_blocks<SH, PACKED, true>(p, (p.T + kDownMembers - 1) / kDownMembers, frag, wave - routed,
+                                                        p.shared_waves);
+  finish_down<OUT>(p, frag, acc, red);
 }
 
 template <int W, bool PACKED, bool XLDS>
 void launch_gate_up(const FewLayer& p, int grid, size_t lds, hipStream_t stream) {
   hipLaunchKernelGGL((few_gate_up_kernel<W, PACKED, XLDS>), dim3(grid), dim3(kThreads), lds, stream, p);
-}
-
-template <int W, bool PACKED, bool TWO>
-void launch_down(const FewLayer& p, hipStream_t stream) {
-  if (p.out_el == EL_F32)
-    hipLaunchKernelGGL((few_down_kernel<W, PACKED, TWO, EL_F32>), dim3(p.D / 16), dim3(kThreads), 0, stream, p);
-  else if constexpr (W != EL_F32)
-    hipLaunchKernelGGL((few_down_kernel<W, PACKED, TWO, EL_BF16>), dim3(p.D / 16), dim3(kThreads), 0, stream, p);
 }
 
 template <int W, bool PACKED>
@@ -153,19 +131,20 @@ hipError_t launch_w(FewLayer p, hipStream_t stream) {
   deal(p, W == EL_E4M3 ? 1.0 : W == EL_BF16 ? 2.0 : 4.0, act_bytes<W>());
   const int64_t most = static_cast<int64_t>(p.T * p.k < p.n_local ? p.T * p.k : p.n_local) * (p.I / 16);
   const int blocks = most < kCus - p.shared_blocks ? static_cast<int>(most) : kCus - p.shared_blocks;
-  // x stays in LDS where it fits beside the reduction buffers (two, or one) and the tables
+  // x stays in LDS where it fits beside the reduction buffers (two, or one) and the routing
   const size_t red = static_cast<size_t>(2) * kWaves * p.T * 16 * sizeof(float);
   const size_t x = static_cast<size_t>(p.T) * (x_row_bytes<W>(p.D) > x_row_bytes<act>(p.D) ? x_row_bytes<W>(p.D)
                                                                                           : x_row_bytes<act>(p.D));
-  const size_t room = kLdsBytes - sizeof(Pairs) - 256;
-  p.red_bufs = 2 * red + x <= room ? 2 : 1;
+  const size_t room = kLdsBytes - sizeof(Route) - 256;
+  p.red_bufs = std::max(2 * red, kRouteScratch) + x <= room ? 2 : 1;
+  p.red_bytes = static_cast<int>(std::max(p.red_bufs * red, kRouteScratch));
   const int grid = p.shared_blocks + blocks;
-  if (p.red_bufs * red + x <= room)
-    launch_gate_up<W, PACKED, true>(p, grid, p.red_bufs * red + x, stream);
-  else
-    launch_gate_up<W, PACKED, false>(p, grid, p.red_bufs * red, stream);
-  if (W != EL_F32 && p.T > 8) launch_down<W, PACKED, true>(p, stream);
-  else launch_down<W, PACKED, false>(p, stream);
+  if (p.red_bytes + x <= room) launch_gate_up<W, PACKED, true>(p, grid, p.red_bytes + x, stream);
+  else launch_gate_up<W, PACKED, false>(p, grid, p.red_bytes, stream);
+  if (p.out_el == EL_F32)
+    hipLaunchKernelGGL((few_down_kernel<W, PACKED, EL_F32>), dim3(p.D / 16), dim3(kThreads), 0, stream, p);
+  else if constexpr (W != EL_F32)
+    hipLaunchKernelGGL((few_down_kernel<W, PACKED, EL_BF16>), dim3(p.D / 16), dim3(kThreads), 0, stream, p);
   return hipGetLastError();
 }
 
@@ -174,9 +153,9 @@ hipError_t launch_w(FewLayer p, hipStream_t stream) {
 void launch_few_logits(int act_el, const FewLayer& p, hipStream_t stream) {
   const dim3 grid((p.E + 15) / 16);
   if (act_el == EL_F32)
-    hipLaunchKernelGGL((few_logits_kernel<EL_F32>), grid, dim3(kThreads), 0, stream, p.x, p.w_router, p.T, p.D, p.E, p.logits);
+    hipLaunchKernelGGL((few_logits_kernel<EL_F32>), grid, dim3(kLogitWaves * kWave), 0, stream, p.x, p.w_router, p.T, p.D, p.E, p.logits);
   else
-    hipLaunchKernelGGL((few_logits_kernel<EL_BF16>), grid, dim3(kThreads), 0, stream, p.x, p.w_router, p.T, p.D, p.E, p.logits);
+    hipLaunchKernelGGL((few_logits_kernel<EL_BF16>), grid, dim3(kLogitWaves * kWave), 0, stream, p.x, p.w_router, p.T, p.D, p.E, p.logits);
 }
 
 hipError_t launch_few_layer(int w_el, bool packed, const FewLayer& p, hipStream_t stream) {

@@ -3,6 +3,8 @@
 
 #include <type_traits>
 
+#include <algorithm>
+
 #include "common.hpp"
 #include "kernels.hpp"
 #include "topk.hpp"
@@ -21,18 +23,17 @@ constexpr int kLdsBytes = 160 * 1024;
 // Weight type W (EL_F32, EL_BF16 or EL_E4M3): a "step" is what 16 bytes per lane cover
 // of 16 rows, EPS values of the reduction dimension, of which lane group g holds the
 // EPS / 4 from g * EPS / 4 on.  NX: 16-byte pieces of the other operand per lane and step.
-// Gate/up blocks are GB steps of both matrices, GN of them in the ring; down blocks DB steps of
-// one matrix with their pieces of h, DN in the ring (DN2 with separate remainders): 2 waves
-// per SIMD have 256 registers each.
+// Gate/up keeps R steps of both matrices in flight; down blocks are DB steps of one matrix with
+// their pieces of h, DN of them in the ring: 2 waves per SIMD have 256 registers each.
 template <int W> struct Wt;
 template <> struct Wt<EL_F32> {
-  static constexpr int EPS = 16, NX = 1, GB = 8, GN = 3, DB = 8, DN = 3, DN2 = 3;
+  static constexpr int EPS = 16, NX = 1, R = 8, DB = 8, DN = 3;
 };
 template <> struct Wt<EL_BF16> {
-  static constexpr int EPS = 32, NX = 1, GB = 8, GN = 3, DB = 8, DN = 3, DN2 = 2;
+  static constexpr int EPS = 32, NX = 1, R = 8, DB = 8, DN = 3;
 };
 template <> struct Wt<EL_E4M3> {
-  static constexpr int EPS = 64, NX = 2, GB = 8, GN = 3, DB = 4, DN = 4, DN2 = 2;
+  static constexpr int EPS = 64, NX = 2, R = 8, DB = 4, DN = 4;
 };
 template <int W> constexpr int act_bytes() { return W == EL_F32 ? 4 : 2; }
 template <int W> __host__ __device__ constexpr int steps_of(int k) { return (k + Wt<W>::EPS - 1) / Wt<W>::EPS; }
@@ -93,16 +94,31 @@ __device__ __forceinline__ void lds_barrier() {
 }
 
 // ---------------------------------------------------------------------------
-// The call's (token, slot) pairs and the experts they name
+// The call's routing: (token, slot) pairs, and the experts they name
 // ---------------------------------------------------------------------------
 
-struct Pairs {
-  int32_t blob[2 * kMaxPairs];  // [T][2][k], as the packed routing blob
-  int32_t first[1024];          // first pair that names each local expert; before that, selection scratch
-  uint16_t list[kMaxPairs];     // local experts with a token, in the order of their first pairs
-  int wave_count[kWaves];
-  int count;
+// An entry is a chosen local expert with up to a kernel's limit of its tokens ("members", by token):
+// x: expert | rank0 << 16, y: token mask of the expert | row << 16.  Its members are the ranks
+// rank0, rank0 + 1, ... of the mask's tokens, their rows of h the rows from `row` on.
+__device__ __forceinline__ int entry_expert(int2 e) { return e.x & 0xFFFF; }
+__device__ __forceinline__ int entry_rank0(int2 e) { return static_cast<int>(static_cast<u32>(e.x) >> 16); }
+__device__ __forceinline__ u32 entry_mask(int2 e) { return static_cast<u32>(e.y) & 0xFFFFu; }
+__device__ __forceinline__ int entry_row(int2 e) { return static_cast<int>(static_cast<u32>(e.y) >> 16); }
+__device__ __forceinline__ int entry_members(int2 e, int limit) {
+  return min(limit, __popc(entry_mask(e)) - entry_rank0(e));
+}
+
+struct Route {
+  int32_t blob[2 * kMaxPairs];      // [T][2][k], as the packed routing blob
+  float weight[kMaxPairs];          // by row of h: routing weight
+  uint8_t token[kMaxPairs];         // and token
+  int2 entry[kMaxPairs];
+  u32 sums[kWaves];
+  int entries;
 };
+// Scratch of route_call, at the start of the dynamic LDS (the reductions' place later): selection
+// candidates, then two words per local expert.
+constexpr size_t kRouteScratch = 2 * 1024 * sizeof(u32);
 
 // Top-k of one token by one wave: the same keys, order and weights as select_topk (topk.hpp), in
 // about a fifth of its time for 512 keys.  The k-th largest of the lanes' own best keys bounds the
@@ -125,7 +141,7 @@ __device__ __forceinline__ void select_few(const float (&key)[PL], int E, int k,
     }
   }
   int rank = 0;
-#pragma unroll
+#pragma unroll 4
   for (int j = 0; j < kWave; ++j) {
     const float ok = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(bk), j));
     const int oi = __builtin_amdgcn_readlane(bi, j);
@@ -189,9 +205,8 @@ __device__ __forceinline__ void select_few(const float (&key)[PL], int E, int k,
 }
 
 template <int PL>
-__device__ __forceinline__ void select_all(Pairs& q, const FewLayer& p) {
+__device__ __forceinline__ void select_all(Route& q, float2* cand, const FewLayer& p) {
   const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
-  float2* cand = reinterpret_cast<float2*>(q.first) + wave * kWave;
   for (int t = wave; t < p.T; t += kWaves) {
     float key[PL];
 #pragma unroll
@@ -206,88 +221,113 @@ __device__ __forceinline__ void select_all(Pairs& q, const FewLayer& p) {
         if (e < p.E) key[i] = key[i] + p.bias[e];
       }
     }
-    select_few(key, p.E, p.k, p.renormalize, cand, q.blob + t * 2 * p.k);
+    select_few(key, p.E, p.k, p.renormalize, cand + wave * kWave, q.blob + t * 2 * p.k);
   }
 }
 
-// The call's routing into q, by all threads: given, or selected from the logits; then the
-// distinct local experts.
-__device__ __forceinline__ void route_call(Pairs& q, const FewLayer& p) {
-  static_assert(sizeof(q.first) >= kWaves * kWave * sizeof(float2), "selection scratch");
+// The call's routing by all threads: given, or selected from the logits; then the experts it names,
+// in the order of the first pairs that do, as entries of up to LIMIT members.  The workgroup
+// with `write` set also writes the down kernel's entries (of up to DOWN_LIMIT), the blob and the
+// error word.
+template <int LIMIT, int DOWN_LIMIT>
+__device__ __forceinline__ void route_call(Route& q, uint8_t* scratch, const FewLayer& p, bool write) {
+  static_assert(kRouteScratch >= kWaves * kWave * sizeof(float2), "selection scratch");
+  static_assert(kThreads >= kMaxPairs, "one pair per thread");
+  int32_t* first = reinterpret_cast<int32_t*>(scratch);  // first pair that names each expert, then its first row
+  u32* mask = reinterpret_cast<u32*>(scratch) + 1024;    // its tokens
   if (p.packed_in) {
     for (int i = threadIdx.x; i < p.T * 2 * p.k; i += kThreads) q.blob[i] = p.packed_in[i];
   } else if (p.E <= 2 * kWave) {
-    select_all<2>(q, p);
+    select_all<2>(q, reinterpret_cast<float2*>(scratch), p);
   } else if (p.E <= 8 * kWave) {
-    select_all<8>(q, p);
+    select_all<8>(q, reinterpret_cast<float2*>(scratch), p);
   } else {
-    select_all<kMaxKeysPerLane>(q, p);
+    select_all<kMaxKeysPerLane>(q, reinterpret_cast<float2*>(scratch), p);
   }
-  wait_vmcnt<0>();  // x is in LDS, too
+  wait_vmcnt<0>();  // loads of x straight into LDS are complete, too
   __syncthreads();
-  // thread i holds pair i (at most 512)
   const int i = threadIdx.x, wave = i / kWave, lane = i % kWave;
-  static_assert(kThreads >= kMaxPairs, "one pair per thread");
+  const int t = i / p.k, j = i - t * p.k, pairs = p.T * p.k;
   int e = -1;
-  if (i < p.T * p.k) {
-    const int id = q.blob[i / p.k * 2 * p.k + i % p.k];
-    if (id >= 0 && id < p.E && id >= p.e_begin && id - p.e_begin < p.n_local) e = id - p.e_begin;
+  float w = 0.f;
+  bool bad = false;
+  if (i < pairs) {
+    const int32_t* ids = q.blob + t * 2 * p.k;
+    const int id = ids[j];
+    bad = id < 0 || id >= p.E;
+    if (!bad && id >= p.e_begin && id - p.e_begin < p.n_local) e = id - p.e_begin;
+    w = __int_as_float(ids[p.k + j]);
+    if (p.packed_in && e >= 0) {
+      // a given token may name an expert again: its first slot takes all the weights
+      for (int n = 0; n < p.k; ++n) {
+        if (n == j || ids[n] != id) continue;
+        if (n < j) e = -1;
+        else w += __int_as_float(ids[p.k + n]);
+      }
+    }
   }
-  if (e >= 0) q.first[e] = 0x7FFFFFFF;
+  if (e >= 0) {
+    first[e] = 0x7FFFFFFF;
+    mask[e] = 0u;
+  }
   __syncthreads();
-  if (e >= 0) atomicMin(&q.first[e], i);
+  if (e >= 0) {
+    atomicMin(&first[e], i);
+    atomicOr(&mask[e], 1u << t);
+  }
   __syncthreads();
-  const bool on = e >= 0 && q.first[e] == i;
-  const uint64_t b = __ballot(on);
-  if (lane == 0) q.wave_count[wave] = __popcll(b);
-  __syncthreads();
-  int n = 0, all = 0;
+  const u32 m = e >= 0 ? mask[e] : 0u;
+  const bool lead = e >= 0 && first[e] == i;
+  const int members = __popc(m);
+  // exclusive sums over the leading pairs before this one: rows, entries, the down kernel's entries
+  u32 mine = lead ? members | ((members + LIMIT - 1) / LIMIT) << 10 | ((members + DOWN_LIMIT - 1) / DOWN_LIMIT) << 20 : 0u;
+  u32 sum = mine;
 #pragma unroll
-  for (int w = 0; w < kWaves; ++w) {
-    const int c = q.wave_count[w];
-    if (w < wave) n += c;
-    all += c;
+  for (int o = 1; o < kWave; o <<= 1) {
+    const u32 v = static_cast<u32>(__shfl_up(static_cast<int>(sum), o, kWave));
+    if (lane >= o) sum += v;
   }
-  if (on) q.list[n + __popcll(b & ((1ull << lane) - 1))] = static_cast<uint16_t>(e);
-  if (i == 0) q.count = all;
+  if (lane == kWave - 1) q.sums[wave] = sum;
   __syncthreads();
-}
-
-// First slot of token t that names local expert e, or -1; weight: the sum over all that do.
-__device__ __forceinline__ int slot_of(const Pairs& q, const FewLayer& p, int t, int e, float& weight) {
-  int slot = -1;
-  weight = 0.f;
-  for (int j = 0; j < p.k; ++j)
-    if (q.blob[t * 2 * p.k + j] == e + p.e_begin) {
-      if (slot < 0) slot = j;
-      weight += __int_as_float(q.blob[t * 2 * p.k + p.k + j]);
-    }
-  return slot;
-}
-
-// What the down kernel needs of the routing, written by one workgroup of the gate/up kernel.
-__device__ void write_tables(Pairs& q, const FewLayer& p) {
-  for (int i = threadIdx.x; i < q.count * 16; i += kThreads) {
-    const int a = i / 16, t = i % 16;
-    float wt;
-    const int j = t < p.T ? slot_of(q, p, t, q.list[a], wt) : -1;
-    p.rows[i] = static_cast<int16_t>(j < 0 ? -1 : t * p.k + j);
-    if (t == 0) p.list[a] = q.list[a];
+  u32 all = 0;
+#pragma unroll
+  for (int n = 0; n < kWaves; ++n) {
+    const u32 v = q.sums[n];
+    if (n < wave) sum += v;
+    all += v;
   }
-  for (int i = threadIdx.x; i < p.T * 2 * p.k; i += kThreads)
-    if (p.packed_out) p.packed_out[i] = q.blob[i];
-  if (threadIdx.x < kWave) {
-    int bad = 0;
-    for (int i = threadIdx.x; i < p.T * p.k; i += kWave) {
-      const int id = q.blob[i / p.k * 2 * p.k + i % p.k];
-      bad += id < 0 || id >= p.E;
-    }
-    bad = wave_sum_int(bad);
-    if (threadIdx.x == 0) {
-      *p.err = bad;
-      *p.count = q.count;
+  sum -= mine;
+  if (lead) {
+    const int row = sum & 1023, at = (sum >> 10) & 1023, at_down = sum >> 20;
+    first[e] = row;
+    for (int n = 0; n * LIMIT < members; ++n)
+      q.entry[at + n] = make_int2(e | (n * LIMIT) << 16, static_cast<int>(m | static_cast<u32>(row + n * LIMIT) << 16));
+    if (write)
+      for (int n = 0; n * DOWN_LIMIT < members; ++n)
+        p.entry[at_down + n] =
+            make_int2(e | (n * DOWN_LIMIT) << 16, static_cast<int>(m | static_cast<u32>(row + n * DOWN_LIMIT) << 16));
+  }
+  if (i == 0) q.entries = (all >> 10) & 1023;
+  __syncthreads();
+  if (e >= 0) {
+    const int r = first[e] + __popc(m & ((1u << t) - 1));
+    q.weight[r] = w;
+    q.token[r] = static_cast<uint8_t>(t);
+  }
+  if (write) {
+    if (p.packed_out)
+      for (int n = i; n < 2 * pairs; n += kThreads) p.packed_out[n] = q.blob[n];
+    const uint64_t b = __ballot(bad);
+    if (lane == 0) q.sums[wave] = __popcll(b);
+    __syncthreads();
+    if (i == 0) {
+      int n = 0;
+      for (int v = 0; v < kWaves; ++v) n += q.sums[v];
+      *p.err = n;
+      *p.entries = all >> 20;
     }
   }
+  __syncthreads();
 }
 
 // ---------------------------------------------------------------------------
@@ -316,124 +356,113 @@ template <int W> __host__ __device__ constexpr int x_row_bytes(int D) {
 }
 
 // Units [u0, u1) of 16 channels, one after another by the whole workgroup: wave w multiplies its
-// eighth of the reduction dimension, the parts are added in wave order in LDS.
-// SHARED: the shared expert's channels; else units of list entry u / (I / 16).
+// eighth of the reduction dimension, the parts are added in wave order in LDS.  Each wave keeps
+// R steps in flight: the last R of a unit are replaced by the next unit's first.
+// SHARED: the shared expert, every token a column; else units of entry u / (I / 16), its members
+// the columns.
 template <int W, bool PACKED, bool XLDS, bool SHARED>
-__device__ __forceinline__ void gate_up_units(const FewLayer& p, const Pairs& q, const uint8_t* xs, float* red, int u0,
+__device__ __forceinline__ void gate_up_units(const FewLayer& p, const Route& q, const uint8_t* xs, float* red, int u0,
                                               int u1) {
-  constexpr int EPS = Wt<W>::EPS, NX = Wt<W>::NX, B = Wt<W>::GB, NBUF = Wt<W>::GN, as = act_bytes<W>();
+  constexpr int EPS = Wt<W>::EPS, NX = Wt<W>::NX, R = Wt<W>::R, as = act_bytes<W>();
   constexpr bool F32 = W == EL_F32;
+  if (u0 >= u1) return;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), lane = threadIdx.x % kWave;
   const int lrow = lane & 15, lgrp = lane >> 4;
   const int S = steps_of<W>(p.D), per = (SHARED ? p.I_shared : p.I) / 16;
   const int s0 = S * wave / kWaves, s1 = S * (wave + 1) / kWaves;
-  const int nb = ((S + kWaves - 1) / kWaves + B - 1) / B;  // blocks per unit, the same for every wave
-  const int total = (u1 - u0) * nb;
+  const int turns = ((S + kWaves - 1) / kWaves + R - 1) / R;  // of R steps per unit, the same for every wave
   const u32 voff = lane_offset<W, PACKED>(p.D, lane);
-  // columns past the last token repeat it and are never read
-  const int t = min(lrow, p.T - 1);
-  const uint8_t* xl = xs + t * x_row_bytes<W>(p.D) + lgrp * (EPS / 4) * as;
-  const uint8_t* xg = static_cast<const uint8_t*>(p.x) + static_cast<int64_t>(t) * p.D * as;
-
-  struct Block {
-    u32x4 w[2][B];
-  };
-  auto load = [&](Block& b, int i) {
-    const int u = u0 + i / nb, j = i % nb;
-    const int frag = __builtin_amdgcn_readfirstlane(u % per);
-    const bool unit = i < total;
-    int64_t eo = 0;
-    if (!SHARED && unit) eo = static_cast<int64_t>(__builtin_amdgcn_readfirstlane(q.list[u / per])) * p.gu_stride;
-    const __amdgpu_buffer_rsrc_t r0 = weight_rsrc(static_cast<const uint8_t*>(SHARED ? p.sh_gate : p.w_gate) + eo);
-    const __amdgpu_buffer_rsrc_t r1 = weight_rsrc(static_cast<const uint8_t*>(SHARED ? p.sh_up : p.w_up) + eo);
-#pragma unroll
-    for (int n = 0; n < B; ++n) {
-      const int s = s0 + j * B + n;
-      const bool real = unit && s < s1;
-      const u32 v = real ? voff : kOutOfRange, o = step_offset<W, PACKED>(p.D, frag, s);
-      b.w[0][n] = buffer_load16<PACKED>(r0, v, o);
-      b.w[1][n] = buffer_load16<PACKED>(r1, v, o);
-    }
-  };
-
-  f32x4 c0 = {0.f, 0.f, 0.f, 0.f}, c1 = {0.f, 0.f, 0.f, 0.f};
   const u32x4 z = {0u, 0u, 0u, 0u};
+  struct Source {
+    __amdgpu_buffer_rsrc_t r0, r1;
+    u32 at;
+    bool on;
+  };
+  auto source = [&](int u) {
+    Source o;
+    o.on = u < u1;
+    int64_t eo = 0;
+    if (!SHARED && o.on) eo = __builtin_amdgcn_readfirstlane(entry_expert(q.entry[u / per])) * p.gu_stride;
+    o.r0 = weight_rsrc(static_cast<const uint8_t*>(SHARED ? p.sh_gate : p.w_gate) + eo);
+    o.r1 = weight_rsrc(static_cast<const uint8_t*>(SHARED ? p.sh_up : p.w_up) + eo);
+    o.at = step_offset<W, PACKED>(p.D, __builtin_amdgcn_readfirstlane(u % per), 0);
+    return o;
+  };
+  u32x4 w0[R], w1[R];
+  auto load = [&](int slot, const Source& o, int s) {
+    const u32 v = o.on && s < s1 ? voff : kOutOfRange;
+    const u32 at = o.at + s * (PACKED ? 1024 : 64);
+    w0[slot] = buffer_load16<PACKED>(o.r0, v, at);
+    w1[slot] = buffer_load16<PACKED>(o.r1, v, at);
+  };
+  Source cur = source(u0);
+#pragma unroll
+  for (int n = 0; n < R; ++n) load(n, cur, s0 + n);
   float* buf = red;
-  int known = -1, slot = -1;  // list entry whose slot and weight this thread's token has looked up
-  float wt = 0.f;
-  auto finish = [&](int u) {
-    if (lrow < p.T) {
-      float* o = buf + (wave * p.T + lrow) * 16 + lgrp * 4;
-      *reinterpret_cast<f32x4*>(o) = c0;
-      *reinterpret_cast<f32x4*>(o + kWaves * p.T * 16) = c1;
+  const int cols = SHARED ? p.T : min(p.T, 16);
+  for (int u = u0; u < u1; ++u) {
+    // columns past the last member repeat it and are never read
+    const int2 en = SHARED ? make_int2(0, 0) : q.entry[u / per];
+    const int members = SHARED ? p.T : __popc(entry_mask(en)), row = entry_row(en);
+    const int t = SHARED ? min(lrow, p.T - 1) : q.token[row + min(lrow, members - 1)];
+    const uint8_t* xl = xs + t * x_row_bytes<W>(p.D) + lgrp * (EPS / 4) * as;
+    const uint8_t* xg = static_cast<const uint8_t*>(p.x) + static_cast<int64_t>(t) * p.D * as;
+    f32x4 c0 = {0.f, 0.f, 0.f, 0.f}, c1 = {0.f, 0.f, 0.f, 0.f};
+    for (int k = 0; k < turns; ++k) {
+      const bool last = k + 1 == turns;
+      if (last) cur = source(u + 1);
+      const int sl = last ? s0 : s0 + (k + 1) * R;
+#pragma unroll
+      for (int n = 0; n < R; ++n) {
+        const int s = s0 + k * R + n;
+        if (s < s1) {
+#pragma unroll
+          for (int m = 0; m < NX; ++m) {
+            u32x4 xv;
+            if constexpr (XLDS) {
+              xv = *reinterpret_cast<const u32x4*>(xl + s * EPS * as + m * 16);
+            } else {
+              const int k0 = s * EPS + lgrp * (EPS / 4);
+              xv = k0 < p.D ? reinterpret_cast<const u32x4*>(xg + static_cast<int64_t>(k0) * as)[m] : z;
+            }
+            c0 = mul<W>(weight_piece<W>(w0[n], m), xv, c0);
+            c1 = mul<W>(weight_piece<W>(w1[n], m), xv, c1);
+          }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        load(n, cur, sl + n);
+        __builtin_amdgcn_sched_barrier(0);
+      }
     }
-    c0 = c1 = f32x4{0.f, 0.f, 0.f, 0.f};
+    if (lrow < members) {
+      float* o = buf + (wave * cols + lrow) * 16 + lgrp * 4;
+      *reinterpret_cast<f32x4*>(o) = c0;
+      *reinterpret_cast<f32x4*>(o + kWaves * cols * 16) = c1;
+    }
     lds_barrier();
-    if (static_cast<int>(threadIdx.x) < p.T * 16) {
-      const int tt = threadIdx.x / 16, ch = threadIdx.x % 16, n = (u % per) * 16 + ch;
+    const int c = threadIdx.x / 16, ch = threadIdx.x % 16, n = (u % per) * 16 + ch;
+    if (c < members) {
       float g = 0.f, v = 0.f;
 #pragma unroll
       for (int w = 0; w < kWaves; ++w) {
-        g += buf[(w * p.T + tt) * 16 + ch];
-        v += buf[((kWaves + w) * p.T + tt) * 16 + ch];
+        g += buf[(w * cols + c) * 16 + ch];
+        v += buf[((kWaves + w) * cols + c) * 16 + ch];
       }
       if constexpr (SHARED) {
-        store_h<F32>(p.h_sh, static_cast<int64_t>(p.T) * p.I_shared, static_cast<int64_t>(tt) * p.I_shared + n, silu(g) * v);
+        store_h<F32>(p.h_sh, static_cast<int64_t>(p.T) * p.I_shared, static_cast<int64_t>(c) * p.I_shared + n, silu(g) * v);
       } else {
-        const int a = u / per, e = q.list[a];
-        if (a != known) {
-          slot = slot_of(q, p, tt, e, wt);
-          known = a;
+        if constexpr (W == EL_E4M3) {
+          const int64_t sc = static_cast<int64_t>(entry_expert(en)) * p.I + n;
+          g *= p.s_gate[sc];
+          v *= p.s_up[sc];
         }
-        if (slot >= 0) {
-          if constexpr (W == EL_E4M3) {
-            g *= p.s_gate[static_cast<int64_t>(e) * p.I + n];
-            v *= p.s_up[static_cast<int64_t>(e) * p.I + n];
-          }
-          store_h<F32>(p.h, static_cast<int64_t>(p.T) * p.k * p.I, (static_cast<int64_t>(tt) * p.k + slot) * p.I + n,
-                       wt * (silu(g) * v));
-        }
+        store_h<F32>(p.h, static_cast<int64_t>(p.T) * p.k * p.I, static_cast<int64_t>(row + c) * p.I + n,
+                     q.weight[row + c] * (silu(g) * v));
       }
     }
     // two buffers: the next unit's parts go into the other one; one buffer: wait until it is read
-    if (p.red_bufs == 2) buf = buf == red ? red + 2 * kWaves * p.T * 16 : red;
+    if (p.red_bufs == 2) buf = buf == red ? red + 2 * kWaves * cols * 16 : red;
     else lds_barrier();
-  };
-  auto use = [&](const Block& b, int i) {
-    const int j = i % nb;
-#pragma unroll
-    for (int n = 0; n < B; ++n) {
-      const int s = s0 + j * B + n;
-      if (s < s1) {
-#pragma unroll
-        for (int m = 0; m < NX; ++m) {
-          u32x4 xv;
-          if constexpr (XLDS) {
-            xv = *reinterpret_cast<const u32x4*>(xl + s * EPS * as + m * 16);
-          } else {
-            const int k0 = s * EPS + lgrp * (EPS / 4);
-            xv = k0 < p.D ? reinterpret_cast<const u32x4*>(xg + static_cast<int64_t>(k0) * as)[m] : z;
-          }
-          c0 = mul<W>(weight_piece<W>(b.w[0][n], m), xv, c0);
-          c1 = mul<W>(weight_piece<W>(b.w[1][n], m), xv, c1);
-        }
-      }
-    }
-    if (j == nb - 1) finish(u0 + i / nb);
-  };
-
-  Block ring[NBUF];
-#pragma unroll
-  for (int j = 0; j < NBUF - 1; ++j) load(ring[j], j);
-  for (int i = 0; i < total; i += NBUF) {
-#pragma unroll
-    for (int j = 0; j < NBUF; ++j) {
-      if (j > 0 && i + j >= total) break;
-      load(ring[(j + NBUF - 1) % NBUF], i + j + NBUF - 1);
-      __builtin_amdgcn_sched_barrier(0);
-      use(ring[j], i + j);
-      __builtin_amdgcn_sched_barrier(0);
-    }
   }
 }
 
@@ -456,103 +485,156 @@ __device__ __forceinline__ void stage_x(const FewLayer& p, uint8_t* xs) {
 // down
 // ---------------------------------------------------------------------------
 
-// Sum over blocks of 16 rows of W_down times h.  Blocks are DB steps of one matrix; this wave
-// takes every `stride`-th from `first` on.  TWO: remainders of h are a second product, else
-// columns 8 to 15.  SHARED: one matrix, h_sh; else one per list entry.
-template <int W, bool PACKED, bool TWO, bool SHARED>
-__device__ __forceinline__ f32x4 down_blocks(const FewLayer& p, const int16_t* rows, int count, int frag, int first,
-                                             int stride) {
-  constexpr int EPS = Wt<W>::EPS, NX = Wt<W>::NX, B = Wt<W>::DB, NBUF = TWO ? Wt<W>::DN2 : Wt<W>::DN;
-  constexpr int as = act_bytes<W>();
+constexpr int kDownMembers = 8;  // per entry: columns 8 to 15 are the remainders
+
+// v in the lane of each of the entry's tokens, from the lane of the member that it is.
+__device__ __forceinline__ f32x4 to_tokens(f32x4 v, int2 en, int limit) {
+  const int lane = threadIdx.x % kWave, t = lane & 15;
+  const u32 m = entry_mask(en);
+  const int r = __popc(m & ((1u << t) - 1)) - entry_rank0(en);
+  const bool on = ((m >> t) & 1u) && r >= 0 && r < limit;
+  f32x4 o;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float got = __int_as_float(__builtin_amdgcn_ds_bpermute(((lane & 48) + (r & 15)) * 4, __float_as_int(v[i])));
+    o[i] = on ? got : 0.0f;
+  }
+  return o;
+}
+
+template <int CTRL>
+__device__ __forceinline__ float dpp_add(float v) {
+  return v + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xF, 0xF, false));
+}
+constexpr int kRor4 = 0x124, kRor8 = 0x128;  // rotate by 4 or 8 lanes within 16
+
+// A wave's blocks first, first + stride, ... of `blocks`, as (hi, lo) = (id / radix, id % radix) without a
+// division each; past the last one it stays on it.
+struct Cursor {
+  int hi, lo, left, dhi, dlo, radix;
+  __device__ __forceinline__ Cursor(int first, int stride, int blocks, int r) : radix(r) {
+    left = first < blocks ? (blocks - first + stride - 1) / stride : 0;
+    hi = first / r;
+    lo = first - hi * r;
+    dhi = stride / r;
+    dlo = stride - dhi * r;
+  }
+  __device__ __forceinline__ void next() {
+    if (--left <= 0) return;
+    hi += dhi;
+    lo += dlo;
+    if (lo >= radix) {
+      lo -= radix;
+      ++hi;
+    }
+  }
+};
+
+// Sum over blocks of 16 rows of W_down times h, in the lanes of the tokens.  Blocks are DB steps of
+// one entry; this wave takes every `stride`-th from `first` on.  SHARED: entries are the call's
+// tokens in eights.
+template <int W, bool PACKED, bool SHARED>
+__device__ __forceinline__ f32x4 down_blocks(const FewLayer& p, int entries, int frag, int first, int stride) {
+  constexpr int EPS = Wt<W>::EPS, NX = Wt<W>::NX, B = Wt<W>::DB, NBUF = Wt<W>::DN, as = act_bytes<W>();
   constexpr bool F32 = W == EL_F32;
-  constexpr int NP = TWO && !F32 ? 2 : 1;  // pieces of h per weight piece
   const int lane = threadIdx.x % kWave, lrow = lane & 15, lgrp = lane >> 4;
   const int K = SHARED ? p.I_shared : p.I;
   const int S = steps_of<W>(K), nb = (S + B - 1) / B;
-  const int blocks = count * nb;
+  const int blocks = entries * nb;
+  if (blocks == 0) return f32x4{0.f, 0.f, 0.f, 0.f};
   const u32 voff = lane_offset<W, PACKED>(K, lane);
-  const int pair_rows = SHARED ? p.T : p.T * p.k;
-  const u32 plane = static_cast<u32>(pair_rows) * K * as;  // bytes of the value plane
+  const u32 plane = static_cast<u32>(SHARED ? p.T : p.T * p.k) * K * as;  // bytes of the value plane
   const __amdgpu_buffer_rsrc_t rh = buffer_rsrc_sized(SHARED ? p.h_sh : p.h, F32 ? plane : 2 * plane);
-  const int t = F32 || TWO ? lrow : lrow & 7;
-  const u32 base = (!F32 && !TWO && lrow >= 8 ? plane : 0u) + lgrp * (EPS / 4) * as;
+  const int c = lrow & (kDownMembers - 1);
+  const u32 base = (!F32 && lrow >= kDownMembers ? plane : 0u) + lgrp * (EPS / 4) * as;
 
-  struct Block {
-    u32x4 w[B], h[B][NX][NP];
-    float sd[W == EL_E4M3 ? 4 : 1];
-    bool on;
+  // the shared expert's entries change first: the second read of a block hits L2
+  auto entry = [&](const Cursor& at) {
+    if constexpr (SHARED)
+      return make_int2(at.lo * kDownMembers << 16, static_cast<int>(((1u << p.T) - 1) | at.lo * kDownMembers << 16));
+    else
+      return make_int2(ld_scalar(&p.entry[at.hi].x), ld_scalar(&p.entry[at.hi].y));
   };
-  auto load = [&](Block& b, int i) {
-    const int id = first + i * stride;
-    const bool there = id < blocks;
-    const int a = there ? id / nb : 0, j = there ? id % nb : 0;
-    int64_t eo = 0;
-    int e = 0, row = t < p.T ? t : -1;
-    if constexpr (!SHARED) {
-      e = ld_scalar(p.list + a);
-      eo = static_cast<int64_t>(e) * p.dn_stride;
-      row = rows[a * 16 + t];
-    }
-    if (!there) row = -1;
-    b.on = row >= 0;
-    const __amdgpu_buffer_rsrc_t r = weight_rsrc(static_cast<const uint8_t*>(SHARED ? p.sh_down : p.w_down) + eo);
-    const u32 ho = base + static_cast<u32>(max(row, 0)) * K * as;
+  auto block_of = [&](const Cursor& at) { return SHARED ? at.hi : at.lo; };
+  struct Block {
+    u32x4 w[B], h[B][NX];
+    float sd[W == EL_E4M3 ? 4 : 1];
+  };
+  auto load = [&](Block& b, Cursor& at) {
+    const bool there = at.left > 0;
+    const int2 en = entry(at);
+    const int e = entry_expert(en), j = block_of(at);
+    at.next();
+    const __amdgpu_buffer_rsrc_t r = weight_rsrc(static_cast<const uint8_t*>(SHARED ? p.sh_down : p.w_down) +
+                                                 static_cast<int64_t>(e) * p.dn_stride);
+    const bool on = there && c < entry_members(en, kDownMembers);
+    const u32 ho = base + static_cast<u32>(entry_row(en) + c) * K * as;
     if constexpr (W == EL_E4M3) {
       const __amdgpu_buffer_rsrc_t rs = weight_rsrc(p.s_down + static_cast<int64_t>(e) * p.D);
 #pragma unroll
       for (int n = 0; n < 4; ++n)
-        b.sd[n] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, there ? lgrp * 16 : kOutOfRange, (frag * 16 + n) * 4, 0));
+        b.sd[n] = __uint_as_float(
+            __builtin_amdgcn_raw_buffer_load_b32(rs, there ? lgrp * 16 : kOutOfRange, (frag * 16 + n) * 4, 0));
     }
 #pragma unroll
     for (int n = 0; n < B; ++n) {
       const int s = j * B + n;
       const bool real = there && s < S;
       b.w[n] = buffer_load16<PACKED>(r, real ? voff : kOutOfRange, step_offset<W, PACKED>(K, frag, s));
-      // lanes without a row, or past the width, read nothing
-      const u32 o = row >= 0 && s * EPS + lgrp * (EPS / 4) < K ? ho : kOutOfRange;
+      // lanes without a member, or past the width, read nothing
+      const u32 o = on && s * EPS + lgrp * (EPS / 4) < K ? ho : kOutOfRange;
 #pragma unroll
-      for (int m = 0; m < NX; ++m) {
-        b.h[n][m][0] = buffer_load16<false>(rh, o + m * 16, s * EPS * as);
-        if constexpr (NP == 2) b.h[n][m][1] = buffer_load16<false>(rh, o + m * 16 + plane, s * EPS * as);
-      }
+      for (int m = 0; m < NX; ++m) b.h[n][m] = buffer_load16<false>(rh, o + m * 16, s * EPS * as);
     }
   };
   f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-  auto use = [&](const Block& b, int i) {
-    f32x4 c = {0.f, 0.f, 0.f, 0.f};
-    const int j = (first + i * stride) % nb;
+  auto use = [&](const Block& b, Cursor& at) {
+    f32x4 v = {0.f, 0.f, 0.f, 0.f};
+    const int j = block_of(at);
+    const int2 en = entry(at);
+    at.next();
 #pragma unroll
-    for (int n = 0; n < B; ++n) {
-      if (j * B + n < S) {
+    for (int n = 0; n < B; ++n)
+      if (j * B + n < S)
 #pragma unroll
-        for (int m = 0; m < NX; ++m) {
-          const u32x4 w = weight_piece<W>(b.w[n], m);
-          c = mul<W>(w, b.h[n][m][0], c);
-          if constexpr (NP == 2) c = mul<W>(w, b.h[n][m][1], c);
-        }
-      }
+        for (int m = 0; m < NX; ++m) v = mul<W>(weight_piece<W>(b.w[n], m), b.h[n][m], v);
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+      if constexpr (W == EL_E4M3) v[n] *= b.sd[n];
+      if constexpr (!F32) v[n] = dpp_add<kRor8>(v[n]);
     }
-    if constexpr (W == EL_E4M3) {
-#pragma unroll
-      for (int n = 0; n < 4; ++n) c[n] *= b.sd[n];
-    }
-    if (b.on) acc += c;
+    acc += to_tokens(v, en, kDownMembers);
   };
+  Cursor ahead(first, stride, blocks, SHARED ? entries : nb), here = ahead;
+  if (here.left == 0) return acc;
   Block ring[NBUF];
-  const int mine = first < blocks ? (blocks - first + stride - 1) / stride : 0;
 #pragma unroll
-  for (int j = 0; j < NBUF - 1; ++j) load(ring[j], j);
-  for (int i = 0; i < mine; i += NBUF) {
+  for (int j = 0; j < NBUF - 1; ++j) load(ring[j], ahead);
+  for (;;) {
 #pragma unroll
     for (int j = 0; j < NBUF; ++j) {
-      if (j > 0 && i + j >= mine) break;
-      load(ring[(j + NBUF - 1) % NBUF], i + j + NBUF - 1);
+      load(ring[(j + NBUF - 1) % NBUF], ahead);
       __builtin_amdgcn_sched_barrier(0);
-      use(ring[j], i + j);
+      use(ring[j], here);
       __builtin_amdgcn_sched_barrier(0);
+      if (here.left == 0) return acc;
     }
   }
-  return acc;
+}
+
+// The waves' sums for 16 channels -> y; red: one f32x4 per thread, written before by this function.
+template <int OUT>
+__device__ __forceinline__ void finish_down(const FewLayer& p, int frag, f32x4 acc, f32x4 (&red)[kWaves][kWave]) {
+  red[threadIdx.x / kWave][threadIdx.x % kWave] = acc;
+  __syncthreads();
+  const int t = threadIdx.x / 16, ch = threadIdx.x % 16, l = (ch / 4) * 16 + t;
+  if (t >= p.T) return;
+  float v = 0.f;
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) v += red[w][l][ch % 4];
+  const int64_t idx = static_cast<int64_t>(t) * p.D + frag * 16 + ch;
+  if constexpr (OUT == EL_F32) static_cast<float*>(p.y)[idx] = v;
+  else static_cast<uint16_t*>(p.y)[idx] = static_cast<uint16_t>(bf16x2_bits(v, 0.f));
 }
 
 // Parts (of `parts`) of a launch for work of `part` out of `all`: at least one, not all.

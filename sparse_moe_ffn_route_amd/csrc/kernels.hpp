@@ -139,9 +139,8 @@ struct FewLayer {
   float* logits;             // [T][E], written unless packed_in
   int32_t* packed_out;       // the routing blob, or NULL
   int32_t* err;              // ids outside [0, E)
-  int32_t* count;            // scratch: local experts with a token,
-  int32_t* list;             // [T * k] which, ascending,
-  int16_t* rows;             // [T * k][16] and each token's row of h (t * k + slot), or -1
+  int32_t* entries;          // scratch: number of the down kernel's entries,
+  int2* entry;               // [T * k] and they (few.hpp)
   const void* w_gate;
   const void* w_up;
   const void* w_down;
@@ -152,12 +151,12 @@ struct FewLayer {
   const void* sh_up;
   const void* sh_down;
   int64_t gu_stride, dn_stride;  // bytes between experts
-  void* h;                   // [T][k][I] fp32, or two bf16 planes of it
+  void* h;                   // [T * k][I] fp32, or two bf16 planes of it
   void* h_sh;                // [T][I_shared] likewise
   void* y;                   // [T][D] of out_el
   int T, D, E, k, I, I_shared, e_begin, n_local, renormalize, out_el;
   void* x_terms;             // 4-bit weights: scratch of few_mx_x_bytes(T, D); h: few_mx_h_bytes(T, k, I)
-  int shared_blocks, shared_waves, red_bufs, shared_red_bufs;  // set by the launchers
+  int shared_blocks, shared_waves, red_bufs, red_bytes, shared_red_bufs;  // set by the launchers
 };
 size_t few_mx_x_bytes(int T, int D);
 size_t few_mx_h_bytes(int T, int k, int I);
