@@ -151,17 +151,24 @@ def _ptr(t: Optional[torch.Tensor]):
         return None
     if not isinstance(t, torch.Tensor):
         raise TypeError("expected a torch.Tensor or None")
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError("tensors must live in GPU memory")
     if not t.is_contiguous():
         raise ValueError("tensors must be contiguous")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
-def _stream(stream) -> ctypes.c_void_p:
+def _stream(stream) -> int:
     if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+        # the current stream's handle; torch.cuda.current_stream() builds an object around it (2.9 us a call)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return stream.cuda_stream
+
+
+def _on_current_device(t: torch.Tensor, what: str):
+    """The library launches on the current device: refuse a tensor of another one."""
+    if t.is_cuda and t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{what} is on cuda:{t.get_device()}, the current device is cuda:{torch.cuda.current_device()}")
 
 
 def _check(status: int, what: str):
@@ -190,8 +197,8 @@ _ELEM_BYTES = {F32: 4, BF16: 2, E4M3: 1}
 
 def _need(t: Optional[torch.Tensor], nbytes: int, what: str):
     """Refuse a tensor smaller than the dims say (the kernels trust the dims)."""
-    if t is not None and t.numel() * t.element_size() < nbytes:
-        raise ValueError(f"{what}: {t.numel() * t.element_size()} bytes, the dims need {nbytes}")
+    if t is not None and t.nbytes < nbytes:
+        raise ValueError(f"{what}: {t.nbytes} bytes, the dims need {nbytes}")
 
 
 def _check_io(dims, x=None, logits=None, packed=None, bias=None, y=None, w_router=None):
@@ -359,6 +366,7 @@ def moe_mx_weight_bytes(n_mats: int, rows: int, cols: int) -> int:
 
 def moe_mx_pack_weights(src: torch.Tensor, dst: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Round [n][rows][cols] (or [rows][cols]) fp32 or bf16 weights to microscaled FP4 images, uint8 [n][bytes]."""
+    _on_current_device(src, "src")
     n, rows, cols = _mats(src)
     if src.dtype not in (torch.float32, torch.bfloat16):
         raise ValueError("weights must be float32 or bfloat16")
@@ -374,6 +382,7 @@ def moe_mx_pack_weights(src: torch.Tensor, dst: Optional[torch.Tensor] = None, s
 def moe_mx_unpack_weights(images: torch.Tensor, rows: int, cols: int, dtype: torch.dtype = torch.bfloat16,
                           dst: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """The values of n images (uint8 [n][bytes]) as [n][rows][cols] of float32 or bfloat16."""
+    _on_current_device(images, "images")
     nbytes = moe_mx_weight_bytes(1, rows, cols)
     n = images.numel() // nbytes if nbytes else images.shape[0]
     if dst is None:
@@ -391,6 +400,7 @@ def moe_mx_unpack_weights(images: torch.Tensor, rows: int, cols: int, dtype: tor
 def moe_layer_forward_few(dims, weights: moe_weights, x, packed_in, logit_bias, y, logits_out=None, packed_out=None,
                           ws=None, stream=None):
     """moe_layer_forward for up to FEW_MAX_T tokens, in two launches after the router's."""
+    _on_current_device(x, "x")
     _check_io(dims, x=x, logits=logits_out, packed=packed_in, bias=logit_bias, y=y)
     _need(packed_out, dims.T * 2 * dims.top_k * 4, "packed_out")
     _check(library().moe_layer_forward_few(ctypes.byref(dims), ctypes.byref(weights), _ptr(x), _ptr(packed_in),
@@ -402,20 +412,29 @@ def moe_layer_forward_few(dims, weights: moe_weights, x, packed_in, logit_bias, 
 def _make_norm(T, D, act, w_post, gate, gate_kind, res_scale, eps, w_next) -> moe_norm:
     """moe_norm after checks of its tensors' types and sizes."""
     if gate_kind is None:
-        gate_kind = "none" if gate is None else "full" if gate.dim() == 2 else None
-        if gate_kind is None:
+        if gate is not None and gate.dim() != 2:
             raise ValueError("a one-dimensional gate needs gate_kind 'token' or 'channel'")
+        gate_kind = "none" if gate is None else "full"
     kind = _GATE_CODE[gate_kind]
-    for t, what in ((w_post, "w_post"), (w_next, "w_next"), (gate if kind != GATE_TOKEN else None, "gate")):
-        if t is not None and t.dtype != act:
-            raise ValueError(f"{what}: {t.dtype}, the residual stream is {act}")
-    if kind == GATE_TOKEN and gate is not None and gate.dtype != torch.float32:
-        raise ValueError("a token gate is float32")
-    es = 4 if act == torch.float32 else 2
-    _need(w_post, D * es, "w_post")
-    _need(w_next, D * es, "w_next")
-    _need(gate, {GATE_NONE: 0, GATE_TOKEN: T * 4, GATE_CHANNEL: D * es, GATE_FULL: T * D * es}[kind], "gate")
+    row = D * (4 if act == torch.float32 else 2)
+    _need_like(w_post, row, act, "w_post")
+    _need_like(w_next, row, act, "w_next")
+    if kind == GATE_TOKEN:
+        if gate is not None and gate.dtype != torch.float32:
+            raise ValueError("a token gate is float32")
+        _need(gate, T * 4, "gate")
+    elif gate is not None:
+        _need_like(gate, row if kind == GATE_CHANNEL else T * row, act, "gate")
     return moe_norm(_ptr(w_post), _ptr(gate), _ptr(w_next), kind, res_scale, eps)
+
+
+def _need_like(t: Optional[torch.Tensor], nbytes: int, dtype: torch.dtype, what: str):
+    """_need, and the type of the residual stream."""
+    if t is not None:
+        if t.dtype != dtype:
+            raise ValueError(f"{what}: {t.dtype}, the residual stream is {dtype}")
+        if t.nbytes < nbytes:
+            raise ValueError(f"{what}: {t.nbytes} bytes, the dims need {nbytes}")
 
 
 def moe_block_norm(y, r, r_out=None, w_post=None, gate=None, gate_kind=None, res_scale=1.0, eps=1e-6, w_next=None,
@@ -423,16 +442,18 @@ def moe_block_norm(y, r, r_out=None, w_post=None, gate=None, gate_kind=None, res
     """Leave a block and enter the next on the residual stream r [T][D]; y None: only enter."""
     if r.dim() != 2:
         raise ValueError("r must be [T][D]")
+    _on_current_device(r, "r")
     T, D = r.shape
-    n = _make_norm(T, D, r.dtype, w_post, gate, gate_kind, res_scale, eps, w_next)
-    for t, what in ((r_out, "r_out"), (x_next, "x_next")):
-        if t is not None and t.dtype != r.dtype:
-            raise ValueError(f"{what}: {t.dtype}, the residual stream is {r.dtype}")
-        _need(t, T * D * r.element_size(), what)
-    _need(y, T * D * (y.element_size() if y is not None else 0), "y")
-    _check(library().moe_block_norm(T, D, _CODE_OF_TORCH.get(r.dtype, -1),
-                                    _CODE_OF_TORCH.get(y.dtype, -1) if y is not None else F32, ctypes.byref(n),
-                                    _ptr(y), _ptr(r), _ptr(r_out), _ptr(x_next), _stream(stream)), "moe_block_norm")
+    act = r.dtype
+    n = _make_norm(T, D, act, w_post, gate, gate_kind, res_scale, eps, w_next)
+    _need_like(r_out, r.nbytes, act, "r_out")
+    _need_like(x_next, r.nbytes, act, "x_next")
+    y_code = F32
+    if y is not None:
+        y_code = _CODE_OF_TORCH.get(y.dtype, -1)
+        _need(y, T * D * y.element_size(), "y")
+    _check(library().moe_block_norm(T, D, _CODE_OF_TORCH.get(act, -1), y_code, ctypes.byref(n), _ptr(y), _ptr(r),
+                                    _ptr(r_out), _ptr(x_next), _stream(stream)), "moe_block_norm")
 
 
 def block_workspace(dims: moe_dims, device="cuda") -> torch.Tensor:
@@ -447,13 +468,14 @@ def moe_block_forward(dims, weights: moe_weights, r, r_out, w_in=None, x_in=None
                       gate=None, gate_kind=None, res_scale=1.0, eps=1e-6, w_next=None, x_next=None, ws=None,
                       stream=None):
     """Pre-norm (or x_in), the layer, and moe_block_norm on the residual stream r."""
-    act = _TORCH_OF.get(dims.act_dtype)
-    n = _make_norm(dims.T, dims.D, act, w_post, gate, gate_kind, res_scale, eps, w_next)
-    for t, what in ((r, "r"), (r_out, "r_out"), (x_next, "x_next"), (x_in, "x_in"), (w_in, "w_in")):
-        if t is not None and t.dtype != act:
-            raise ValueError(f"{what}: {t.dtype}, the layer's hidden states are {act}")
-        _need(t, (1 if what == "w_in" else dims.T) * dims.D * _ELEM_BYTES[dims.act_dtype], what)
-    _check_io(dims, bias=logit_bias)
+    _on_current_device(r, "r")
+    T, D, act = dims.T, dims.D, _TORCH_OF.get(dims.act_dtype)
+    n = _make_norm(T, D, act, w_post, gate, gate_kind, res_scale, eps, w_next)
+    row = D * _ELEM_BYTES.get(dims.act_dtype, 0)
+    for t, what in ((r, "r"), (r_out, "r_out"), (x_next, "x_next"), (x_in, "x_in")):
+        _need_like(t, T * row, act, what)
+    _need_like(w_in, row, act, "w_in")
+    _need(logit_bias, dims.E * 4, "logit bias")
     _check(library().moe_block_forward(ctypes.byref(dims), ctypes.byref(weights), _ptr(w_in), _ptr(x_in),
                                        _ptr(logit_bias), ctypes.byref(n), _ptr(r), _ptr(r_out), _ptr(x_next),
                                        _ptr(ws), ws.numel() if ws is not None else 0, _stream(stream)),

@@ -42,6 +42,8 @@ int check_dims(const moe_dims* d) {
   if (d->w_dtype == MOE_MXFP4 && d->weight_layout != MOE_LAYOUT_PACKED) return MOE_ERR_UNSUPPORTED;
   // every row index and byte offset below fits the kernels' integer types
   const int64_t tk = static_cast<int64_t>(d->T) * d->top_k;
+  if (d->w_dtype == MOE_MXFP4 && tk * std::max(mx_row_bytes(d->D), mx_row_bytes(d->I)) >= (1ll << 32))
+    return MOE_ERR_UNSUPPORTED;
   if (tk > (1ll << 30) || static_cast<int64_t>(d->T) * d->E > (1ll << 31) - 1) return MOE_ERR_UNSUPPORTED;
   // one expert's (and the router's) weight matrix is addressed with 32-bit offsets
   const int64_t wsz = d->w_dtype == MOE_F32 ? 4 : d->w_dtype == MOE_BF16 ? 2 : 1;
@@ -240,22 +242,28 @@ int routed_bm(const moe_dims& d, bool gathered) {
 // records of h, down to out_rows.
 int mx_experts(const moe_dims& d, void* ws, const Layout& L, const void* a_rows, const int32_t* perm,
                const int32_t* offsets, const void* w_gate, const void* w_up, const void* w_down, void* out_rows,
-               hipEvent_t ev_gate_up, hipEvent_t ev_down, hipStream_t s) {
+               bool have_tile_prefix, hipEvent_t ev_gate_up, hipEvent_t ev_down, hipStream_t s) {
   const int bm = mx_bm(d);
   const int tk = d.T * d.top_k;
+  int32_t* prefix = at<int32_t>(ws, L.tp_a);
+  const int m_tiles = routed_tile_bound(tk, d.n_local, bm, 1, 1);
   void* xm = at<void>(ws, L.xq);
   void* hm = at<void>(ws, L.h);
-  MOE_TRY(launch_mx_rows(a_rows, perm ? d.T : tk, perm ? nullptr : offsets + d.n_local, d.D, xm, s));
+  MOE_TRY(launch_mx_rows(a_rows, perm ? d.T : tk, perm ? nullptr : offsets + d.n_local, d.D, xm, offsets, d.n_local,
+                         bm, have_tile_prefix ? nullptr : prefix, s));
   MxGemm p{};
-  p.a = xm; p.perm = perm; p.offsets = offsets; p.tile_prefix = at<int32_t>(ws, L.tp_a); p.n_groups = d.n_local;
+  p.a = xm; p.perm = perm; p.offsets = offsets; p.tile_prefix = prefix; p.n_groups = d.n_local;
+  // tiles to expect: the local experts that are likely to have rows, with their share of the rows
+  const double share = static_cast<double>(tk) * d.n_local / d.E;
+  p.busy_tiles = std::max(1, std::min(m_tiles, static_cast<int>(std::min<double>(d.n_local, share) + share / bm)));
   p.w0 = w_gate; p.w1 = w_up; p.w_stride = d.I / 16 * mx_fragment_bytes(d.D);
   p.out = hm; p.N = d.I; p.K = d.D;
-  MOE_TRY(launch_mx_gemm(true, EL_BF16, bm, p, routed_tile_bound(tk, d.n_local, bm, d.I, mx_gemm_bn(true)), s));
+  MOE_TRY(launch_mx_gemm(true, EL_BF16, bm, p, m_tiles, s));
   if (ev_gate_up) MOE_TRY(hipEventRecord(ev_gate_up, s));
-  p.a = hm; p.perm = nullptr; p.tile_prefix = at<int32_t>(ws, L.tp_b);
+  p.a = hm; p.perm = nullptr;
   p.w0 = w_down; p.w1 = nullptr; p.w_stride = d.D / 16 * mx_fragment_bytes(d.I);
   p.out = out_rows; p.N = d.D; p.K = d.I;
-  MOE_TRY(launch_mx_gemm(false, d.out_dtype, bm, p, routed_tile_bound(tk, d.n_local, bm, d.D, mx_gemm_bn(false)), s));
+  MOE_TRY(launch_mx_gemm(false, d.out_dtype, bm, p, m_tiles, s));
   if (ev_down) MOE_TRY(hipEventRecord(ev_down, s));
   return MOE_OK;
 }
@@ -282,10 +290,11 @@ int experts_forward(const moe_dims& d, void* ws, const Layout& L, const void* a_
   const int hel = h_el(d);
   const bool shared = d.I_shared > 0 && sh_gate;
 
-  if (!have_tile_prefix) MOE_TRY(launch_tile_prefix(offsets, d.n_local, bm, bm, tp_a, tp_b, s));
+  if (!have_tile_prefix && d.w_dtype != MOE_MXFP4) MOE_TRY(launch_tile_prefix(offsets, d.n_local, bm, bm, tp_a, tp_b, s));
 
   if (d.w_dtype == MOE_MXFP4) {
-    const int st = mx_experts(d, ws, L, a_rows, perm, offsets, w_gate, w_up, w_down, out_rows, ev_gate_up, ev_down, s);
+    const int st = mx_experts(d, ws, L, a_rows, perm, offsets, w_gate, w_up, w_down, out_rows, have_tile_prefix,
+                              ev_gate_up, ev_down, s);
     if (st != MOE_OK) return st;
   } else {
     const int bn_gu = gemm_bn(true, shape, w_el(d), packed), bn_dn = gemm_bn(false, shape, w_el(d), packed);

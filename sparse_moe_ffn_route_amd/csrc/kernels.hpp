@@ -108,8 +108,9 @@ hipError_t launch_mx_pack(int src_el, const void* src, int64_t n_mats, int rows,
                           hipStream_t stream);
 hipError_t launch_mx_unpack(int dst_el, const void* src, int64_t n_mats, int rows, int cols, void* dst,
                             hipStream_t stream);
+// prefix (nullable): also the M-tile prefix [n_groups + 1] for tile height bm of the groups at offsets.
 hipError_t launch_mx_rows(const void* src, int rows, const int32_t* n_rows_dev, int cols, void* dst,
-                          hipStream_t stream);
+                          const int32_t* offsets, int n_groups, int bm, int32_t* prefix, hipStream_t stream);
 
 // Grouped GEMM on 4-bit rows and weights.  Rows of group g are [offsets[g], offsets[g + 1]); row r
 // reads record row perm[r] (or r).  tile_prefix: M-tile prefix for height bm (16, 32 or 128).
@@ -124,9 +125,10 @@ struct MxGemm {
   int64_t w_stride;            // bytes between consecutive groups' images
   void* out;                   // SwiGLU: records of width N; else [rows][N] of the output type
   int N, K;
+  int busy_tiles;              // M-tiles to expect (m_tiles is an upper bound)
+  int parts;                   // set by the launcher: parts of the channels, one workgroup each
 };
-int mx_gemm_bn(bool swiglu);  // channels per workgroup
-hipError_t launch_mx_gemm(bool swiglu, int out_el, int bm, const MxGemm& p, int max_tiles, hipStream_t stream);
+hipError_t launch_mx_gemm(bool swiglu, int out_el, int bm, const MxGemm& p, int m_tiles, hipStream_t stream);
 
 // The whole layer for up to kFewMaxT tokens.  w_el: EL_F32, EL_BF16, EL_E4M3 or 3 (4-bit images,
 // MOE_MXFP4); x, router and shared weights are F32 with F32 experts, else BF16.

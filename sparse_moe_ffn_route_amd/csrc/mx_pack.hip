@@ -122,11 +122,44 @@ __global__ __launch_bounds__(256) void mx_unpack_kernel(const uint8_t* __restric
   }
 }
 
+// M-tile prefix of at most 1024 groups by one workgroup of 256 threads: four groups per thread.
+__device__ void tile_prefix(const int32_t* offsets, int n_groups, int bm, int32_t* prefix) {
+  __shared__ int sums[4];
+  const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave, g0 = threadIdx.x * 4;
+  int c[4], mine = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    c[i] = g0 + i < n_groups ? (offsets[g0 + i + 1] - offsets[g0 + i] + bm - 1) / bm : 0;
+    mine += c[i];
+  }
+  int sum = mine;
+#pragma unroll
+  for (int o = 1; o < kWave; o <<= 1) {
+    const int v = __shfl_up(sum, o, kWave);
+    if (lane >= o) sum += v;
+  }
+  if (lane == kWave - 1) sums[wave] = sum;
+  __syncthreads();
+  for (int w = 0; w < wave; ++w) sum += sums[w];
+  sum -= mine;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (g0 + i <= n_groups) prefix[g0 + i] = sum;
+    sum += c[i];
+  }
+  if (threadIdx.x == 255 && n_groups == 1024) prefix[1024] = sum;
+}
+
 // bf16 rows -> records.  Four lanes share a block (8 values each): loads of 16 bytes and
 // stores of 4 bytes per lane are contiguous over the wave, one wave per record.
 __global__ __launch_bounds__(256) void mx_rows_kernel(const uint16_t* __restrict__ src, int rows,
                                                       const int32_t* __restrict__ n_rows_dev, int cols,
-                                                      uint8_t* __restrict__ dst) {
+                                                      uint8_t* __restrict__ dst, const int32_t* __restrict__ offsets,
+                                                      int n_groups, int bm, int32_t* __restrict__ prefix) {
+  if (prefix && blockIdx.x == gridDim.x - 1) {
+    tile_prefix(offsets, n_groups, bm, prefix);
+    return;
+  }
   const int groups = mx_groups(cols);
   const int64_t u = static_cast<int64_t>(blockIdx.x) * 4 + threadIdx.x / kWave;
   const int64_t row = u / groups;
@@ -183,11 +216,12 @@ hipError_t launch_mx_unpack(int dst_el, const void* src, int64_t n_mats, int row
 }
 
 hipError_t launch_mx_rows(const void* src, int rows, const int32_t* n_rows_dev, int cols, void* dst,
-                          hipStream_t stream) {
+                          const int32_t* offsets, int n_groups, int bm, int32_t* prefix, hipStream_t stream) {
   const int64_t units = static_cast<int64_t>(rows) * mx_groups(cols);
   if (units == 0) return hipSuccess;
-  hipLaunchKernelGGL(mx_rows_kernel, dim3(static_cast<uint32_t>((units + 3) / 4)), dim3(256), 0, stream,
-                     static_cast<const uint16_t*>(src), rows, n_rows_dev, cols, static_cast<uint8_t*>(dst));
+  hipLaunchKernelGGL(mx_rows_kernel, dim3(static_cast<uint32_t>((units + 3) / 4) + (prefix ? 1 : 0)), dim3(256), 0,
+                     stream, static_cast<const uint16_t*>(src), rows, n_rows_dev, cols, static_cast<uint8_t*>(dst),
+                     offsets, n_groups, bm, prefix);
   return hipGetLastError();
 }
 
