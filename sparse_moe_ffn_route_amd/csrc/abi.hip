@@ -226,11 +226,11 @@ int route_tokens(const moe_dims& d, const void* x, const void* w_router, float* 
   return hip_status(launch_route(nullptr, 1, logits, bias, d.T, d.E, d.top_k, d.renormalize, packed, s));
 }
 
-// M-tile height of the 4-bit grouped GEMMs, by the average routed rows per expert: one tile of
-// 16 or 32 rows reads each weight byte once; above, 128-row tiles reuse it.
+// M-tile height of the 4-bit grouped GEMMs, by the average routed rows per expert: up to 32 rows a
+// tile of one unit, above tiles of up to four.
 int mx_bm(const moe_dims& d) {
   const double avg = static_cast<double>(d.T) * d.top_k / d.E;
-  return avg <= 16.0 ? 16 : avg <= 32.0 ? 32 : 128;
+  return avg <= 32.0 ? 32 : 128;
 }
 
 // M-tile height of the routed grouped GEMMs of these dims.

@@ -113,7 +113,7 @@ hipError_t launch_mx_rows(const void* src, int rows, const int32_t* n_rows_dev, 
                           const int32_t* offsets, int n_groups, int bm, int32_t* prefix, hipStream_t stream);
 
 // Grouped GEMM on 4-bit rows and weights.  Rows of group g are [offsets[g], offsets[g + 1]); row r
-// reads record row perm[r] (or r).  tile_prefix: M-tile prefix for height bm (16, 32 or 128).
+// reads record row perm[r] (or r).  tile_prefix: M-tile prefix for height bm (32 or 128).
 struct MxGemm {
   const void* a;               // records of width K
   const int32_t* perm;
