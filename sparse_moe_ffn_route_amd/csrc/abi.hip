@@ -5,6 +5,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <cmath>
 #include <mutex>
 
 #include "moe.h"
@@ -253,9 +254,9 @@ int mx_experts(const moe_dims& d, void* ws, const Layout& L, const void* a_rows,
                          bm, have_tile_prefix ? nullptr : prefix, s));
   MxGemm p{};
   p.a = xm; p.perm = perm; p.offsets = offsets; p.tile_prefix = prefix; p.n_groups = d.n_local;
-  // tiles to expect: the local experts that are likely to have rows, with their share of the rows
-  const double share = static_cast<double>(tk) * d.n_local / d.E;
-  p.busy_tiles = std::max(1, std::min(m_tiles, static_cast<int>(std::min<double>(d.n_local, share) + share / bm)));
+  // tiles to expect: of the local experts that are likely to have rows, each with an even share of them
+  const double rows = static_cast<double>(tk) * d.n_local / d.E, busy = std::max(1.0, std::min<double>(d.n_local, rows));
+  p.busy_tiles = std::min(m_tiles, static_cast<int>(busy * std::max(1.0, std::ceil(rows / busy / bm))));
   p.w0 = w_gate; p.w1 = w_up; p.w_stride = d.I / 16 * mx_fragment_bytes(d.D);
   p.out = hm; p.N = d.I; p.K = d.D;
   MOE_TRY(launch_mx_gemm(true, EL_BF16, bm, p, m_tiles, s));

@@ -204,11 +204,29 @@ __device__ __forceinline__ void swap_halves(u32& a, u32& b) {
   b = r[1];
 }
 
+// Plain results pass through LDS, 16 rows of 128 bytes at a time in a place of each wave's own, and go
+// out as whole lines (stored from where the MFMA leaves them, 16 bytes here and there, they took
+// twice the time).
+constexpr int kStageRow = 128 + 16;
+constexpr int kStage = 16 * kStageRow;
+
+// Rows r0 .. r0 + 15 (of nrows) of the stage -> row r of the output at out + r * stride.
+__device__ __forceinline__ void flush_stage(const uint8_t* stage, uint8_t* out, size_t stride, int r0, int nrows, int lane) {
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int r = i * 8 + lane / 8;
+    const u32x4 v = *reinterpret_cast<const u32x4*>(stage + r * kStageRow + (lane & 7) * 16);
+    if (r0 + r < nrows) *reinterpret_cast<u32x4*>(out + static_cast<size_t>(r0 + r) * stride + (lane & 7) * 16) = v;
+  }
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+}
+
 // A wave's results for its channels ncol0 .. -> memory.  Lane l holds column (token) l % 32 and, in
 // element 4 i + k, channel 8 i + 4 (l / 32) + k of the pair's 32.
 template <int MU, bool SWIGLU, int OUT>
 __device__ __forceinline__ void store_tile(const MxGemm& p, const f32x16 (&acc)[kPairs][MU], int row0, int nrows,
-                                           int ncol0, int lane) {
+                                           int ncol0, int lane, uint8_t* stage) {
   if (ncol0 >= p.N) return;
   const int half = lane >> 5;
 #pragma unroll
@@ -252,28 +270,38 @@ __device__ __forceinline__ void store_tile(const MxGemm& p, const f32x16 (&acc)[
         }
       }
     } else {
+      // the wave's 64 channels are all there (N is a multiple of 64)
+      constexpr int es = OUT == EL_F32 ? 4 : 2;
+      uint8_t* out = static_cast<uint8_t*>(p.out) + (static_cast<size_t>(row0) * p.N + ncol0) * es;
+      const size_t stride = static_cast<size_t>(p.N) * es;
+      uint8_t* at = stage + (lane & 15) * kStageRow;
 #pragma unroll
-      for (int f = 0; f < kPairs; ++f) {
-        if (ncol0 + f * 32 >= p.N) continue;
-        const size_t idx = static_cast<size_t>(grow) * p.N + ncol0 + f * 32;
-        const f32x16 o = acc[f][m];
+      for (int part = 0; part < 2; ++part) {  // rows 0 .. 15 and 16 .. 31 of the unit
+        const bool mine = ((lane >> 4) & 1) == part;
         if constexpr (OUT == EL_F32) {
-          if (live)
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              *reinterpret_cast<float4*>(static_cast<float*>(p.out) + idx + 8 * i + 4 * half) =
-                  make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+          for (int f = 0; f < kPairs; ++f) {
+            if (mine)
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                *reinterpret_cast<float4*>(at + (2 * i + half) * 16) =
+                    make_float4(acc[f][m][4 * i], acc[f][m][4 * i + 1], acc[f][m][4 * i + 2], acc[f][m][4 * i + 3]);
+            flush_stage(stage, out + f * 128, stride, m * kUnitRows + part * 16, nrows, lane);
+          }
         } else {
 #pragma unroll
-          for (int i = 0; i < 4; i += 2) {
-            // lanes below 32 get channels 8 i .. + 7, the lanes above the eight after them
-            u32 a0 = bf16x2_bits(o[4 * i], o[4 * i + 1]), a1 = bf16x2_bits(o[4 * i + 2], o[4 * i + 3]);
-            u32 b0 = bf16x2_bits(o[4 * i + 4], o[4 * i + 5]), b1 = bf16x2_bits(o[4 * i + 6], o[4 * i + 7]);
-            swap_halves(a0, b0);
-            swap_halves(a1, b1);
-            if (live)
-              *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + idx + 8 * (i + half)) = make_uint4(a0, a1, b0, b1);
-          }
+          for (int f = 0; f < kPairs; ++f)
+#pragma unroll
+            for (int i = 0; i < 4; i += 2) {
+              // lanes below 32 get channels 8 i .. + 7, the lanes above the eight after them
+              const f32x16& o = acc[f][m];
+              u32 a0 = bf16x2_bits(o[4 * i], o[4 * i + 1]), a1 = bf16x2_bits(o[4 * i + 2], o[4 * i + 3]);
+              u32 b0 = bf16x2_bits(o[4 * i + 4], o[4 * i + 5]), b1 = bf16x2_bits(o[4 * i + 6], o[4 * i + 7]);
+              swap_halves(a0, b0);
+              swap_halves(a1, b1);
+              if (mine) *reinterpret_cast<uint4*>(at + (f * 4 + i + half) * 16) = make_uint4(a0, a1, b0, b1);
+            }
+          flush_stage(stage, out, stride, m * kUnitRows + part * 16, nrows, lane);
         }
       }
     }
@@ -358,7 +386,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void mx_resident_kernel(MxGemm p) {
 #pragma unroll
           for (int j = 0; j < 2; ++j) sc[q][j] = nsc[q][j];
       }
-      store_tile<MU, SWIGLU, OUT>(p, acc, t.row0, t.nrows, b * BN + wcol, lane);
+      store_tile<MU, SWIGLU, OUT>(p, acc, t.row0, t.nrows, b * BN + wcol, lane, lds + G * kBuf + wave * kStage);
     }
   });
 }
@@ -366,7 +394,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void mx_resident_kernel(MxGemm p) {
 template <int MF, bool SWIGLU, int OUT>
 __global__ __launch_bounds__(kWaves * 64, 2) void mx_ring_kernel(MxGemm p) {
   constexpr int BN = mx_bn(SWIGLU), kBuf = MF * kUnitRows * kMxRecord;
-  __shared__ __attribute__((aligned(16))) uint8_t lds[kRing * kBuf];
+  __shared__ __attribute__((aligned(16))) uint8_t lds[kRing * kBuf + (SWIGLU ? 0 : kWaves * kStage)];
   const int total = ld_scalar(p.tile_prefix + p.n_groups) * p.parts;
   if (static_cast<int>(blockIdx.x) >= total) return;
   const Tile t = locate(p, xcd_remap(blockIdx.x, total), p.parts);
@@ -411,8 +439,28 @@ __global__ __launch_bounds__(kWaves * 64, 2) void mx_ring_kernel(MxGemm p) {
       wait_vmcnt<kLead * kGroupLoads>();
       bare_barrier();
     }
-    store_tile<MU, SWIGLU, OUT>(p, acc, t.row0, t.nrows, ncol0, lane);
+    store_tile<MU, SWIGLU, OUT>(p, acc, t.row0, t.nrows, ncol0, lane, lds + kRing * kBuf + wave * kStage);
   });
+}
+
+// Into how many parts a resident tile's blocks of channels go, one workgroup each.  Tiles of one unit
+// are bound by their weights and take as many workgroups as there are blocks (64 such tiles of 16
+// blocks: 24.7 us, against 27.9 with half as many).  Taller ones cost about 0.7 of a block's time to
+// begin with, and run in rounds of two workgroups per CU: 128 tiles of 16 blocks took 49 us in 4
+// parts (one round), 52 in 8 and 58 in 16; 192 tiles 106 us in 3 parts (two rounds, the second
+// almost empty), 91 in 5.
+int resident_parts(int tiles, int blocks) {
+  int best = 1;
+  double least = 0.0;
+  for (int parts = 1; parts <= blocks; ++parts) {
+    const int rounds = (tiles * parts + 511) / 512;
+    const double cost = rounds * (static_cast<double>((blocks + parts - 1) / parts) + 0.7);
+    if (parts == 1 || cost < least) {
+      best = parts;
+      least = cost;
+    }
+  }
+  return best;
 }
 
 template <int MF, bool SWIGLU, int OUT>
@@ -420,9 +468,9 @@ hipError_t launch_mf(MxGemm p, int m_tiles, hipStream_t stream) {
   const int lds = mx_groups(p.K) * MF * kUnitRows * kMxRecord;
   const int blocks = (p.N + mx_bn(SWIGLU) - 1) / mx_bn(SWIGLU);
   if (lds <= kResidentBytes) {
-    // parts of the channels: enough workgroups for two per CU
-    p.parts = std::min(blocks, std::max(1, (2 * 256 + p.busy_tiles - 1) / p.busy_tiles));
-    hipLaunchKernelGGL((mx_resident_kernel<MF, SWIGLU, OUT>), dim3(m_tiles * p.parts), dim3(kWaves * 64), lds, stream, p);
+    p.parts = MF == 1 ? blocks : resident_parts(p.busy_tiles, blocks);
+    hipLaunchKernelGGL((mx_resident_kernel<MF, SWIGLU, OUT>), dim3(m_tiles * p.parts), dim3(kWaves * 64),
+                       lds + (SWIGLU ? 0 : kWaves * kStage), stream, p);
   } else {
     p.parts = blocks;
     hipLaunchKernelGGL((mx_ring_kernel<MF, SWIGLU, OUT>), dim3(m_tiles * p.parts), dim3(kWaves * 64), 0, stream, p);
