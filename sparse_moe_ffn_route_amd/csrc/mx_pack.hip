@@ -14,6 +14,7 @@ namespace moe {
 namespace {
 
 typedef uint32_t u32;
+typedef float f32x2 __attribute__((ext_vector_type(2)));
 
 // 8 consecutive values as float.
 template <int EL>
@@ -40,7 +41,7 @@ __device__ __forceinline__ void load8(const void* base, size_t idx, float (&v)[8
 // out as whole 1 KB runs and the scales as one 256-byte store.
 template <int EL>
 __global__ __launch_bounds__(256) void mx_pack_kernel(const void* __restrict__ src, uint8_t* __restrict__ dst,
-                                                      int64_t units, int frags, int cols) {
+                                                      int64_t units, int cols) {
   const int64_t u = static_cast<int64_t>(blockIdx.x) * 4 + threadIdx.x / kWave;
   if (u >= units) return;
   const int lane = threadIdx.x % kWave;
@@ -76,17 +77,12 @@ __global__ __launch_bounds__(256) void mx_pack_kernel(const void* __restrict__ s
   *reinterpret_cast<u32*>(out + steps * kMxRun + lane * 4) = scales;
 }
 
-// The value of a code (nibble i of w) times the block's scale; scale byte 255 is NaN.
-__device__ __forceinline__ float mx_value(u32 w, int i, float scale) {
-  const u32 c = (w >> (4 * i)) & 15u, m = c & 7u;
-  const float a = m < 2 ? 0.5f * m : static_cast<float>((2u | (m & 1u)) << (m >> 1)) * 0.25f;
-  const float v = a * scale;
-  return c & 8u ? -v : v;
-}
-
+// One wave per (matrix, 16 rows, group).  Lane l decodes one dword of codes at a time, 8 values of row
+// r0 + l / 16 from (l % 16) * 8 on, so that four rows' 128 values go out as whole lines (a lane that
+// decoded a block of its own stored 16 bytes every 64 and took twice the time).
 template <int EL>
 __global__ __launch_bounds__(256) void mx_unpack_kernel(const uint8_t* __restrict__ src, void* __restrict__ dst,
-                                                        int64_t units, int frags, int cols) {
+                                                        int64_t units, int cols) {
   const int64_t u = static_cast<int64_t>(blockIdx.x) * 4 + threadIdx.x / kWave;
   if (u >= units) return;
   const int lane = threadIdx.x % kWave;
@@ -95,28 +91,37 @@ __global__ __launch_bounds__(256) void mx_unpack_kernel(const uint8_t* __restric
   const int64_t fr = u / groups;
   const int steps = min(4, mx_steps(cols) - g * 4);
   const uint8_t* in = src + fr * mx_fragment_bytes(cols) + static_cast<int64_t>(g) * kMxGroupBytes;
-  const size_t row = static_cast<size_t>(fr) * 16 + (lane & 15);
-  const u32 scales = *reinterpret_cast<const u32*>(in + steps * kMxRun + lane * 4);
-  for (int s = 0; s < steps; ++s) {
-    const int k0 = g * kMxGroup + s * kMxStep + (lane >> 4) * kMxBlock;
-    if (k0 >= cols) continue;
-    const u32x4 codes = *reinterpret_cast<const u32x4*>(in + s * kMxRun + lane * 16);
-    const u32 b = (scales >> (8 * s)) & 255u;
-    const float scale = b == 255u ? __uint_as_float(0x7FC00000u) : ldexpf(1.0f, static_cast<int>(b) - 127);
+  const int blk = (lane & 15) >> 2, r = lane >> 4;
+  u32 scales[4];
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      float v[8];
+  for (int i = 0; i < 4; ++i)
+    scales[i] = *reinterpret_cast<const u32*>(in + steps * kMxRun + (blk * 16 + i * 4 + r) * 4);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = mx_value(codes[c], i, scale);
-      const size_t idx = row * cols + k0 + c * 8;
+  for (int s = 0; s < 4; ++s) {
+    const int k0 = g * kMxGroup + s * kMxStep + (lane & 15) * 8;
+    if (s >= steps || k0 >= cols) continue;
+    u32 w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      w[i] = *reinterpret_cast<const u32*>(in + s * kMxRun + blk * 256 + (i * 4 + r) * 16 + (lane & 3) * 4);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const u32 b = (scales[i] >> (8 * s)) & 255u;
+      const float scale = __uint_as_float(b == 255u ? 0x7FC00000u : b << 23);  // byte 255 stands for NaN
+      const size_t idx = (static_cast<size_t>(fr) * 16 + i * 4 + r) * cols + k0;
+      f32x2 v[4];
+      v[0] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[i], 1.0f, 0) * scale;
+      v[1] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[i], 1.0f, 1) * scale;
+      v[2] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[i], 1.0f, 2) * scale;
+      v[3] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[i], 1.0f, 3) * scale;
       if constexpr (EL == EL_F32) {
         float4* p = reinterpret_cast<float4*>(static_cast<float*>(dst) + idx);
-        p[0] = make_float4(v[0], v[1], v[2], v[3]);
-        p[1] = make_float4(v[4], v[5], v[6], v[7]);
+        p[0] = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
+        p[1] = make_float4(v[2].x, v[2].y, v[3].x, v[3].y);
       } else {
         *reinterpret_cast<uint4*>(static_cast<uint16_t*>(dst) + idx) =
-            make_uint4(bf16x2_bits(v[0], v[1]), bf16x2_bits(v[2], v[3]), bf16x2_bits(v[4], v[5]),
-                       bf16x2_bits(v[6], v[7]));
+            make_uint4(bf16x2_bits(v[0].x, v[0].y), bf16x2_bits(v[1].x, v[1].y), bf16x2_bits(v[2].x, v[2].y),
+                       bf16x2_bits(v[3].x, v[3].y));
       }
     }
   }
@@ -187,31 +192,29 @@ __global__ __launch_bounds__(256) void mx_rows_kernel(const uint16_t* __restrict
 
 hipError_t launch_mx_pack(int src_el, const void* src, int64_t n_mats, int rows, int cols, void* dst,
                           hipStream_t stream) {
-  const int frags = rows / 16;
-  const int64_t units = n_mats * frags * mx_groups(cols);
+  const int64_t units = n_mats * (rows / 16) * mx_groups(cols);
   if (units == 0) return hipSuccess;
   const dim3 grid(static_cast<uint32_t>((units + 3) / 4));
   if (src_el == EL_F32)
     hipLaunchKernelGGL((mx_pack_kernel<EL_F32>), grid, dim3(256), 0, stream, src, static_cast<uint8_t*>(dst), units,
-                       frags, cols);
+                       cols);
   else
     hipLaunchKernelGGL((mx_pack_kernel<EL_BF16>), grid, dim3(256), 0, stream, src, static_cast<uint8_t*>(dst), units,
-                       frags, cols);
+                       cols);
   return hipGetLastError();
 }
 
 hipError_t launch_mx_unpack(int dst_el, const void* src, int64_t n_mats, int rows, int cols, void* dst,
                             hipStream_t stream) {
-  const int frags = rows / 16;
-  const int64_t units = n_mats * frags * mx_groups(cols);
+  const int64_t units = n_mats * (rows / 16) * mx_groups(cols);
   if (units == 0) return hipSuccess;
   const dim3 grid(static_cast<uint32_t>((units + 3) / 4));
   if (dst_el == EL_F32)
     hipLaunchKernelGGL((mx_unpack_kernel<EL_F32>), grid, dim3(256), 0, stream, static_cast<const uint8_t*>(src), dst,
-                       units, frags, cols);
+                       units, cols);
   else
     hipLaunchKernelGGL((mx_unpack_kernel<EL_BF16>), grid, dim3(256), 0, stream, static_cast<const uint8_t*>(src), dst,
-                       units, frags, cols);
+                       units, cols);
   return hipGetLastError();
 }
 
