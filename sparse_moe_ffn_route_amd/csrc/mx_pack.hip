@@ -15,30 +15,79 @@ namespace {
 
 typedef uint32_t u32;
 typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16v2 __attribute__((ext_vector_type(2)));
 
-// 8 consecutive values as float.
+// 8 consecutive values: fp32, or bf16 as they are.
 template <int EL>
-__device__ __forceinline__ void load8(const void* base, size_t idx, float (&v)[8]) {
-  if constexpr (EL == EL_F32) {
-    const u32x4* p = reinterpret_cast<const u32x4*>(static_cast<const float*>(base) + idx);
-    const u32x4 a = p[0], b = p[1];
+struct Octet {
+  u32 w[EL == EL_F32 ? 8 : 4];
+
+  __device__ __forceinline__ void load(const void* base, size_t idx) {
+    constexpr int bytes = EL == EL_F32 ? 4 : 2;
+    const u32x4* p = reinterpret_cast<const u32x4*>(static_cast<const uint8_t*>(base) + idx * bytes);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[i] = __uint_as_float(a[i]);
-      v[4 + i] = __uint_as_float(b[i]);
-    }
-  } else {
-    const u32x4 a = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(base) + idx);
+    for (int i = 0; i < bytes; ++i) reinterpret_cast<u32x4&>(w[4 * (i / 2)]) = p[i / 2];
+  }
+
+  // Bits of the largest magnitude, as fp32.
+  __device__ __forceinline__ u32 abs_max() const {
+    if constexpr (EL == EL_F32) {
+      u32 m = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[2 * i] = bf16_bits_to_f32(a[i] & 0xFFFFu);
-      v[2 * i + 1] = __uint_as_float(a[i] & 0xFFFF0000u);
+      for (int i = 0; i < 8; ++i) m = max(m, w[i] & 0x7FFFFFFFu);
+      return m;
+    } else {
+      u16x2 m = {0, 0};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, w[i] & 0x7FFF7FFFu));
+      return static_cast<u32>(m.x > m.y ? m.x : m.y) << 16;
     }
+  }
+
+  // Codes of the values divided by scale, a power of two.
+  __device__ __forceinline__ u32 codes(float scale) const {
+    u32 r = 0;
+    if constexpr (EL == EL_F32) {
+      r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, __uint_as_float(w[0]), __uint_as_float(w[1]), scale, 0);
+      r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, __uint_as_float(w[2]), __uint_as_float(w[3]), scale, 1);
+      r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, __uint_as_float(w[4]), __uint_as_float(w[5]), scale, 2);
+      r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, __uint_as_float(w[6]), __uint_as_float(w[7]), scale, 3);
+    } else {
+      r = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(r, __builtin_bit_cast(bf16v2, w[0]), scale, 0);
+      r = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(r, __builtin_bit_cast(bf16v2, w[1]), scale, 1);
+      r = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(r, __builtin_bit_cast(bf16v2, w[2]), scale, 2);
+      r = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(r, __builtin_bit_cast(bf16v2, w[3]), scale, 3);
+    }
+    return r;
+  }
+};
+
+// The value of the lane whose index differs by X (1 or 2) from this one's, within its four.
+template <int X>
+__device__ __forceinline__ u32 quad_xor(u32 v) {
+  constexpr int ctrl = X == 1 ? 0xB1 : 0x4E;  // quad_perm 1,0,3,2 and 2,3,0,1
+  return static_cast<u32>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), ctrl, 0xF, 0xF, false));
+}
+
+// w[i] of lane q becomes w[q] of lane i, within four lanes.
+__device__ __forceinline__ void quad_transpose(u32 (&w)[4], int q) {
+  const bool odd = (q & 1) != 0, high = (q & 2) != 0;
+#pragma unroll
+  for (int i = 0; i < 4; i += 2) {
+    const u32 got = quad_xor<1>(odd ? w[i] : w[i + 1]);
+    if (odd) w[i] = got; else w[i + 1] = got;
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const u32 got = quad_xor<2>(high ? w[i] : w[i + 2]);
+    if (high) w[i] = got; else w[i + 2] = got;
   }
 }
 
-// One wave per (matrix, 16 rows, group): lane l encodes one block per step, so the codes go
-// out as whole 1 KB runs and the scales as one 256-byte store.
+// One wave per (matrix, 16 rows, group).  Lane l reads 8 values of row 4 i + l / 16 from (l % 16) * 8 on
+// (whole lines), a block's four lanes share its magnitude, and a 4x4 transpose between them makes each
+// the holder of one block, so the codes go out as whole 1 KB runs and the scales as one 256-byte store.
 template <int EL>
 __global__ __launch_bounds__(256) void mx_pack_kernel(const void* __restrict__ src, uint8_t* __restrict__ dst,
                                                       int64_t units, int cols) {
@@ -50,31 +99,34 @@ __global__ __launch_bounds__(256) void mx_pack_kernel(const void* __restrict__ s
   const int64_t fr = u / groups;  // fragment over all matrices
   const int steps = min(4, mx_steps(cols) - g * 4);
   uint8_t* out = dst + fr * mx_fragment_bytes(cols) + static_cast<int64_t>(g) * kMxGroupBytes;
-  const size_t row = static_cast<size_t>(fr) * 16 + (lane & 15);
+  const int q = lane & 3, blk = (lane & 15) >> 2, r = lane >> 4;
+  const int slot = blk * 16 + q * 4 + r;  // the block that this lane stores
   u32 scales = 0x7F7F7F7Fu;
-  for (int s = 0; s < steps; ++s) {
-    const int k0 = g * kMxGroup + s * kMxStep + (lane >> 4) * kMxBlock;
-    u32x4 codes = {0u, 0u, 0u, 0u};
-    if (k0 < cols) {
-      float v[4][8];
-      u32 m = 0;
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        load8<EL>(src, row * cols + k0 + c * 8, v[c]);
+  for (int s = 0; s < 4; ++s) {
+    if (s >= steps) continue;
+    const int k0 = g * kMxGroup + s * kMxStep + (lane & 15) * 8;
+    const int k = min(k0, cols - 8);  // behind the last value: read again, stored as zero
+    Octet<EL> v[4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) m = max(m, mx_abs_bits(v[c][i]));
-      }
+    for (int i = 0; i < 4; ++i) v[i].load(src, (static_cast<size_t>(fr) * 16 + i * 4 + r) * cols + k);
+    u32 codes[4];
+    u32 byte = 127u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      u32 m = v[i].abs_max();
+      m = max(m, quad_xor<1>(m));
+      m = max(m, quad_xor<2>(m));
       const u32 b = mx_scale_byte(m);
-      scales = (scales & ~(0xFFu << (8 * s))) | (b << (8 * s));
-      if (b != 255u) {
-        const float inv = mx_inverse_scale(b);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) codes[c] = mx_codes8(v[c], inv);
-      }
+      const u32 c = v[i].codes(__uint_as_float(b << 23));
+      codes[i] = b == 255u || k0 >= cols ? 0u : c;
+      byte = i == q ? b : byte;
     }
-    *reinterpret_cast<u32x4*>(out + s * kMxRun + lane * 16) = codes;
+    if (k0 < cols) scales = (scales & ~(0xFFu << (8 * s))) | (byte << (8 * s));
+    quad_transpose(codes, q);
+    *reinterpret_cast<u32x4*>(out + s * kMxRun + slot * 16) = u32x4{codes[0], codes[1], codes[2], codes[3]};
   }
-  *reinterpret_cast<u32*>(out + steps * kMxRun + lane * 4) = scales;
+  *reinterpret_cast<u32*>(out + steps * kMxRun + slot * 4) = scales;
 }
 
 // One wave per (matrix, 16 rows, group).  Lane l decodes one dword of codes at a time, 8 values of row
@@ -173,15 +225,13 @@ __global__ __launch_bounds__(256) void mx_rows_kernel(const uint16_t* __restrict
   if (row >= n) return;
   const int lane = threadIdx.x % kWave;
   const int k0 = g * kMxGroup + lane * 8;
-  float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  if (k0 < cols) load8<EL_BF16>(src, static_cast<size_t>(row) * cols + k0, v);
-  u32 m = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) m = max(m, mx_abs_bits(v[i]));
-  m = max(m, static_cast<u32>(__shfl_xor(static_cast<int>(m), 1, kWave)));
-  m = max(m, static_cast<u32>(__shfl_xor(static_cast<int>(m), 2, kWave)));
+  Octet<EL_BF16> v = {};
+  if (k0 < cols) v.load(src, static_cast<size_t>(row) * cols + k0);
+  u32 m = v.abs_max();
+  m = max(m, quad_xor<1>(m));
+  m = max(m, quad_xor<2>(m));
   const u32 b = mx_scale_byte(m);
-  const u32 codes = b == 255u ? 0u : mx_codes8(v, mx_inverse_scale(b));
+  const u32 codes = b == 255u ? 0u : v.codes(__uint_as_float(b << 23));
   uint8_t* out = dst + row * mx_row_bytes(cols) + static_cast<int64_t>(g) * kMxRecord;
   *reinterpret_cast<u32*>(out + lane * 4) = codes;
   const int blk = lane >> 2;  // block of the group: step blk / 4, lane group blk % 4

@@ -110,6 +110,46 @@ def test_pack_weights_image_and_values(n, rows, cols, dtype):
         np.testing.assert_array_equal(to_np(got), want)
 
 
+def _around_every_border(dtype):
+    """Per exponent field: a largest value, and what lies around every rounding border below it, as [16][cols]."""
+    if dtype == torch.bfloat16:
+        man = torch.arange(128)
+        field = torch.arange(1, 255)[:, None, None]
+        v = ((field - torch.arange(5)[:, None]).clamp(min=0) << 7 | man).reshape(254, -1)  # five binades' values
+        top = (torch.arange(1, 255) << 7 | 127)
+        bits = torch.cat([v, v | 0x8000], 1)
+    else:
+        tie = torch.tensor([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0, 7.0]).view(torch.int32)
+        tie = torch.cat([tie - 1, tie, tie + 1]).long()
+        field = torch.arange(1, 255)
+        v = torch.where(field[:, None] > 6, tie + ((field[:, None] - 129) << 23), torch.randint(1 << 22, (254, 24)))
+        top = field << 23 | 0x7FFFFF
+        bits = torch.cat([v, v | 0x80000000], 1)
+    n = -(-bits.shape[1] // 31)
+    out = torch.zeros(254, n, 32, dtype=torch.int64)
+    out[:, :, 31] = top[:, None]
+    flat = torch.zeros(254, n * 31, dtype=torch.int64)
+    flat[:, :bits.shape[1]] = bits
+    out[:, :, :31] = flat.reshape(254, n, 31)
+    flat = out.reshape(-1)
+    cols = -(-flat.numel() // 16 // 64) * 64
+    flat = torch.cat([flat, torch.zeros(16 * cols - flat.numel(), dtype=torch.int64)]).reshape(16, cols)
+    if dtype == torch.bfloat16:
+        return torch.where(flat > 32767, flat - 65536, flat).to(torch.int16).view(torch.bfloat16)
+    return torch.where(flat > 2 ** 31 - 1, flat - 2 ** 32, flat).to(torch.int32).view(torch.float32)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_pack_weights_around_every_border(dtype):
+    v = _around_every_border(dtype)
+    codes, exps = mx.encode(v.double().numpy()[None])
+    img = moe.moe_mx_pack_weights(v.cuda()[None])
+    np.testing.assert_array_equal(img.cpu().numpy().reshape(1, -1), mx.image(codes, exps))
+    back = moe.moe_mx_unpack_weights(img, *v.shape, dtype=torch.float32).cpu().numpy()
+    np.testing.assert_array_equal(back, mx.decode(codes, exps).astype(np.float32))
+
+
 @pytest.mark.gpu
 def test_pack_weights_non_finite_blocks():
     """A NaN or an infinity makes its block NaN and no other."""
