@@ -68,8 +68,8 @@ enum moe_status {
   MOE_ERR_BAD_DIMS = -2,    /* T < 0, D/E/I/top_k < 1, top_k > E, expert slice outside [0, E) */
   MOE_ERR_UNSUPPORTED = -3, /* dtype combination, D or I not a multiple of 64, E > 1024, top_k > 32,
                                one expert's or the router's weight matrix of 2 GiB or more, MXFP4 with
-                               T * top_k rows of x or h in 4 bits of 4 GiB or more; a call that does not
-                               take these dims (stated there) */
+                               T * top_k rows of x or h in 4 bits of 4 GiB or more, or x, images, rows or ws
+                               off a 16-byte boundary; a call that does not take these dims (stated there) */
   MOE_ERR_WORKSPACE = -4,   /* ws_bytes smaller than moe_workspace_bytes(dims) */
   MOE_ERR_HIP = -5,         /* a kernel launch failed (see moe_last_hip_error) */
   MOE_ERR_SCRATCH_LIMIT = -6 /* moe_layer_forward_noalloc: the dims need more than MOE_STATIC_SCRATCH_BYTES */
@@ -335,7 +335,7 @@ int moe_pack_weights(int32_t dtype, int64_t n_mats, int32_t rows, int32_t cols, 
  *
  *   src_dtype / dst_dtype  MOE_F32 or MOE_BF16
  *   n_mats, rows, cols     as in moe_pack_weights: rows a multiple of 16, cols of 64
- *   src, dst               device; images at 16-byte, rows at 16-byte aligned addresses
+ *   src, dst               device, at 16-byte aligned addresses (else MOE_ERR_UNSUPPORTED)
  * moe_mx_weight_bytes returns 0 for sizes outside these rules.
  */
 size_t moe_mx_weight_bytes(int64_t n_mats, int32_t rows, int32_t cols);
@@ -354,8 +354,8 @@ int moe_mx_unpack_weights(int32_t dst_dtype, int64_t n_mats, int32_t rows, int32
  *     the exact layer than moe_layer_forward's;
  *   - a token that names one expert in several slots gets it once with the summed weight.
  * The sum over experts is taken in another order than moe_layer_forward's; each call is
- * deterministic.  Returns MOE_ERR_UNSUPPORTED for T > MOE_FEW_MAX_T and where T * top_k * I or
- * T * I_shared reaches 2^28.
+ * deterministic.  Returns MOE_ERR_UNSUPPORTED for T > MOE_FEW_MAX_T, where T * top_k * I or
+ * T * I_shared reaches 2^28, and where x, a weight matrix or ws is not at a 16-byte aligned address.
  */
 #define MOE_FEW_MAX_T 16
 int moe_layer_forward_few(const moe_dims* dims, const moe_weights* weights, const void* x, const int32_t* packed_in,

@@ -89,7 +89,7 @@ int router_splits(const moe_dims& d) {
 struct Layout {
   size_t err, logits, logits_part, packed, hist, base, rank, bad, counts, offsets, tp_a, tp_b, perm_token, inv_pos;
   size_t cand_key, cand_id, cand_stats;
-  size_t xq, sx, h, h_sh, hq, sh, out_rows, few_h, few_h_sh, few_entries, few_xt, total;
+  size_t xq, sx, h, h_sh, hq, sh, out_rows, layer, few_h, few_h_sh, few_entries, few_xt, total;
 };
 
 // Whether the few-token layer takes these dims: it addresses h (4 bytes per value) with 32-bit offsets.
@@ -137,6 +137,7 @@ Layout layout(const moe_dims& d) {
   L.hq = take(fp8 ? tk * d.I : 0);
   L.sh = take(fp8 ? tk * 4 : 0);
   L.out_rows = take(tk * d.D * os);
+  L.layer = off;  // all but the few-token layer's parts
   // h of the few-token layer: fp32, two bf16 planes, or the terms of the 4-bit kernels
   L.few_h = take(!is_few(d) ? 0 : mx ? few_mx_h_bytes(d.T, d.top_k, d.I) : tk * d.I * 4);
   L.few_xt = take(is_few(d) && mx ? few_mx_x_bytes(d.T, d.D) : 0);
@@ -147,6 +148,12 @@ Layout layout(const moe_dims& d) {
 }
 
 template <typename P> P* at(void* ws, size_t off) { return reinterpret_cast<P*>(static_cast<uint8_t*>(ws) + off); }
+
+// Whether a kernel may read or write 16 bytes at a time at these addresses (NULL: not used).
+template <typename... P>
+bool aligned16(const P*... ptrs) {
+  return ((reinterpret_cast<uintptr_t>(ptrs) | ...) & 15) == 0;
+}
 
 int hip_status(hipError_t e) {
   if (e == hipSuccess) return MOE_OK;
@@ -244,6 +251,7 @@ int routed_bm(const moe_dims& d, bool gathered) {
 int mx_experts(const moe_dims& d, void* ws, const Layout& L, const void* a_rows, const int32_t* perm,
                const int32_t* offsets, const void* w_gate, const void* w_up, const void* w_down, void* out_rows,
                bool have_tile_prefix, hipEvent_t ev_gate_up, hipEvent_t ev_down, hipStream_t s) {
+  if (!aligned16(a_rows, w_gate, w_up, w_down, out_rows, ws)) return MOE_ERR_UNSUPPORTED;
   const int bm = mx_bm(d);
   const int tk = d.T * d.top_k;
   int32_t* prefix = at<int32_t>(ws, L.tp_a);
@@ -592,14 +600,15 @@ int moe_layer_forward_noalloc(const moe_dims* dims, const moe_weights* w, const 
                               int32_t* bad_ids, void* const* stage_events, void* stream) {
   const int st = check_dims(dims);
   if (st != MOE_OK) return st;
-  const size_t need = layout(*dims).total;
-  if (need > MOE_STATIC_SCRATCH_BYTES) return MOE_ERR_SCRATCH_LIMIT;
+  const Layout L = layout(*dims);
+  if (L.layer > MOE_STATIC_SCRATCH_BYTES) return MOE_ERR_SCRATCH_LIMIT;
   if (dims->T == 0) return MOE_OK;
   void* ws = nullptr;
   const int sst = static_scratch(&ws);
   if (sst != MOE_OK) return sst;
-  const int r = moe_layer_forward(dims, w, x, packed_in, logit_bias, y, logits_out, packed_out, ws,
-                                  MOE_STATIC_SCRATCH_BYTES, stage_events, stream);
+  // the few-token layer's parts lie behind everything that this call touches
+  const int r = moe_layer_forward(dims, w, x, packed_in, logit_bias, y, logits_out, packed_out, ws, L.total,
+                                  stage_events, stream);
   if (r != MOE_OK || !bad_ids) return r;
   return hip_status(hipMemcpyAsync(bad_ids, static_cast<uint8_t*>(ws) + MOE_WS_ERROR_OFFSET, sizeof(int32_t),
                                    hipMemcpyDeviceToDevice, static_cast<hipStream_t>(stream)));
@@ -617,6 +626,7 @@ int moe_mx_pack_weights(int32_t src_dtype, int64_t n_mats, int32_t rows, int32_t
   if (st != MOE_OK) return st;
   if (n_mats == 0 || rows == 0 || cols == 0) return MOE_OK;
   if (!src || !dst) return MOE_ERR_NULL_ARG;
+  if (!aligned16(src, dst)) return MOE_ERR_UNSUPPORTED;
   return hip_status(launch_mx_pack(src_dtype, src, n_mats, rows, cols, dst, static_cast<hipStream_t>(stream)));
 }
 
@@ -627,6 +637,7 @@ int moe_mx_unpack_weights(int32_t dst_dtype, int64_t n_mats, int32_t rows, int32
   if (st != MOE_OK) return st;
   if (n_mats == 0 || rows == 0 || cols == 0) return MOE_OK;
   if (!src || !dst) return MOE_ERR_NULL_ARG;
+  if (!aligned16(src, dst)) return MOE_ERR_UNSUPPORTED;
   return hip_status(launch_mx_unpack(dst_dtype, src, n_mats, rows, cols, dst, static_cast<hipStream_t>(stream)));
 }
 
@@ -642,6 +653,9 @@ int moe_layer_forward_few(const moe_dims* dims, const moe_weights* w, const void
   const Layout L = layout(d);
   if (ws_bytes < L.total) return MOE_ERR_WORKSPACE;
   if (d.T == 0) return MOE_OK;
+  if (!aligned16(x, ws, packed_in ? nullptr : w->w_router, w->w_gate, w->w_up, w->w_down,
+                 d.I_shared ? w->sh_gate : nullptr, d.I_shared ? w->sh_up : nullptr, d.I_shared ? w->sh_down : nullptr))
+    return MOE_ERR_UNSUPPORTED;
   const bool mx = d.w_dtype == MOE_MXFP4;
   const int64_t es = d.w_dtype == MOE_F32 ? 4 : d.w_dtype == MOE_BF16 ? 2 : 1;
   FewLayer p{};

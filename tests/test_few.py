@@ -44,6 +44,12 @@ def test_argument_checks():
     assert call(_dims(), w=no_router) == moe.ERR_NULL_ARG
     assert call(_dims(), n=moe.moe_workspace_bytes(_dims()) - 1) == moe.ERR_WORKSPACE
     assert call(_dims(T=0)) == moe.OK
+    off = ctypes.c_void_p(258)
+    assert call(_dims(), x=off) == moe.ERR_UNSUPPORTED                     # off a 16-byte boundary
+    assert call(_dims(), ws=off) == moe.ERR_UNSUPPORTED
+    for i in range(4):
+        ptr = [off if i == j else fake for j in range(4)]
+        assert call(_dims(), w=moe.moe_weights(*ptr, *[None] * 6)) == moe.ERR_UNSUPPORTED
     with pytest.raises(ValueError, match="x:"):
         moe.moe_layer_forward_few(_dims(), w, torch.zeros(4, 64, dtype=torch.bfloat16), None, None,
                                   torch.zeros(8, 64, dtype=torch.bfloat16))
@@ -102,6 +108,9 @@ CASES = [
     (13, 576, 64, 6, 128, 0, 16, 16, True, True),
     (5, 128, 32, 2, 64, 0, 30, 1, True, True),
     (2, 4160, 8, 2, 64, 64, 0, 8, False, True),
+    (16, 8192, 4, 2, 64, 64, 0, 4, False, True),       # x past the LDS
+    (16, 4096, 6, 3, 128, 192, 0, 6, True, True),      # x in the LDS as 4-bit terms or not at all
+    (11, 2048, 6, 3, 1088, 0, 0, 6, False, True),
 ]
 
 
@@ -242,6 +251,92 @@ def test_streams_graphs_and_repeats(w):
         assert torch.equal(y, want[i])
         moe.moe_layer_forward_few(d, wts, xs[(i + 1) % 3], None, None, y2, ws=ws)
         assert torch.equal(y2, want[(i + 1) % 3])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("E,k", [(8, 2), (100, 7), (130, 32), (600, 5), (1024, 32)])
+def test_equal_and_nan_logits(E, k):
+    """Equal logits keep the lowest ids; tokens with a NaN, with equal and with ordinary logits in one call route as
+    the full layer routes them, and the ordinary ones' results stay within the bar (the experts of a call are summed
+    in the order in which its tokens name them, so another token's choice may change a sum's order)."""
+    rng = np.random.default_rng(E)
+    T, D, I = 6, 128, 64
+    layer = Layer(rng, D, E, E, I, 0, "bf16")
+    layer.router[::2] = layer.router[0]                                    # half of the experts in a tie
+    x = torch.from_numpy(rng.standard_normal((T, D)).astype(np.float32)).to(torch.bfloat16)
+    x[1] = 0                                                               # all of them
+    clean, logits, blob, _ = _run(layer, x.cuda(), True, T, D, E, k, I, 0, 0, E, True, "f32")
+    ids, wt = oracle.unpack_routing(blob.cpu().numpy())
+    np.testing.assert_array_equal(ids, oracle.route(logits.cpu().numpy(), k)[0])
+    np.testing.assert_array_equal(ids[1], np.arange(k))
+    assert rel_err(to_np(clean), layer.reference(to_np(x), ids, wt.astype(np.float64), 0)) <= 1e-4 + 2.0 ** -24
+    x[3, 5] = float("nan")
+    got, _, blob, ws = _run(layer, x.cuda(), True, T, D, E, k, I, 0, 0, E, True, "f32")
+    rest = [0, 1, 2, 4, 5]
+    assert rel_err(to_np(got)[rest], to_np(clean)[rest]) <= 2 * (1e-4 + 2.0 ** -24)
+    d = moe.make_dims(T, D, E, k, I, 0, 0, E, True, "bf16", "bf16", "f32", "packed")
+    full = torch.empty_like(blob)
+    y2 = torch.empty(T, D, device="cuda")
+    moe.moe_layer_forward(d, layer.on_gpu(True), x.cuda(), None, None, y2, None, full, moe.workspace(d))
+    np.testing.assert_array_equal(blob[:, 0].cpu().numpy(), full[:, 0].cpu().numpy())
+    assert np.isnan(to_np(got)[3]).all() == np.isnan(to_np(y2)[3]).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("w", ["bf16", "e4m3", "mxfp4"])
+def test_two_calls_at_once(w):
+    """Two layers on two streams, each with its workspace: both give what they give alone."""
+    rng = np.random.default_rng(9)
+    shapes = [(7, 256, 32, 4, 128, 64), (16, 512, 24, 3, 192, 0)]
+    jobs = []
+    for T, D, E, k, I, Is in shapes:
+        layer = Layer(rng, D, E, E, I, Is, w)
+        x = torch.from_numpy(rng.standard_normal((T, D)).astype(np.float32)).to(layer.f).cuda()
+        d = moe.make_dims(T, D, E, k, I, Is, 0, E, True, "bf16", w, "bf16", "packed")
+        wts, ws = layer.on_gpu(True), moe.workspace(d)
+        y = torch.empty_like(x)
+        moe.moe_layer_forward_few(d, wts, x, None, None, y, ws=ws)
+        torch.cuda.synchronize()
+        jobs.append((layer, d, wts, x, ws, y, torch.cuda.Stream()))
+    outs = [[torch.empty_like(j[3]) for _ in range(8)] for j in jobs]
+    torch.cuda.synchronize()
+    for i in range(8):
+        for o, (_, d, wts, x, ws, _, s) in zip(outs, jobs):
+            moe.moe_layer_forward_few(d, wts, x, None, None, o[i], ws=ws, stream=s)
+    torch.cuda.synchronize()
+    for o, j in zip(outs, jobs):
+        assert all(torch.equal(v, j[5]) for v in o)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("w", ["bf16", "mxfp4"])
+def test_experts_behind_four_gigabytes(w):
+    """A call that takes the last of so many experts that their matrices pass 4 GiB, against the same one alone."""
+    T, D, I, k = 3, 4096, 2048, 1
+    one = moe.moe_mx_weight_bytes(1, I, D) if w == "mxfp4" else I * D * 2
+    n = (1 << 32) // one + 2
+    g = torch.Generator(device="cuda").manual_seed(1)
+    mats = [torch.randn(s, generator=g, device="cuda", dtype=torch.bfloat16) / s[-1] ** 0.5
+            for s in ((1, I, D), (1, I, D), (1, D, I))]
+    pack = moe.moe_mx_pack_weights if w == "mxfp4" else moe.moe_pack_weights
+    small = [pack(m).view(torch.uint8).reshape(-1) for m in mats]
+    big = [torch.zeros(n * one, dtype=torch.uint8, device="cuda") for _ in small]
+    for b, s in zip(big, small):
+        b[-one:] = s
+    x = torch.randn(T, D, generator=g, device="cuda").to(torch.bfloat16)
+    wt = torch.tensor([[0.5], [1.0], [0.25]])
+    ys = []
+    for count, m in ((n, big), (1, small)):
+        ids = np.full((T, 1), count - 1, np.int32)
+        blob = torch.from_numpy(oracle.pack_routing(ids, wt.numpy())).cuda()
+        d = moe.make_dims(T, D, count, k, I, 0, 0, count, True, "bf16", w, "f32", "packed")
+        wts = moe.make_weights(None, *m)
+        for call in (moe.moe_layer_forward_few, moe.moe_layer_forward):
+            y = torch.empty(T, D, device="cuda")
+            call(d, wts, x, blob, None, y, ws=moe.workspace(d))
+            ys.append(y)
+    assert torch.equal(ys[0], ys[2]) and torch.equal(ys[1], ys[3])
+    assert ys[0].abs().max() > 0.1
 
 
 @pytest.mark.gpu

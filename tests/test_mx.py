@@ -45,6 +45,8 @@ def test_pack_and_unpack_argument_checks():
         assert f(moe.BF16, 1, 16, 64, None, fake, None) == moe.ERR_NULL_ARG
         assert f(moe.BF16, 1, 16, 64, fake, None, None) == moe.ERR_NULL_ARG
         assert f(moe.BF16, 0, 16, 64, None, None, None) == moe.OK
+        assert f(moe.BF16, 1, 16, 64, ctypes.c_void_p(264), fake, None) == moe.ERR_UNSUPPORTED  # off 16 bytes
+        assert f(moe.BF16, 1, 16, 64, fake, ctypes.c_void_p(264), None) == moe.ERR_UNSUPPORTED
     with pytest.raises(ValueError, match="float32 or bfloat16"):
         moe.moe_mx_pack_weights(torch.zeros(16, 64, dtype=torch.float16))
     with pytest.raises(ValueError, match="images"):
@@ -62,6 +64,11 @@ def test_dims_take_mxfp4_with_packed_bf16_only():
     lib = moe.library()
     d, fake = moe.make_dims(**ok), ctypes.c_void_p(256)
     w = moe.moe_weights(fake, fake, fake, fake, None, None, None, None, None, None)
+    off = ctypes.c_void_p(264)
+    for i in range(5):                          # rows, images, output off a 16-byte boundary
+        p = [off if i == j else fake for j in range(5)]
+        assert lib.moe_grouped_ffn(ctypes.byref(d), p[0], None, None, fake, p[1], p[2], p[3], None, None, None, p[4],
+                                   fake, 1 << 30, None) == moe.ERR_UNSUPPORTED
     assert lib.moe_audit_workspace_bytes(ctypes.byref(d), 4) == 0
     assert lib.moe_audit(ctypes.byref(d), ctypes.byref(w), fake, fake, fake, fake, 4, None, fake, fake, 1 << 30,
                          None) == moe.ERR_UNSUPPORTED
@@ -189,6 +196,10 @@ FFN = [
     ([260, 40], 1088, 576, "f32"),
     ([0, 0, 40, 0], 128, 64, "bf16"),
     ([70], 4224, 64, "bf16"),
+    ([200, 50], 128, 1088, "bf16"),             # h wider than the LDS, in tall tiles and in short ones
+    ([8, 30], 64, 4224, "f32"),
+    ([0, 2, 0, 1] * 256, 64, 64, "bf16"),       # the most groups
+    ([40] * 70 + [0] * 5, 64, 64, "f32"),
 ]
 
 
@@ -293,3 +304,54 @@ def test_layer_forward(T, D, E, k, I, Is, begin, nl, given):
         lim += 2.0 ** -8 * (np.abs(h) @ np.abs(dn).T)       # the shared h is stored in bf16
     lim += 1e-4 * np.abs(ref).max(1, keepdims=True)
     assert (np.abs(to_np(y) - ref) <= lim).all(), float((np.abs(to_np(y) - ref) - lim).max())
+
+
+@pytest.mark.gpu
+def test_layer_captured_and_without_a_workspace():
+    """The layer captured and replayed, with eager calls between, and on the library's own scratch: the same bits."""
+    rng = np.random.default_rng(3)
+    D, E, k, I, Is = 256, 16, 3, 128, 64
+    bf = lambda *s: torch.from_numpy((rng.standard_normal(s) / np.sqrt(s[-1])).astype(np.float32)).to(torch.bfloat16)  # noqa: E731
+    _, img, _ = _weights(rng, E, D, I)
+    keep = [bf(E, D).cuda(), *img, *[moe.moe_pack_weights(bf(*s).cuda()) for s in ((Is, D), (Is, D), (D, Is))]]
+    wts = moe.make_weights(*keep[:4], None, None, None, *keep[4:])
+    for T in (1, 30, 300):
+        d = moe.make_dims(T, D, E, k, I, Is, 0, E, True, "bf16", "mxfp4", "bf16", "packed")
+        xs = [bf(T, D).cuda() for _ in range(3)]
+        ws = moe.workspace(d)
+        x, y, y2 = (torch.empty_like(xs[0]) for _ in range(3))
+        want = []
+        for v in xs:
+            moe.moe_layer_forward(d, wts, v, None, None, y, ws=ws)
+            want.append(y.clone())
+            moe.moe_layer_forward_noalloc(d, wts, v, None, None, y2)
+            assert torch.equal(y2, y)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            moe.moe_layer_forward(d, wts, x, None, None, y, ws=ws)
+        for i in (0, 2, 1, 0):
+            x.copy_(xs[i])
+            g.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(y, want[i])
+            moe.moe_layer_forward(d, wts, xs[(i + 1) % 3], None, None, y2, ws=ws)
+            assert torch.equal(y2, want[(i + 1) % 3])
+
+
+@pytest.mark.gpu
+def test_rows_behind_four_gigabytes():
+    """Grouped rows whose fp32 results pass 4 GiB: the last rows equal those of a small call on the same tokens."""
+    D, I, T = 8192, 64, 140000
+    g = torch.Generator(device="cuda").manual_seed(2)
+    mats = [torch.randn(s, generator=g, device="cuda") / s[-1] ** 0.5 for s in ((1, I, D), (1, I, D), (1, D, I))]
+    img = [moe.moe_mx_pack_weights(m) for m in mats]
+    x = torch.randn(T, D, generator=g, device="cuda", dtype=torch.bfloat16)
+    res = []
+    for n in (T, 200):
+        d = moe.make_dims(n, D, 1, 1, I, act="bf16", w="mxfp4", out="f32", layout="packed")
+        out = torch.empty(n, D, device="cuda")
+        offsets = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+        moe.moe_grouped_ffn(d, x[T - n:], None, None, offsets, *img, None, None, None, out, moe.workspace(d))
+        res.append(out[-200:].clone())
+        del out
+    assert torch.equal(res[0], res[1]) and res[0].abs().max() > 0.1
