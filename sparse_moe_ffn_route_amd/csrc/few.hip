@@ -96,9 +96,10 @@ __global__ __launch_bounds__(kThreads, 2) void few_gate_up_kernel(FewLayer p) {
     gate_up_units<SH, PACKED, XLDS, true>(p, q, xs, red, units * b / p.shared_blocks, units * (b + 1) / p.shared_blocks);
     return;
   }
-  if constexpr (XLDS) stage_x<W>(p, xs);
   const int b = blockIdx.x - p.shared_blocks, blocks = gridDim.x - p.shared_blocks;
-  route_call<16, kDownMembers>(q, lds, p, b == blocks - 1);
+  route_call<16, kDownMembers>(q, lds, p, b == blocks - 1, [&] {
+    if constexpr (XLDS) stage_x<W>(p, xs);
+  });
   const int units = __builtin_amdgcn_readfirstlane(q.entries) * (p.I / 16);
   gate_up_units<W, PACKED, XLDS, false>(p, q, xs, red, static_cast<int>(static_cast<int64_t>(units) * b / blocks),
                                         static_cast<int>(static_cast<int64_t>(units) * (b + 1) / blocks));

@@ -116,51 +116,43 @@ struct Route {
   u32 sums[kWaves];
   int entries;
 };
-// Scratch of route_call, at the start of the dynamic LDS (the reductions' place later): selection
-// candidates, then two words per local expert.
+// Scratch of route_call, at the start of the dynamic LDS (the reductions' place later): two words per
+// local expert.
 constexpr size_t kRouteScratch = 2 * 1024 * sizeof(u32);
+
+// A key's place among keys, in its 16 highest bits: larger for larger keys, equal for both zeros.
+__device__ __forceinline__ u32 key_place(float k) {
+  const u32 b = __float_as_uint(k + 0.0f);
+  return (b & 0x80000000u ? ~b : b | 0x80000000u) >> 16;
+}
 
 // Top-k of one token by one wave: the same keys, order and weights as select_topk (topk.hpp), in
 // about a fifth of its time for 512 keys.  The k-th largest of the lanes' own best keys bounds the
-// k-th largest of all from below; the keys that reach it (a few more than k) are ranked against
-// each other.  More than 64 of them (many equal keys) take select_topk.
+// k-th largest of all from below, and so does what its 16 highest bits say, which 16 counts over the
+// lanes find; the keys that reach it (a few more than k) are ranked against each other.  More than 64
+// of them (many equal keys) take select_topk.
 template <int PL>
 __device__ __forceinline__ void select_few(const float (&key)[PL], int E, int k, int renormalize,
                                            float2* __restrict__ cand, int32_t* __restrict__ out) {
   const int lane = threadIdx.x % kWave;
-  float bk = -INFINITY;
-  int bi = 0x7FFFFFFF;
+  u32 best = 0;  // below every key's place
   bool nan = false;
 #pragma unroll
   for (int i = 0; i < PL; ++i) {
-    const int e = lane + i * kWave;
     nan |= key[i] != key[i];
-    if (e < E && key_before(key[i], e, bk, bi)) {
-      bk = key[i];
-      bi = e;
-    }
+    if (lane + i * kWave < E) best = max(best, key_place(key[i]));
   }
-  int rank = 0;
-#pragma unroll 4
-  for (int j = 0; j < kWave; ++j) {
-    const float ok = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(bk), j));
-    const int oi = __builtin_amdgcn_readlane(bi, j);
-    rank += key_before(ok, oi, bk, bi) ? 1 : 0;
-  }
-  // lanes without a key come last; k <= E lanes or more have one, or every key is a candidate
-  const uint64_t at = __ballot(rank == k - 1 && bi < E);
-  float lk = -INFINITY;
-  int li = 0x7FFFFFFF;
-  if (at) {
-    const int l = __ffsll(static_cast<unsigned long long>(at)) - 1;
-    lk = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(bk), l));
-    li = __builtin_amdgcn_readlane(bi, l);
+  u32 least = 0;  // min(E, 64) >= k lanes have a key, so at least k reach it
+#pragma unroll
+  for (int bit = 15; bit >= 0; --bit) {
+    const u32 at = least | 1u << bit;
+    if (__popcll(__ballot(best >= at)) >= k) least = at;
   }
   int n = 0;
 #pragma unroll
   for (int i = 0; i < PL; ++i) {
     const int e = lane + i * kWave;
-    const bool on = e < E && !key_before(lk, li, key[i], e);
+    const bool on = e < E && key_place(key[i]) >= least;
     const uint64_t b = __ballot(on);
     const int pos = n + __popcll(b & ((1ull << lane) - 1));
     if (on && pos < kWave) cand[pos] = make_float2(key[i], __int_as_float(e));
@@ -204,45 +196,57 @@ __device__ __forceinline__ void select_few(const float (&key)[PL], int E, int k,
   }
 }
 
-template <int PL>
-__device__ __forceinline__ void select_all(Route& q, float2* cand, const FewLayer& p) {
-  const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
-  for (int t = wave; t < p.T; t += kWaves) {
-    float key[PL];
+// Every wave's tokens; `beside` runs between the loads of their logits and the selection.
+template <int PL, typename F>
+__device__ __forceinline__ void select_all(Route& q, const FewLayer& p, const F& beside) {
+  constexpr int N = kFewMaxT / kWaves;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), lane = threadIdx.x % kWave;
+  float key[N][PL], bias[PL];
+#pragma unroll
+  for (int i = 0; i < PL; ++i) {
+    const int e = min(lane + i * kWave, p.E - 1);
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+      key[n][i] = p.logits[static_cast<int64_t>(min(wave + n * kWaves, p.T - 1)) * p.E + e];
+    bias[i] = p.bias ? p.bias[e] : 0.0f;
+  }
+  beside();
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    const int t = wave + n * kWaves;
+    if (t >= p.T) break;
 #pragma unroll
     for (int i = 0; i < PL; ++i) {
-      const int e = lane + i * kWave;
-      key[i] = e < p.E ? p.logits[static_cast<int64_t>(t) * p.E + e] : -INFINITY;
+      key[n][i] = lane + i * kWave < p.E ? key[n][i] : -INFINITY;
+      if (p.bias) key[n][i] = key[n][i] + bias[i];
     }
-    if (p.bias) {
-#pragma unroll
-      for (int i = 0; i < PL; ++i) {
-        const int e = lane + i * kWave;
-        if (e < p.E) key[i] = key[i] + p.bias[e];
-      }
-    }
-    select_few(key, p.E, p.k, p.renormalize, cand + wave * kWave, q.blob + t * 2 * p.k);
+    select_few(key[n], p.E, p.k, p.renormalize, reinterpret_cast<float2*>(q.entry) + wave * kWave, q.blob + t * 2 * p.k);
   }
 }
 
 // The call's routing by all threads: given, or selected from the logits; then the experts it names,
 // in the order of the first pairs that do, as entries of up to LIMIT members.  The workgroup
 // with `write` set also writes the down kernel's entries (of up to DOWN_LIMIT), the blob and the
-// error word.
-template <int LIMIT, int DOWN_LIMIT>
-__device__ __forceinline__ void route_call(Route& q, uint8_t* scratch, const FewLayer& p, bool write) {
-  static_assert(kRouteScratch >= kWaves * kWave * sizeof(float2), "selection scratch");
+// error word.  `beside`, work that needs no routing, runs while the logits are on their way.
+template <int LIMIT, int DOWN_LIMIT, typename F>
+__device__ __forceinline__ void route_call(Route& q, uint8_t* scratch, const FewLayer& p, bool write, const F& beside) {
+  static_assert(sizeof(q.entry) >= kWaves * kWave * sizeof(float2), "selection candidates");
   static_assert(kThreads >= kMaxPairs, "one pair per thread");
   int32_t* first = reinterpret_cast<int32_t*>(scratch);  // first pair that names each expert, then its first row
   u32* mask = reinterpret_cast<u32*>(scratch) + 1024;    // its tokens
+  for (int e = threadIdx.x; e < p.n_local; e += kThreads) {
+    first[e] = 0x7FFFFFFF;
+    mask[e] = 0u;
+  }
   if (p.packed_in) {
     for (int i = threadIdx.x; i < p.T * 2 * p.k; i += kThreads) q.blob[i] = p.packed_in[i];
+    beside();
   } else if (p.E <= 2 * kWave) {
-    select_all<2>(q, reinterpret_cast<float2*>(scratch), p);
+    select_all<2>(q, p, beside);
   } else if (p.E <= 8 * kWave) {
-    select_all<8>(q, reinterpret_cast<float2*>(scratch), p);
+    select_all<8>(q, p, beside);
   } else {
-    select_all<kMaxKeysPerLane>(q, reinterpret_cast<float2*>(scratch), p);
+    select_all<kMaxKeysPerLane>(q, p, beside);
   }
   wait_vmcnt<0>();  // loads of x straight into LDS are complete, too
   __syncthreads();
@@ -266,11 +270,6 @@ __device__ __forceinline__ void route_call(Route& q, uint8_t* scratch, const Few
       }
     }
   }
-  if (e >= 0) {
-    first[e] = 0x7FFFFFFF;
-    mask[e] = 0u;
-  }
-  __syncthreads();
   if (e >= 0) {
     atomicMin(&first[e], i);
     atomicOr(&mask[e], 1u << t);

@@ -258,9 +258,10 @@ __global__ __launch_bounds__(kThreads, 2) void few_mx_gate_up_kernel(FewLayer p)
     gate_up_units<EL_BF16, true, XLDS, true>(p, q, xs, red, units * b / p.shared_blocks, units * (b + 1) / p.shared_blocks);
     return;
   }
-  if constexpr (XLDS) make_terms(p, xs, 0, 1);
   const int b = blockIdx.x - p.shared_blocks, blocks = gridDim.x - p.shared_blocks;
-  route_call<kGateMembers, kHMembers>(q, lds, p, b == blocks - 1);
+  route_call<kGateMembers, kHMembers>(q, lds, p, b == blocks - 1, [&] {
+    if constexpr (XLDS) make_terms(p, xs, 0, 1);
+  });
   const int units = __builtin_amdgcn_readfirstlane(q.entries) * (p.I / kUnit);
   mx_gate_up_units<XLDS>(p, q, XLDS ? xs : static_cast<uint8_t*>(p.x_terms), red,
                          static_cast<int>(static_cast<int64_t>(units) * b / blocks),
