@@ -37,12 +37,14 @@ __device__ __forceinline__ int term_scale(u32 amax_bits) {
   return b < 17 ? 17 : b;
 }
 
+// BYTE: of both scale registers.
+template <int BYTE = 0>
 __device__ __forceinline__ f32x4 mx_mul(const u32x4& a, const u32x4& b0, const u32x4& b1, f32x4 c, u32 sa, u32 sb) {
   const u32x4 z = {0u, 0u, 0u, 0u};
   const i32x8 av = __builtin_bit_cast(i32x8, __builtin_shufflevector(a, z, 0, 1, 2, 3, 4, 5, 6, 7));
   const i32x8 bv = __builtin_bit_cast(i32x8, __builtin_shufflevector(b0, b1, 0, 1, 2, 3, 4, 5, 6, 7));
-  // A: fp4 (format 4); B: e4m3 (format 0); byte 0 of the scale registers
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(av, bv, c, 4, 0, 0, static_cast<int>(sa), 0,
+  // A: fp4 (format 4); B: e4m3 (format 0)
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(av, bv, c, 4, 0, BYTE, static_cast<int>(sa), BYTE,
                                                           static_cast<int>(sb));
 }
 
@@ -116,9 +118,11 @@ __global__ __launch_bounds__(kThreads) void few_terms_kernel(FewLayer p) {
 // gate/up
 // ---------------------------------------------------------------------------
 
-// Rows of h: [T * k][term] of whole steps' bytes, then a scale byte per row, term and block.
+// Rows of h: [T * k][term] of whole steps' bytes, then a scale byte per row, term and block, 16 per group
+// of 512 values: for each lane group the dword of its four steps.
 __host__ __device__ constexpr int ht_row(int I) { return mx_steps(I) * kMxStep; }
-__host__ __device__ constexpr int ht_blocks(int I) { return mx_steps(I) * 4; }
+__host__ __device__ constexpr int ht_blocks(int I) { return mx_groups(I) * 16; }
+__host__ __device__ constexpr int ht_scale(int blk) { return (blk & ~15) + (blk & 3) * 4 + ((blk >> 2) & 3); }
 
 constexpr int kGateMembers = 8;  // per entry: columns 8 to 15 are the second terms
 constexpr int kHMembers = 4;     // per entry of the down kernel: four terms
@@ -232,7 +236,9 @@ __device__ __forceinline__ void mx_gate_up_units(const FewLayer& p, const Route&
         const u32 code = f32x2_to_e4m3x2(rest, 0.0f);
         out[r * hrow + (u % per) * kUnit + ch] = static_cast<uint8_t>(code);
         rest = (rest - e4m3_lo(code)) * 32.0f;
-        if (ch == 0) out_sc[r * hblocks + u % per] = static_cast<uint8_t>(b == 255 ? 255 : b - i * kTermStep);
+        if (ch == 0) out_sc[r * hblocks + ht_scale(u % per)] = static_cast<uint8_t>(b == 255 ? 255 : b - i * kTermStep);
+        // the two blocks that fill the last step have no codes, and a scale that is no NaN
+        else if (ch <= 2 && u % per == per - 1 && (p.I & 64)) out_sc[r * hblocks + ht_scale(per - 1 + ch)] = 127;
       }
     }
     if (p.red_bufs == 2) buf = buf == red ? red + 2 * part : red;
@@ -272,9 +278,9 @@ __global__ __launch_bounds__(kThreads, 2) void few_mx_gate_up_kernel(FewLayer p)
 // down
 // ---------------------------------------------------------------------------
 
-// As down_blocks (few.hpp): entries of up to four members, whose four terms are the columns 4 i + member.
+// As down_blocks (few.hpp), a block being a group of four steps: entries of up to four members, whose four terms are the columns 4 i + member.
 __device__ __forceinline__ f32x4 mx_down_blocks(const FewLayer& p, int entries, int frag, int first, int stride) {
-  constexpr int B = 4, NBUF = 3;
+  constexpr int B = kMxGroup / kMxStep, NBUF = 3;
   const int lane = threadIdx.x % kWave, lrow = lane & 15, lgrp = lane >> 4;
   const int S = mx_steps(p.I), nb = (S + B - 1) / B;
   const int blocks = entries * nb;
@@ -287,7 +293,7 @@ __device__ __forceinline__ f32x4 mx_down_blocks(const FewLayer& p, int entries, 
   auto entry = [&](const Cursor& at) { return make_int2(ld_scalar(&p.entry[at.hi].x), ld_scalar(&p.entry[at.hi].y)); };
   struct Block {
     u32x4 w[B], h[B][2];
-    u32 sc[B], hs[B];
+    u32 sc, hs;  // byte n: step n
   };
   auto load = [&](Block& b, Cursor& at) {
     const bool there = at.left > 0;
@@ -298,18 +304,18 @@ __device__ __forceinline__ f32x4 mx_down_blocks(const FewLayer& p, int entries, 
         weight_rsrc(static_cast<const uint8_t*>(p.w_down) + static_cast<int64_t>(entry_expert(en)) * p.dn_stride);
     const bool on = there && c < entry_members(en, kHMembers);
     const u32 rt = static_cast<u32>(entry_row(en) + c) * kTerms + term;
+    b.sc = __builtin_amdgcn_raw_buffer_load_b32(r, there ? lane * 4 : kOutOfRange,
+                                                frag_at + j * kMxGroupBytes + min(B, S - B * j) * kMxRun, 0);
+    b.hs = __builtin_amdgcn_raw_buffer_load_b32(rh, on ? codes + rt * hblocks + j * 16 + lgrp * 4 : kOutOfRange, 0, 0);
 #pragma unroll
     for (int n = 0; n < B; ++n) {
       const int s = j * B + n, k0 = s * kMxStep;
       const bool real = there && s < S;
       b.w[n] = buffer_load16<true>(r, real ? lane * 16 : kOutOfRange, run_offset(frag_at, s));
-      b.sc[n] = __builtin_amdgcn_raw_buffer_load_b8(r, real ? lane * 4 : kOutOfRange, byte_offset(frag_at, s, S), 0);
       // lanes without a member, or past the width, read nothing: zeros
       const u32 at = rt * hrow + k0 + lgrp * 16;
       b.h[n][0] = buffer_load16<false>(rh, on && k0 < p.I ? at : kOutOfRange, 0);
       b.h[n][1] = buffer_load16<false>(rh, on && k0 + 64 < p.I ? at + 64 : kOutOfRange, 0);
-      b.hs[n] = __builtin_amdgcn_raw_buffer_load_b8(
-          rh, on && k0 + lgrp * 32 < p.I ? codes + rt * hblocks + s * 4 + lgrp : kOutOfRange, 0, 0);
     }
   };
   f32x4 acc = {0.f, 0.f, 0.f, 0.f};
@@ -318,9 +324,10 @@ __device__ __forceinline__ f32x4 mx_down_blocks(const FewLayer& p, int entries, 
     const int2 en = entry(at);
     const int j = at.lo;
     at.next();
-#pragma unroll
-    for (int n = 0; n < B; ++n)
-      if (j * B + n < S) v = mx_mul(b.w[n], b.h[n][0], b.h[n][1], v, b.sc[n], b.hs[n]);
+    v = mx_mul<0>(b.w[0], b.h[0][0], b.h[0][1], v, b.sc, b.hs);
+    if (j * B + 1 < S) v = mx_mul<1>(b.w[1], b.h[1][0], b.h[1][1], v, b.sc, b.hs);
+    if (j * B + 2 < S) v = mx_mul<2>(b.w[2], b.h[2][0], b.h[2][1], v, b.sc, b.hs);
+    if (j * B + 3 < S) v = mx_mul<3>(b.w[3], b.h[3][0], b.h[3][1], v, b.sc, b.hs);
 #pragma unroll
     for (int n = 0; n < 4; ++n) v[n] = dpp_add<kRor4>(dpp_add<kRor8>(v[n]));
     acc += to_tokens(v, en, kHMembers);
@@ -357,7 +364,7 @@ __global__ __launch_bounds__(kThreads, 2) void few_mx_down_kernel(FewLayer p) {
 
 size_t few_mx_x_bytes(int T, int D) { return static_cast<size_t>(xt_bytes(T, D)); }
 size_t few_mx_h_bytes(int T, int k, int I) {
-  return static_cast<size_t>(T) * k * kTerms * (ht_row(I) + ht_blocks(I));
+  return static_cast<size_t>(T) * k * kTerms * (ht_row(I) + ht_blocks(I));  // a multiple of 16 bytes
 }
 
 hipError_t launch_few_mx(FewLayer p, hipStream_t stream) {
