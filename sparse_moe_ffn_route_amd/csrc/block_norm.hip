@@ -17,29 +17,30 @@ namespace moe {
 
 namespace {
 
-// V consecutive values as float (V = 8: 16-byte accesses; V = 1: any alignment).
+// V consecutive values as stored (V = 8: 16-byte accesses; V = 1: any alignment).
 template <int EL, int V>
-__device__ __forceinline__ void load_v(const void* base, int64_t idx, float (&v)[V]) {
-  if constexpr (V == 1) {
-    v[0] = EL == EL_F32 ? static_cast<const float*>(base)[idx]
-                        : bf16_bits_to_f32(static_cast<const uint16_t*>(base)[idx]);
-  } else if constexpr (EL == EL_F32) {
-    const u32x4* p = reinterpret_cast<const u32x4*>(static_cast<const float*>(base) + idx);
-    const u32x4 a = p[0], b = p[1];
+struct Chunk {
+  static constexpr int kWords = V == 1 ? 1 : EL == EL_F32 ? 8 : 4;
+  uint32_t w[kWords];
+
+  __device__ __forceinline__ void load(const void* base, int64_t idx) {
+    if constexpr (V == 1) {
+      w[0] = EL == EL_F32 ? static_cast<const uint32_t*>(base)[idx] : static_cast<const uint16_t*>(base)[idx];
+    } else {
+      const u32x4* p = reinterpret_cast<const u32x4*>(static_cast<const uint8_t*>(base) + idx * (EL == EL_F32 ? 4 : 2));
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[i] = __uint_as_float(a[i]);
-      v[4 + i] = __uint_as_float(b[i]);
-    }
-  } else {
-    const u32x4 a = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(base) + idx);
+      for (int i = 0; i < kWords / 4; ++i) {
+        const u32x4 a = p[i];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[2 * i] = bf16_bits_to_f32(a[i] & 0xFFFFu);
-      v[2 * i + 1] = __uint_as_float(a[i] & 0xFFFF0000u);
+        for (int j = 0; j < 4; ++j) w[4 * i + j] = a[j];
+      }
     }
   }
-}
+  __device__ __forceinline__ float operator[](int i) const {
+    if constexpr (EL == EL_F32) return __uint_as_float(w[i]);
+    else return i % 2 == 0 ? bf16_bits_to_f32(w[i / 2] & 0xFFFFu) : __uint_as_float(w[i / 2] & 0xFFFF0000u);
+  }
+};
 
 template <int EL, int V>
 __device__ __forceinline__ void store_v(void* base, int64_t idx, const float (&v)[V]) {
@@ -72,50 +73,58 @@ __device__ __forceinline__ float block_sum(float v, float* red) {
 template <int EL, int YEL, int V, int NC>
 __global__ __launch_bounds__(kThreads) void block_norm_kernel(BlockNorm p) {
   __shared__ float red[2][kThreads / kWave];
+  // Short rows: weights and gate are requested with the row, so that a call of few rows waits for
+  // memory once rather than after each sum; longer rows keep the registers.
+  constexpr bool kEarly = NC * V <= 16;
   const int64_t row = blockIdx.x;
   const int64_t base = row * p.D;
-  float r[NC][V];
+  const bool gated = p.gate_kind >= kGateChannel;
+  Chunk<YEL, V> yc[NC];
+  Chunk<EL, V> rc[NC], wp[kEarly ? NC : 1], g[kEarly ? NC : 1], wn[kEarly ? NC : 1];
+  auto load_post = [&](int c, int d) {
+    if (p.w_post) wp[kEarly ? c : 0].load(p.w_post, d);
+    if (gated) g[kEarly ? c : 0].load(p.gate, p.gate_kind == kGateChannel ? d : base + d);
+  };
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
     const int d = (c * kThreads + threadIdx.x) * V;
-    if (d < p.D) load_v<EL, V>(p.r, base + d, r[c]);
+    if (d >= p.D) continue;
+    rc[c].load(p.r, base + d);
+    if (p.y) {
+      yc[c].load(p.y, base + d);
+      if constexpr (kEarly) load_post(c, d);
+    }
+    if (kEarly && p.w_next) wn[kEarly ? c : 0].load(p.w_next, d);
   }
+  float r[NC][V];
+#pragma unroll
+  for (int c = 0; c < NC; ++c)
+#pragma unroll
+    for (int i = 0; i < V; ++i) r[c][i] = rc[c][i];
   if (p.y) {
-    float y[NC][V];
     float ss = 0.f;
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
       const int d = (c * kThreads + threadIdx.x) * V;
-      if (d < p.D) {
-        load_v<YEL, V>(p.y, base + d, y[c]);
+      if (d < p.D)
 #pragma unroll
-        for (int i = 0; i < V; ++i) ss = fmaf(y[c][i], y[c][i], ss);
-      }
+        for (int i = 0; i < V; ++i) ss = fmaf(yc[c][i], yc[c][i], ss);
     }
     float rs = 1.0f;
     if (p.w_post) rs = 1.0f / sqrtf(block_sum(ss, red[0]) / p.D + p.eps);
     const float gt = p.gate_kind == kGateToken ? static_cast<const float*>(p.gate)[row] : 1.0f;
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-      const int d = (c * kThreads + threadIdx.x) * V;
+      const int d = (c * kThreads + threadIdx.x) * V, w = kEarly ? c : 0;
       if (d >= p.D) continue;
-      if (p.w_post) {
-        float w[V];
-        load_v<EL, V>(p.w_post, d, w);
+      if constexpr (!kEarly) load_post(c, d);
+      float z[V];
 #pragma unroll
-        for (int i = 0; i < V; ++i) y[c][i] = y[c][i] * rs * w[i];
-      }
-      if (p.gate_kind >= kGateChannel) {
-        float g[V];
-        load_v<EL, V>(p.gate, p.gate_kind == kGateChannel ? d : base + d, g);
+      for (int i = 0; i < V; ++i) z[i] = p.w_post ? yc[c][i] * rs * wp[w][i] : yc[c][i];
 #pragma unroll
-        for (int i = 0; i < V; ++i) y[c][i] *= g[i];
-      } else {
+      for (int i = 0; i < V; ++i) z[i] *= gated ? g[w][i] : gt;
 #pragma unroll
-        for (int i = 0; i < V; ++i) y[c][i] *= gt;
-      }
-#pragma unroll
-      for (int i = 0; i < V; ++i) r[c][i] = fmaf(p.res_scale, r[c][i], y[c][i]);
+      for (int i = 0; i < V; ++i) r[c][i] = fmaf(p.res_scale, r[c][i], z[i]);
       store_v<EL, V>(p.r_out, base + d, r[c]);
     }
   }
@@ -131,12 +140,12 @@ __global__ __launch_bounds__(kThreads) void block_norm_kernel(BlockNorm p) {
     const float rs = 1.0f / sqrtf(block_sum(ss, red[1]) / p.D + p.eps);
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-      const int d = (c * kThreads + threadIdx.x) * V;
+      const int d = (c * kThreads + threadIdx.x) * V, w = kEarly ? c : 0;
       if (d >= p.D) continue;
-      float w[V], o[V];
-      load_v<EL, V>(p.w_next, d, w);
+      if constexpr (!kEarly) wn[0].load(p.w_next, d);
+      float o[V];
 #pragma unroll
-      for (int i = 0; i < V; ++i) o[i] = r[c][i] * rs * w[i];
+      for (int i = 0; i < V; ++i) o[i] = r[c][i] * rs * wn[w][i];
       store_v<EL, V>(p.x_next, base + d, o);
     }
   }
