@@ -406,7 +406,7 @@ int moe_block_norm(int32_t T, int32_t D, int32_t act_dtype, int32_t y_dtype, con
  *       MOE_FEW_MAX_T tokens), else moe_layer_forward, rounded to out_dtype;
  *   r_out, x_next as moe_block_norm(n, y, r).
  *
- *   w_in, x_in   exactly one of them is given: w_in [D], x_in [T][D], act_dtype
+ *   w_in, x_in   exactly one of them is given: w_in [D], x_in [T][D] (as the layer's x), act_dtype
  *   r, r_out, x_next  act_dtype, as in moe_block_norm
  *   ws           at least moe_block_workspace_bytes(dims) bytes (0 for invalid dims); the layer's
  *                workspace, error word included, is its first part

@@ -368,6 +368,33 @@ int check_layer_args(const moe_dims& d, const moe_weights* w, const void* x, con
   return MOE_OK;
 }
 
+// The few-token layer.  norm_r given: x is made of it first, rms(norm_r) * norm_w.
+int few_layer(const moe_dims& d, const Layout& L, const moe_weights* w, const void* x, const int32_t* packed_in,
+              const float* logit_bias, void* y, float* logits_out, int32_t* packed_out, void* ws, const void* norm_r,
+              const void* norm_w, float norm_eps, hipStream_t stream) {
+  if (!aligned16(x, ws, packed_in ? nullptr : w->w_router, w->w_gate, w->w_up, w->w_down,
+                 d.I_shared ? w->sh_gate : nullptr, d.I_shared ? w->sh_up : nullptr, d.I_shared ? w->sh_down : nullptr))
+    return MOE_ERR_UNSUPPORTED;
+  const bool mx = d.w_dtype == MOE_MXFP4;
+  const int64_t es = d.w_dtype == MOE_F32 ? 4 : d.w_dtype == MOE_BF16 ? 2 : 1;
+  FewLayer p{};
+  p.x = x; p.w_router = w->w_router; p.bias = logit_bias; p.packed_in = packed_in;
+  p.logits = logits_out ? logits_out : at<float>(ws, L.logits);
+  p.norm_r = norm_r; p.norm_w = norm_w; p.norm_x = const_cast<void*>(x); p.norm_eps = norm_eps;
+  p.packed_out = packed_out; p.err = at<int32_t>(ws, L.err);
+  p.entries = at<int32_t>(ws, L.few_entries); p.entry = at<int2>(ws, L.few_entries) + 1;
+  p.x_terms = at<void>(ws, L.few_xt);
+  p.w_gate = w->w_gate; p.w_up = w->w_up; p.w_down = w->w_down;
+  p.s_gate = w->s_gate; p.s_up = w->s_up; p.s_down = w->s_down;
+  p.sh_gate = w->sh_gate; p.sh_up = w->sh_up; p.sh_down = w->sh_down;
+  p.gu_stride = mx ? d.I / 16 * mx_fragment_bytes(d.D) : static_cast<int64_t>(d.I) * d.D * es;
+  p.dn_stride = mx ? d.D / 16 * mx_fragment_bytes(d.I) : static_cast<int64_t>(d.I) * d.D * es;
+  p.h = at<void>(ws, L.few_h); p.h_sh = at<void>(ws, L.few_h_sh); p.y = y;
+  p.T = d.T; p.D = d.D; p.E = d.E; p.k = d.top_k; p.I = d.I; p.I_shared = d.I_shared; p.e_begin = d.expert_begin;
+  p.n_local = d.n_local; p.renormalize = d.renormalize; p.out_el = d.out_dtype;
+  return hip_status(launch_few_layer(d.w_dtype, d.weight_layout == MOE_LAYOUT_PACKED, p, stream));
+}
+
 // Sizes of 4-bit weight matrices: the kernels address one matrix with 32-bit offsets, and a launch
 // has one workgroup per four (16-row, 512-value) pieces.
 int mx_check(int64_t n_mats, int32_t rows, int32_t cols) {
@@ -644,36 +671,17 @@ int moe_mx_unpack_weights(int32_t dst_dtype, int64_t n_mats, int32_t rows, int32
 int moe_layer_forward_few(const moe_dims* dims, const moe_weights* w, const void* x, const int32_t* packed_in,
                           const float* logit_bias, void* y, float* logits_out, int32_t* packed_out, void* ws,
                           size_t ws_bytes, void* stream) {
-  int st = check_dims(dims);
+  const int st = check_dims(dims);
   if (st != MOE_OK) return st;
   const moe_dims& d = *dims;
   if (!is_few(d)) return MOE_ERR_UNSUPPORTED;
-  st = check_layer_args(d, w, x, packed_in, y, ws);
-  if (st != MOE_OK) return st;
+  const int ast = check_layer_args(d, w, x, packed_in, y, ws);
+  if (ast != MOE_OK) return ast;
   const Layout L = layout(d);
   if (ws_bytes < L.total) return MOE_ERR_WORKSPACE;
   if (d.T == 0) return MOE_OK;
-  if (!aligned16(x, ws, packed_in ? nullptr : w->w_router, w->w_gate, w->w_up, w->w_down,
-                 d.I_shared ? w->sh_gate : nullptr, d.I_shared ? w->sh_up : nullptr, d.I_shared ? w->sh_down : nullptr))
-    return MOE_ERR_UNSUPPORTED;
-  const bool mx = d.w_dtype == MOE_MXFP4;
-  const int64_t es = d.w_dtype == MOE_F32 ? 4 : d.w_dtype == MOE_BF16 ? 2 : 1;
-  FewLayer p{};
-  p.x = x; p.w_router = w->w_router; p.bias = logit_bias; p.packed_in = packed_in;
-  p.logits = logits_out ? logits_out : at<float>(ws, L.logits);
-  p.packed_out = packed_out; p.err = at<int32_t>(ws, L.err);
-  p.entries = at<int32_t>(ws, L.few_entries); p.entry = at<int2>(ws, L.few_entries) + 1;
-  p.x_terms = at<void>(ws, L.few_xt);
-  p.w_gate = w->w_gate; p.w_up = w->w_up; p.w_down = w->w_down;
-  p.s_gate = w->s_gate; p.s_up = w->s_up; p.s_down = w->s_down;
-  p.sh_gate = w->sh_gate; p.sh_up = w->sh_up; p.sh_down = w->sh_down;
-  p.gu_stride = mx ? d.I / 16 * mx_fragment_bytes(d.D) : static_cast<int64_t>(d.I) * d.D * es;
-  p.dn_stride = mx ? d.D / 16 * mx_fragment_bytes(d.I) : static_cast<int64_t>(d.I) * d.D * es;
-  p.h = at<void>(ws, L.few_h); p.h_sh = at<void>(ws, L.few_h_sh); p.y = y;
-  p.T = d.T; p.D = d.D; p.E = d.E; p.k = d.top_k; p.I = d.I; p.I_shared = d.I_shared; p.e_begin = d.expert_begin;
-  p.n_local = d.n_local; p.renormalize = d.renormalize; p.out_el = d.out_dtype;
-  return hip_status(launch_few_layer(d.w_dtype, d.weight_layout == MOE_LAYOUT_PACKED, p,
-                                     static_cast<hipStream_t>(stream)));
+  return few_layer(d, L, w, x, packed_in, logit_bias, y, logits_out, packed_out, ws, nullptr, nullptr, 0.0f,
+                   static_cast<hipStream_t>(stream));
 }
 
 int moe_block_norm(int32_t T, int32_t D, int32_t act_dtype, int32_t y_dtype, const moe_norm* n, const void* y,
@@ -708,18 +716,19 @@ int moe_block_forward(const moe_dims* dims, const moe_weights* weights, const vo
   if (st != MOE_OK) return st;
   if (ws_bytes < B.total) return MOE_ERR_WORKSPACE;
   if (d.T == 0) return MOE_OK;
-  const void* x = x_in;
-  if (w_in) {
+  const void* x = x_in ? x_in : at<void>(ws, B.x);
+  // few tokens: entering is part of the layer's first launch
+  const bool few = is_few(d), fused = few && w_in && aligned16(r, w_in);
+  if (w_in && !fused) {
     moe_norm enter{};
     enter.w_next = w_in;
     enter.eps = n->eps;
-    x = at<void>(ws, B.x);
     st = moe_block_norm(d.T, d.D, d.act_dtype, d.act_dtype, &enter, nullptr, r, nullptr, at<void>(ws, B.x), stream);
     if (st != MOE_OK) return st;
   }
-  st = is_few(d) ? moe_layer_forward_few(dims, weights, x, nullptr, logit_bias, y, nullptr, nullptr, ws, B.y, stream)
-                 : moe_layer_forward(dims, weights, x, nullptr, logit_bias, y, nullptr, nullptr, ws, B.y, nullptr,
-                                     stream);
+  st = few ? few_layer(d, layout(d), weights, x, nullptr, logit_bias, y, nullptr, nullptr, ws, fused ? r : nullptr,
+                       fused ? w_in : nullptr, n->eps, static_cast<hipStream_t>(stream))
+           : moe_layer_forward(dims, weights, x, nullptr, logit_bias, y, nullptr, nullptr, ws, B.y, nullptr, stream);
   if (st != MOE_OK) return st;
   return moe_block_norm(d.T, d.D, d.act_dtype, d.out_dtype, n, y, r, r_out, x_next, stream);
 }

@@ -158,6 +158,11 @@ struct FewLayer {
   void* y;                   // [T][D] of out_el
   int T, D, E, k, I, I_shared, e_begin, n_local, renormalize, out_el;
   void* x_terms;             // 4-bit weights: scratch of few_mx_x_bytes(T, D); h: few_mx_h_bytes(T, k, I)
+  // x = rms(norm_r) * norm_w, to be written to norm_x (= x); norm_r NULL: x is there.  Selected routing only.
+  const void* norm_r;
+  const void* norm_w;
+  void* norm_x;
+  float norm_eps;
   int shared_blocks, shared_waves, red_bufs, red_bytes, shared_red_bufs;  // set by the launchers
 };
 size_t few_mx_x_bytes(int T, int D);

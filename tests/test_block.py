@@ -269,6 +269,30 @@ def test_block_forward_is_its_three_calls():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("T,D,E,k,w,off", [(1, 64, 4, 1, "bf16", 0), (16, 4160, 70, 3, "bf16", 0), (7, 8192, 5, 2, "f32", 0),
+                                           (16, 2048, 600, 4, "f32", 0), (3, 320, 12, 3, "bf16", 1), (3, 320, 12, 3, "f32", 1)])
+def test_entering_inside_the_layer(T, D, E, k, w, off):
+    """Few tokens enter in the layer's first launch (or, off a 16-byte boundary, before it): the same bits as the
+    three calls, in place as well."""
+    rng = np.random.default_rng(D)
+    layer = Layer(rng, D, E, E, 64, 0, w)
+    wts = layer.on_gpu(True)
+    flat = torch.from_numpy(rng.standard_normal(T * D + 8).astype(np.float32)).to(layer.f).cuda()
+    r = flat[off:off + T * D].view(T, D)
+    wi = torch.from_numpy((1 + 0.1 * rng.standard_normal(D)).astype(np.float32)).to(layer.f).cuda()
+    d = moe.make_dims(T, D, E, k, 64, 0, 0, E, True, w, w, w, "packed")
+    r1, x1 = torch.empty(T, D, dtype=layer.f, device="cuda"), torch.empty(T, D, dtype=layer.f, device="cuda")
+    moe.moe_block_forward(d, wts, r, r1, w_in=wi, w_post=wi, eps=1e-3, w_next=wi, x_next=x1, ws=moe.block_workspace(d))
+    x, y, r2, x2 = (torch.empty_like(r1) for _ in range(4))
+    moe.moe_block_norm(None, r, w_next=wi, x_next=x, eps=1e-3)
+    moe.moe_layer_forward_few(d, wts, x, None, None, y, ws=moe.workspace(d))
+    moe.moe_block_norm(y, r, r2, w_post=wi, w_next=wi, x_next=x2, eps=1e-3)
+    assert torch.equal(r1, r2) and torch.equal(x1, x2)
+    moe.moe_block_forward(d, wts, r, r, w_in=wi, w_post=wi, eps=1e-3, ws=moe.block_workspace(d))
+    assert torch.equal(r, r2)
+
+
+@pytest.mark.gpu
 def test_block_captured_and_replayed():
     rng = np.random.default_rng(7)
     D, E, k, I = 128, 8, 2, 64
