@@ -239,8 +239,13 @@ __device__ __forceinline__ void route_call(Route& q, uint8_t* scratch, const Few
     mask[e] = 0u;
   }
   if (p.packed_in) {
-    for (int i = threadIdx.x; i < p.T * 2 * p.k; i += kThreads) q.blob[i] = p.packed_in[i];
+    constexpr int N = 2 * kMaxPairs / kThreads;
+    int32_t v[N];
+#pragma unroll
+    for (int n = 0; n < N; ++n) v[n] = p.packed_in[min(static_cast<int>(threadIdx.x) + n * kThreads, p.T * 2 * p.k - 1)];
     beside();
+#pragma unroll
+    for (int n = 0; n < N; ++n) q.blob[threadIdx.x + n * kThreads] = v[n];
   } else if (p.E <= 2 * kWave) {
     select_all<2>(q, p, beside);
   } else if (p.E <= 8 * kWave) {
