@@ -2,7 +2,8 @@
 // records (formats in mx.hpp).
 //
 // All three are streams: pack reads 2 (bf16) or 4 (fp32) bytes and writes 17/32 byte per
-// value, unpack the reverse.
+// value, unpack the reverse.  Measured, 64 matrices of 1024 x 4096 (537 MB of bf16, 143 MB of images): pack
+// 152 us, 4.5 TB/s (a device copy reaches 4.9); unpack 107 us, 6.4 TB/s (a fill reaches 6.9).
 #include <type_traits>
 
 #include "common.hpp"
@@ -85,7 +86,8 @@ __device__ __forceinline__ void quad_transpose(u32 (&w)[4], int q) {
   }
 }
 
-// One wave per (matrix, 16 rows, group).  Lane l reads 8 values of row 4 i + l / 16 from (l % 16) * 8 on
+// One wave per (matrix, 16 rows, group).  (Reading 1 KB of one row at a time instead took 172 us against 152.)
+// Lane l reads 8 values of row 4 i + l / 16 from (l % 16) * 8 on
 // (whole lines), a block's four lanes share its magnitude, and a 4x4 transpose between them makes each
 // the holder of one block, so the codes go out as whole 1 KB runs and the scales as one 256-byte store.
 template <int EL>
