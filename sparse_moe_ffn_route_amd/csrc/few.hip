@@ -39,112 +39,9 @@ using namespace few;
 // logits
 // ---------------------------------------------------------------------------
 
-// 16 waves split the width: at D = 4096 each has all its loads (8 steps of 16 experts) in flight at
-// once, so the launch is a few memory latencies long.  (The shared expert's gate/up beside the logits, on CUs
-// that are idle here, made this launch 1.5 us longer and the next hardly shorter.)
-constexpr int kLogitWaves = 16;
-constexpr int kNormWaves = 4;  // parts of a row's sum of squares: the waves of block_norm.hip
-
-// 16 bytes as floats.
-template <int EL>
-__device__ __forceinline__ void unpack(const u32x4& a, float* v) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if constexpr (EL == EL_F32) {
-      v[i] = __uint_as_float(a[i]);
-    } else {
-      v[2 * i] = bf16_bits_to_f32(a[i] & 0xFFFFu);
-      v[2 * i + 1] = __uint_as_float(a[i] & 0xFFFF0000u);
-    }
-  }
-}
-
-
-// NORM: x = rms(r) * w_in, made here (the same arithmetic in the same order as block_norm.hip) and
-// written by the first workgroup for the launches after this one.
 template <int EL, bool NORM>
 __global__ __launch_bounds__(kLogitWaves * kWave) void few_logits_kernel(FewLayer p) {
-  __shared__ f32x4 red[kLogitWaves][kWave];
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), lane = threadIdx.x % kWave;
-  const int lrow = lane & 15, lgrp = lane >> 4;
-  const int e0 = blockIdx.x * 16;
-  constexpr int es = EL == EL_F32 ? 4 : 2;
-  const int S = p.D * es / 64;
-  const int s0 = S * wave / kLogitWaves, s1 = S * (wave + 1) / kLogitWaves;
-  const int e = min(e0 + lrow, p.E - 1), t = min(lrow, p.T - 1);
-  const uint8_t* wp = static_cast<const uint8_t*>(p.w_router) + static_cast<int64_t>(e) * p.D * es + lgrp * 16;
-  const int64_t xo = static_cast<int64_t>(t) * p.D * es + lgrp * 16;
-  const uint8_t* xp = static_cast<const uint8_t*>(NORM ? p.norm_r : p.x) + xo;
-  const uint8_t* np = static_cast<const uint8_t*>(p.norm_w) + lgrp * 16;
-  const u32x4 z = {0u, 0u, 0u, 0u};
-  f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-  constexpr int U = 8;
-  u32x4 a[U], b[U], n[NORM ? U : 1];
-  auto load_a = [&](int s) {
-#pragma unroll
-    for (int i = 0; i < U; ++i) a[i] = *reinterpret_cast<const u32x4*>(wp + static_cast<int64_t>(min(s + i, s1 - 1)) * 64);
-  };
-  if (s0 < s1) load_a(s0);
-  float inv = 1.0f;
-  if constexpr (NORM) {
-    __shared__ float sums[kFewMaxT][kNormWaves];
-    for (int j = wave; j < p.T * kNormWaves; j += kLogitWaves) {
-      const int row = j / kNormWaves, part = j % kNormWaves;
-      const uint8_t* rp = static_cast<const uint8_t*>(p.norm_r) + static_cast<int64_t>(row) * p.D * es;
-      float ss = 0.f;
-      for (int d = (part * kWave + lane) * 8; d < p.D; d += kNormWaves * kWave * 8) {
-        const u32x4* q = reinterpret_cast<const u32x4*>(rp + static_cast<int64_t>(d) * es);
-        float v[8];
-        unpack<EL>(q[0], v);
-        if constexpr (EL == EL_F32) unpack<EL>(q[1], v + 4);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) ss = fmaf(v[i], v[i], ss);
-      }
-      ss = wave_sum(ss);
-      if (lane == 0) sums[row][part] = ss;
-    }
-    __syncthreads();
-    float ss = sums[t][0];
-#pragma unroll
-    for (int i = 1; i < kNormWaves; ++i) ss += sums[t][i];
-    inv = 1.0f / sqrtf(ss / p.D + p.norm_eps);
-  }
-  for (int s = s0; s < s1; s += U) {
-    if (s != s0) load_a(s);
-#pragma unroll
-    for (int i = 0; i < U; ++i) {
-      const int q = min(s + i, s1 - 1);
-      b[i] = *reinterpret_cast<const u32x4*>(xp + static_cast<int64_t>(q) * 64);
-      if constexpr (NORM) n[i] = *reinterpret_cast<const u32x4*>(np + static_cast<int64_t>(q) * 64);
-    }
-#pragma unroll
-    for (int i = 0; i < U; ++i) {
-      if (s + i >= s1) continue;
-      if constexpr (NORM) {
-        constexpr int V = 16 / es;
-        float v[V], w[V];
-        unpack<EL>(b[i], v);
-        unpack<EL>(n[i], w);
-#pragma unroll
-        for (int j = 0; j < V; ++j) v[j] = v[j] * inv * w[j];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) b[i][j] = EL == EL_F32 ? __float_as_uint(v[j]) : bf16x2_bits(v[2 * j % V], v[(2 * j + 1) % V]);
-        if (blockIdx.x == 0 && lrow < p.T)
-          *reinterpret_cast<u32x4*>(static_cast<uint8_t*>(p.norm_x) + xo + static_cast<int64_t>(s + i) * 64) = b[i];
-      }
-      acc = mfma_chunk<EL>(a[i], lrow < p.T ? b[i] : z, acc);
-    }
-  }
-  red[wave][lane] = acc;
-  __syncthreads();
-  if (threadIdx.x < 256) {
-    const int l = threadIdx.x & 63, r = threadIdx.x >> 6;
-    float v = 0.f;
-#pragma unroll
-    for (int w = 0; w < kLogitWaves; ++w) v += red[w][l][r];
-    const int tt = l & 15, ee = e0 + (l >> 4) * 4 + r;
-    if (tt < p.T && ee < p.E) p.logits[static_cast<int64_t>(tt) * p.E + ee] = v;
-  }
+  logits_block<EL, NORM>(p, blockIdx.x);
 }
 
 // Workgroups [0, shared_blocks) take the shared expert's units and need no routing; the others

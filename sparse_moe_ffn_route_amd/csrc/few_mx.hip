@@ -68,54 +68,81 @@ __device__ __forceinline__ u32 byte_offset(u32 frag_at, int s, int S) {
 // one scale byte per row and block.
 __host__ __device__ constexpr int xt_row(int D) { return mx_steps(D) * kMxStep + 16; }
 __host__ __device__ constexpr int xt_blocks(int D) { return mx_steps(D) * 4; }
-__host__ __device__ constexpr int xt_bytes(int T, int D) { return 2 * T * (xt_row(D) + xt_blocks(D)); }
+__host__ __device__ constexpr int xt_bytes(int T, int D) { return (2 * T * (xt_row(D) + xt_blocks(D)) + 15) & ~15; }
 
-// By all threads of a workgroup: four lanes a block, eight values each.  first / stride: tokens.
+// By all THREADS of a workgroup: four lanes a block, eight values each, of four tokens at a time, whose
+// loads are in flight together.  first / stride: tokens.
+template <int THREADS>
 __device__ __forceinline__ void make_terms(const FewLayer& p, uint8_t* xt, int first, int stride) {
+  constexpr int N = 4;
   const int row = xt_row(p.D), blocks = xt_blocks(p.D);
   uint8_t* scales = xt + 2 * p.T * row;
-  for (int t = first; t < p.T; t += stride)
-    for (int c = threadIdx.x; c < blocks * 4; c += kThreads) {
-      float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      if (c * 8 < p.D) {
-        const u32x4 a = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(p.x) +
-                                                        static_cast<int64_t>(t) * p.D + c * 8);
+  for (int t0 = first; t0 < p.T; t0 += N * stride)
+    for (int c = threadIdx.x; c < blocks * 4; c += THREADS) {
+      u32x4 x[N];
+#pragma unroll
+      for (int n = 0; n < N; ++n) {
+        const int t = min(t0 + n * stride, p.T - 1), k = min(c * 8, p.D - 8);
+        x[n] = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(p.x) + static_cast<int64_t>(t) * p.D + k);
+      }
+#pragma unroll
+      for (int n = 0; n < N; ++n) {
+        const int t = t0 + n * stride;
+        if (t >= p.T) break;
+        float v[8];
+        u32 m = 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          v[2 * i] = bf16_bits_to_f32(a[i] & 0xFFFFu);
-          v[2 * i + 1] = __uint_as_float(a[i] & 0xFFFF0000u);
+          const u32 w = c * 8 < p.D ? x[n][i] : 0u;  // zeros behind the last value
+          v[2 * i] = bf16_bits_to_f32(w & 0xFFFFu);
+          v[2 * i + 1] = __uint_as_float(w & 0xFFFF0000u);
+          m = max(m, max(mx_abs_bits(v[2 * i]), mx_abs_bits(v[2 * i + 1])));
         }
-      }
-      u32 m = 0;
+        m = max(m, static_cast<u32>(__shfl_xor(static_cast<int>(m), 1, kWave)));
+        m = max(m, static_cast<u32>(__shfl_xor(static_cast<int>(m), 2, kWave)));
+        const int b = term_scale(m);
+        u32 t0s[2] = {0u, 0u}, t1s[2] = {0u, 0u};
+        if (b != 255) {
+          const float inv = ldexpf(1.0f, 127 - b);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) m = max(m, mx_abs_bits(v[i]));
-      m = max(m, static_cast<u32>(__shfl_xor(static_cast<int>(m), 1, kWave)));
-      m = max(m, static_cast<u32>(__shfl_xor(static_cast<int>(m), 2, kWave)));
-      const int b = term_scale(m);
-      u32 t0[2] = {0u, 0u}, t1[2] = {0u, 0u};
-      if (b != 255) {
-        const float inv = ldexpf(1.0f, 127 - b);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float a0 = v[2 * i] * inv, a1 = v[2 * i + 1] * inv;
-          const u32 hi = f32x2_to_e4m3x2(a0, a1);
-          const u32 lo = f32x2_to_e4m3x2((a0 - e4m3_lo(hi)) * 32.0f, (a1 - e4m3_hi(hi)) * 32.0f);
-          t0[i / 2] |= hi << (16 * (i & 1));
-          t1[i / 2] |= lo << (16 * (i & 1));
+          for (int i = 0; i < 4; ++i) {
+            const float a0 = v[2 * i] * inv, a1 = v[2 * i + 1] * inv;
+            const u32 hi = f32x2_to_e4m3x2(a0, a1);
+            const u32 lo = f32x2_to_e4m3x2((a0 - e4m3_lo(hi)) * 32.0f, (a1 - e4m3_hi(hi)) * 32.0f);
+            t0s[i / 2] |= hi << (16 * (i & 1));
+            t1s[i / 2] |= lo << (16 * (i & 1));
+          }
         }
-      }
-      *reinterpret_cast<uint2*>(xt + (2 * t) * row + c * 8) = make_uint2(t0[0], t0[1]);
-      *reinterpret_cast<uint2*>(xt + (2 * t + 1) * row + c * 8) = make_uint2(t1[0], t1[1]);
-      if ((c & 3) == 0) {
-        scales[(2 * t) * blocks + c / 4] = static_cast<uint8_t>(b);
-        scales[(2 * t + 1) * blocks + c / 4] = static_cast<uint8_t>(b == 255 ? 255 : b - kTermStep);
+        *reinterpret_cast<uint2*>(xt + (2 * t) * row + c * 8) = make_uint2(t0s[0], t0s[1]);
+        *reinterpret_cast<uint2*>(xt + (2 * t + 1) * row + c * 8) = make_uint2(t1s[0], t1s[1]);
+        if ((c & 3) == 0) {
+          scales[(2 * t) * blocks + c / 4] = static_cast<uint8_t>(b);
+          scales[(2 * t + 1) * blocks + c / 4] = static_cast<uint8_t>(b == 255 ? 255 : b - kTermStep);
+        }
       }
     }
 }
 
-// For tokens too wide for LDS: the same into the workspace, one workgroup per token.
+// Logits, and beside them on CUs that are idle here the terms of each token, for gate/up to copy: made in
+// each of its workgroups they took 2.7 us of 4 tokens and 4.4 of 8 before any weight was asked for.
+__global__ __launch_bounds__(kLogitWaves * kWave) void few_mx_first_kernel(FewLayer p) {
+  const int block = static_cast<int>(blockIdx.x) - p.T;
+  if (block >= 0) logits_block<EL_BF16, false>(p, block);
+  else make_terms<kLogitWaves * kWave>(p, static_cast<uint8_t*>(p.x_terms), blockIdx.x, p.T);
+}
+
+// Without that launch, tokens too wide for LDS.
 __global__ __launch_bounds__(kThreads) void few_terms_kernel(FewLayer p) {
-  make_terms(p, static_cast<uint8_t*>(p.x_terms), blockIdx.x, gridDim.x);
+  make_terms<kThreads>(p, static_cast<uint8_t*>(p.x_terms), blockIdx.x, gridDim.x);
+}
+
+// Made terms into LDS, complete after wait_vmcnt<0> and a barrier.
+__device__ __forceinline__ void stage_terms(const FewLayer& p, uint8_t* xt) {
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), lane = threadIdx.x % kWave;
+  const __amdgpu_buffer_rsrc_t r = buffer_rsrc(p.x_terms);
+  const int bytes = xt_bytes(p.T, p.D);
+  for (int c = wave * 1024; c < bytes; c += kWaves * 1024)
+    if (c + lane * 16 < bytes) buffer_load16_to_lds(r, xt + c, lane * 16, c);
 }
 
 // ---------------------------------------------------------------------------
@@ -270,7 +297,10 @@ __global__ __launch_bounds__(kThreads, 2) void few_mx_gate_up_kernel(FewLayer p)
   }
   const int b = blockIdx.x - p.shared_blocks, blocks = gridDim.x - p.shared_blocks;
   route_call<kGateMembers, kHMembers>(q, lds, p, b == blocks - 1, [&] {
-    if constexpr (XLDS) make_terms(p, xs, 0, 1);
+    if constexpr (XLDS) {
+      if (p.terms_made) stage_terms(p, xs);
+      else make_terms<kThreads>(p, xs, 0, 1);
+    }
   });
   const int units = __builtin_amdgcn_readfirstlane(q.entries) * (p.I / kUnit);
   mx_gate_up_units<XLDS>(p, q, XLDS ? xs : static_cast<uint8_t*>(p.x_terms), red,
@@ -372,7 +402,11 @@ size_t few_mx_h_bytes(int T, int k, int I) {
 }
 
 hipError_t launch_few_mx(FewLayer p, hipStream_t stream) {
-  if (!p.packed_in) launch_few_logits(EL_BF16, p, stream);
+  p.terms_made = !p.packed_in && !p.norm_r;
+  if (p.terms_made)
+    hipLaunchKernelGGL(few_mx_first_kernel, dim3(p.T + (p.E + 15) / 16), dim3(kLogitWaves * kWave), 0, stream, p);
+  else if (!p.packed_in)
+    launch_few_logits(EL_BF16, p, stream);
   deal(p, 17.0 / 32, 2.0);
   const int64_t most = static_cast<int64_t>(p.T * p.k < p.n_local ? p.T * p.k : p.n_local) * (p.I / kUnit);
   const int blocks = most < kCus - p.shared_blocks ? static_cast<int>(most) : kCus - p.shared_blocks;
@@ -389,7 +423,7 @@ hipError_t launch_few_mx(FewLayer p, hipStream_t stream) {
   if (p.red_bytes + x <= room) {
     hipLaunchKernelGGL((few_mx_gate_up_kernel<true>), dim3(grid), dim3(kThreads), p.red_bytes + x, stream, p);
   } else {
-    hipLaunchKernelGGL(few_terms_kernel, dim3(p.T), dim3(kThreads), 0, stream, p);
+    if (!p.terms_made) hipLaunchKernelGGL(few_terms_kernel, dim3(p.T), dim3(kThreads), 0, stream, p);
     hipLaunchKernelGGL((few_mx_gate_up_kernel<false>), dim3(grid), dim3(kThreads), p.red_bytes, stream, p);
   }
   if (p.out_el == EL_F32) hipLaunchKernelGGL((few_mx_down_kernel<EL_F32>), dim3(p.D / 16), dim3(kThreads), 0, stream, p);

@@ -163,7 +163,7 @@ struct FewLayer {
   const void* norm_w;
   void* norm_x;
   float norm_eps;
-  int shared_blocks, shared_waves, red_bufs, red_bytes, shared_red_bufs;  // set by the launchers
+  int shared_blocks, shared_waves, red_bufs, red_bytes, shared_red_bufs, terms_made;  // set by the launchers
 };
 size_t few_mx_x_bytes(int T, int D);
 size_t few_mx_h_bytes(int T, int k, int I);
