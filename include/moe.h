@@ -346,12 +346,13 @@ int moe_mx_unpack_weights(int32_t dst_dtype, int64_t n_mats, int32_t rows, int32
 
 /*
  * moe_layer_forward for 1 to MOE_FEW_MAX_T tokens (a few requests' next tokens), in three
- * launches, two with given routing: router logits; top-k and gate/up; down and combine.  The
- * arguments, the result's definition, the error word and the workspace are
- * moe_layer_forward's, for every w_dtype and layout it takes, with two differences:
- *   - x and h are not quantised for MOE_E4M3 and MOE_MXFP4 weights (such a call is bound by the
- *     weights' bytes, and the products run in bf16 on exact weight values), so y is closer to
- *     the exact layer than moe_layer_forward's;
+ * launches, two with given routing (and one for MXFP4 tokens too wide for LDS): router logits;
+ * top-k and gate/up; down and combine.  The arguments, the result's definition, the error word
+ * and the workspace are moe_layer_forward's, for every w_dtype and layout it takes, with two
+ * differences:
+ *   - x and h are not rounded to the weights' type for MOE_E4M3 and MOE_MXFP4 (such a call is
+ *     bound by the weights' bytes): products are of exact weight values with x and with h to 16
+ *     bits or more, so y is closer to the exact layer than moe_layer_forward's;
  *   - a token that names one expert in several slots gets it once with the summed weight.
  * The sum over experts is taken in another order than moe_layer_forward's; each call is
  * deterministic.  Returns MOE_ERR_UNSUPPORTED for T > MOE_FEW_MAX_T, where T * top_k * I or

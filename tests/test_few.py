@@ -219,6 +219,50 @@ def test_non_finite_values_stay_with_their_token_and_expert():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("given", [True, False])
+@pytest.mark.parametrize("w", ["e4m3", "mxfp4"])
+def test_non_finite_tokens_on_narrow_weights(w, given):
+    """A token with an infinity or a NaN is NaN and changes no other token's row, however many share its experts."""
+    rng = np.random.default_rng(18)
+    T, D, E, k, I = 16, 704, 4, 2, 192
+    layer = Layer(rng, D, E, E, I, 64, w)
+    x = torch.from_numpy(rng.standard_normal((T, D)).astype(np.float32)).to(torch.bfloat16)
+    blob = _run(layer, x.cuda(), True, T, D, E, k, I, 64, 0, E, True, "f32")[2]
+    args = (True, T, D, E, k, I, 64, 0, E, True, "f32", blob if given else None)
+    clean = to_np(_run(layer, x.cuda(), *args)[0])
+    for t, c, v in ((0, 0, "inf"), (9, 703, "nan"), (15, 350, "-inf")):
+        bad = x.clone()
+        bad[t, c] = float(v)
+        got = to_np(_run(layer, bad.cuda(), *args)[0])
+        assert not np.isfinite(got[t]).any()
+        rest = np.delete(np.arange(T), t)
+        # with its own routing the NaN token names other experts, and the order of a sum may change
+        if given:
+            np.testing.assert_array_equal(got[rest], clean[rest])
+        else:
+            assert rel_err(got[rest], clean[rest]) <= 2 * (1e-4 + 2.0 ** -24)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("w", ["f32", "bf16", "e4m3", "mxfp4"])
+@pytest.mark.parametrize("Is", [0, 128])
+def test_no_token_chose_a_local_expert(w, Is):
+    rng = np.random.default_rng(1)
+    T, D, E, k, I = 4, 192, 12, 2, 64
+    layer = Layer(rng, D, E, 3, I, Is, w)
+    x = torch.from_numpy(rng.standard_normal((T, D)).astype(np.float32)).to(layer.f)
+    ids = np.tile(np.array([[0, 11]], np.int32), (T, 1))
+    blob = torch.from_numpy(oracle.pack_routing(ids, np.ones((T, k), np.float32))).cuda()
+    y, _, _, ws = _run(layer, x.cuda(), True, T, D, E, k, I, Is, 4, 3, True, "f32", blob)
+    assert int(moe.workspace_error_count(ws).cpu()[0]) == 0
+    if Is:
+        ref = layer.reference(to_np(x), ids, np.ones((T, k)), 4)
+        assert rel_err(to_np(y), ref) <= 1e-4 + 2.0 ** -24
+    else:
+        assert (to_np(y) == 0).all()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("w", ["bf16", "mxfp4", "f32"])
 def test_streams_graphs_and_repeats(w):
     """The call on another stream, captured and replayed between eager calls on other inputs and the same

@@ -326,6 +326,11 @@ def test_layer_captured_and_without_a_workspace():
             want.append(y.clone())
             moe.moe_layer_forward_noalloc(d, wts, v, None, None, y2)
             assert torch.equal(y2, y)
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        moe.moe_layer_forward(d, wts, xs[1], None, None, y2, ws=ws, stream=side)
+        side.synchronize()
+        assert torch.equal(y2, want[1])
         g = torch.cuda.CUDAGraph()
         with torch.cuda.graph(g):
             moe.moe_layer_forward(d, wts, x, None, None, y, ws=ws)
