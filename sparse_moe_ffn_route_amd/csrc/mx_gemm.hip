@@ -75,6 +75,7 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t matrix_rsrc(const void* base) 
 // The tile of one workgroup: group, rows, and which part of the channels.
 struct Tile {
   int g, part, row0, nrows;
+  bool alone;  // the only M-tile of its group: nothing else reads its weights
 };
 
 // Tile L of the order (group, part of the channels, M-tile).
@@ -99,9 +100,14 @@ __device__ __forceinline__ Tile locate(const MxGemm& p, int L, int parts) {
   const int r = __builtin_amdgcn_readfirstlane(local % mt) * per;
   t.row0 = beg + r;
   t.nrows = min(per, count - r);
+  t.alone = mt == 1;
   return t;
 }
 
+// Weights that only one tile reads bypass the caches' replacement (NT): 64 experts of 50 rows took 47 us for
+// gate/up and 31 for down, 59 and 34 without; with two tiles per expert, which share them in L2, it
+// is 97 against 81.  Tiles of one unit (at most 32 rows on average) are mostly alone and always do.
+//
 // A wave's weights: pairs of fragments, of both matrices or of one, from channel ncol on.  Half j of a
 // step is its blocks 2 j and 2 j + 1: lanes l % 32 < 16 the pair's first fragment, the others its
 // second, two pieces of 512 contiguous bytes per load.
@@ -346,18 +352,14 @@ struct RowLoader {
   }
 };
 
-template <int MF, bool SWIGLU, int OUT>
-__global__ __launch_bounds__(kWaves * 64, 2) void mx_resident_kernel(MxGemm p) {
+template <int MF, bool SWIGLU, int OUT, bool NT>
+__device__ __forceinline__ void resident_tile(const MxGemm& p, const Tile& t, uint8_t* lds) {
   constexpr int BN = mx_bn(SWIGLU), kBuf = MF * kUnitRows * kMxRecord;
-  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
-  const int total = ld_scalar(p.tile_prefix + p.n_groups) * p.parts;
-  if (static_cast<int>(blockIdx.x) >= total) return;
-  const Tile t = locate(p, xcd_remap(blockIdx.x, total), p.parts);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), lane = threadIdx.x % kWave;
   const int blocks = (p.N + BN - 1) / BN;  // of channels; this workgroup takes [b0, b1)
   const int b0 = blocks * t.part / p.parts, b1 = blocks * (t.part + 1) / p.parts;
   if (b0 == b1) return;
-  Weights<SWIGLU, MF == 1> wt(p, t.g, lane);
+  Weights<SWIGLU, NT> wt(p, t.g, lane);
   const int S = wt.S, G = wt.G, wcol = wave * (BN / kWaves);
   {
     const RowLoader<MF> rows(p, t, static_cast<u32>(mx_row_bytes(p.K)));
@@ -399,14 +401,20 @@ __global__ __launch_bounds__(kWaves * 64, 2) void mx_resident_kernel(MxGemm p) {
 }
 
 template <int MF, bool SWIGLU, int OUT>
-__global__ __launch_bounds__(kWaves * 64, 2) void mx_ring_kernel(MxGemm p) {
-  constexpr int BN = mx_bn(SWIGLU), kBuf = MF * kUnitRows * kMxRecord;
-  __shared__ __attribute__((aligned(16))) uint8_t lds[kRing * kBuf + (SWIGLU ? 0 : kWaves * kStage)];
+__global__ __launch_bounds__(kWaves * 64, 2) void mx_resident_kernel(MxGemm p) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   const int total = ld_scalar(p.tile_prefix + p.n_groups) * p.parts;
   if (static_cast<int>(blockIdx.x) >= total) return;
   const Tile t = locate(p, xcd_remap(blockIdx.x, total), p.parts);
+  if (MF == 1 || t.alone) resident_tile<MF, SWIGLU, OUT, true>(p, t, lds);
+  else resident_tile<MF, SWIGLU, OUT, false>(p, t, lds);
+}
+
+template <int MF, bool SWIGLU, int OUT, bool NT>
+__device__ __forceinline__ void ring_tile(const MxGemm& p, const Tile& t, uint8_t* lds) {
+  constexpr int BN = mx_bn(SWIGLU), kBuf = MF * kUnitRows * kMxRecord;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), lane = threadIdx.x % kWave;
-  Weights<SWIGLU, MF == 1> wt(p, t.g, lane);
+  Weights<SWIGLU, NT> wt(p, t.g, lane);
   const int S = wt.S, G = wt.G, ncol0 = t.part * BN + wave * (BN / kWaves);
   const RowLoader<MF> rows(p, t, static_cast<u32>(mx_row_bytes(p.K)));
   constexpr int kLead = kRing - 1;  // groups of rows requested ahead
@@ -448,6 +456,16 @@ __global__ __launch_bounds__(kWaves * 64, 2) void mx_ring_kernel(MxGemm p) {
     }
     store_tile<MU, SWIGLU, OUT>(p, acc, t.row0, t.nrows, ncol0, lane, lds + kRing * kBuf + wave * kStage);
   });
+}
+
+template <int MF, bool SWIGLU, int OUT>
+__global__ __launch_bounds__(kWaves * 64, 2) void mx_ring_kernel(MxGemm p) {
+  __shared__ __attribute__((aligned(16))) uint8_t lds[kRing * MF * kUnitRows * kMxRecord + (SWIGLU ? 0 : kWaves * kStage)];
+  const int total = ld_scalar(p.tile_prefix + p.n_groups) * p.parts;
+  if (static_cast<int>(blockIdx.x) >= total) return;
+  const Tile t = locate(p, xcd_remap(blockIdx.x, total), p.parts);
+  if (MF == 1 || t.alone) ring_tile<MF, SWIGLU, OUT, true>(p, t, lds);
+  else ring_tile<MF, SWIGLU, OUT, false>(p, t, lds);
 }
 
 // Into how many parts a resident tile's blocks of channels go, one workgroup each.  Tiles of one unit
