@@ -234,11 +234,13 @@ int route_tokens(const moe_dims& d, const void* x, const void* w_router, float* 
   return hip_status(launch_route(nullptr, 1, logits, bias, d.T, d.E, d.top_k, d.renormalize, packed, s));
 }
 
-// M-tile height of the 4-bit grouped GEMMs, by the average routed rows per expert: up to 32 rows a
-// tile of one unit, above tiles of up to four.
+// M-tile height of the 4-bit grouped GEMMs, by the average routed rows per expert: up to 16 rows a
+// tile of one unit, above tiles of up to four, so that few experts need a second tile and the weights
+// again (64 experts of 4096 x 1024, gate/up: 25 rows each 45 us with the taller tile, 55 with the
+// shorter; 10 rows 45 both; 10 rows of 1024 x 512 10.1 and 8.6).
 int mx_bm(const moe_dims& d) {
   const double avg = static_cast<double>(d.T) * d.top_k / d.E;
-  return avg <= 32.0 ? 32 : 128;
+  return avg <= 16.0 ? 32 : 128;
 }
 
 // M-tile height of the routed grouped GEMMs of these dims.

@@ -7,8 +7,9 @@
 //
 // One workgroup per row: the row's y, r and gate are read once into registers (kept there
 // through both reductions), so the traffic is the floor: 2 to 3 reads and 1 to 2 writes per
-// value.  Measured, bf16 rows of 4096 with a gate for every value: 8192 rows (336 MB) in 59 us, 5.7 TB/s (a device
-// copy reaches 4.9); one row in 3 us, a few memory latencies.
+// value.  Measured, bf16 rows of 4096 with a gate for every value: 8192 rows (336 MB) in 52 us, 6.4 TB/s (a device
+// copy reaches 4.9; 60 us with loads through the caches' ordinary replacement, 57 with stores past it, too);
+// one row in 3 us, a few memory latencies.
 #include <type_traits>
 
 #include "common.hpp"
@@ -24,6 +25,8 @@ struct Chunk {
   static constexpr int kWords = V == 1 ? 1 : EL == EL_F32 ? 8 : 4;
   uint32_t w[kWords];
 
+  // NT: past the caches' replacement, for what is read once.
+  template <bool NT = false>
   __device__ __forceinline__ void load(const void* base, int64_t idx) {
     if constexpr (V == 1) {
       w[0] = EL == EL_F32 ? static_cast<const uint32_t*>(base)[idx] : static_cast<const uint16_t*>(base)[idx];
@@ -31,7 +34,7 @@ struct Chunk {
       const u32x4* p = reinterpret_cast<const u32x4*>(static_cast<const uint8_t*>(base) + idx * (EL == EL_F32 ? 4 : 2));
 #pragma unroll
       for (int i = 0; i < kWords / 4; ++i) {
-        const u32x4 a = p[i];
+        const u32x4 a = NT ? __builtin_nontemporal_load(p + i) : p[i];
 #pragma unroll
         for (int j = 0; j < 4; ++j) w[4 * i + j] = a[j];
       }
@@ -84,15 +87,15 @@ __global__ __launch_bounds__(kThreads) void block_norm_kernel(BlockNorm p) {
   Chunk<EL, V> rc[NC], wp[kEarly ? NC : 1], g[kEarly ? NC : 1], wn[kEarly ? NC : 1];
   auto load_post = [&](int c, int d) {
     if (p.w_post) wp[kEarly ? c : 0].load(p.w_post, d);
-    if (gated) g[kEarly ? c : 0].load(p.gate, p.gate_kind == kGateChannel ? d : base + d);
+    if (gated) g[kEarly ? c : 0].template load<true>(p.gate, p.gate_kind == kGateChannel ? d : base + d);
   };
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
     const int d = (c * kThreads + threadIdx.x) * V;
     if (d >= p.D) continue;
-    rc[c].load(p.r, base + d);
+    rc[c].template load<true>(p.r, base + d);
     if (p.y) {
-      yc[c].load(p.y, base + d);
+      yc[c].template load<true>(p.y, base + d);
       if constexpr (kEarly) load_post(c, d);
     }
     if (kEarly && p.w_next) wn[kEarly ? c : 0].load(p.w_next, d);

@@ -106,7 +106,7 @@ __device__ __forceinline__ Tile locate(const MxGemm& p, int L, int parts) {
 
 // Weights that only one tile reads bypass the caches' replacement (NT): 64 experts of 50 rows took 47 us for
 // gate/up and 31 for down, 59 and 34 without; with two tiles per expert, which share them in L2, it
-// is 97 against 81.  Tiles of one unit (at most 32 rows on average) are mostly alone and always do.
+// is 97 against 81.  Tiles of one unit (at most 16 rows on average) are mostly alone and always do.
 //
 // A wave's weights: pairs of fragments, of both matrices or of one, from channel ncol on.  Half j of a
 // step is its blocks 2 j and 2 j + 1: lanes l % 32 < 16 the pair's first fragment, the others its

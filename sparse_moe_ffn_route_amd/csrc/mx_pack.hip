@@ -3,7 +3,9 @@
 //
 // All three are streams: pack reads 2 (bf16) or 4 (fp32) bytes and writes 17/32 byte per
 // value, unpack the reverse.  Measured, 64 matrices of 1024 x 4096 (537 MB of bf16, 143 MB of images): pack
-// 152 us, 4.5 TB/s (a device copy reaches 4.9); unpack 107 us, 6.4 TB/s (a fill reaches 6.9).
+// 120 us, unpack 122, 5.6 TB/s (a device copy reaches 4.9).  What is read or written once goes past the caches'
+// replacement: pack took 158 without that, and unpack 107 after such a pack, whose images it
+// then found in the cache before HBM, 128 otherwise.
 #include <type_traits>
 
 #include "common.hpp"
@@ -24,11 +26,17 @@ template <int EL>
 struct Octet {
   u32 w[EL == EL_F32 ? 8 : 4];
 
+  // NT: past the caches' replacement, for what is read once.
+  template <bool NT = false>
   __device__ __forceinline__ void load(const void* base, size_t idx) {
     constexpr int bytes = EL == EL_F32 ? 4 : 2;
     const u32x4* p = reinterpret_cast<const u32x4*>(static_cast<const uint8_t*>(base) + idx * bytes);
 #pragma unroll
-    for (int i = 0; i < bytes; ++i) reinterpret_cast<u32x4&>(w[4 * (i / 2)]) = p[i / 2];
+    for (int i = 0; i < bytes / 2; ++i) {
+      const u32x4 a = NT ? __builtin_nontemporal_load(p + i) : p[i];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w[4 * i + j] = a[j];
+    }
   }
 
   // Bits of the largest magnitude, as fp32.
@@ -86,7 +94,7 @@ __device__ __forceinline__ void quad_transpose(u32 (&w)[4], int q) {
   }
 }
 
-// One wave per (matrix, 16 rows, group).  (Reading 1 KB of one row at a time instead took 172 us against 152.)
+// One wave per (matrix, 16 rows, group).  (Reading 1 KB of one row at a time instead took 172 us against 158.)
 // Lane l reads 8 values of row 4 i + l / 16 from (l % 16) * 8 on
 // (whole lines), a block's four lanes share its magnitude, and a 4x4 transpose between them makes each
 // the holder of one block, so the codes go out as whole 1 KB runs and the scales as one 256-byte store.
@@ -111,7 +119,7 @@ __global__ __launch_bounds__(256) void mx_pack_kernel(const void* __restrict__ s
     const int k = min(k0, cols - 8);  // behind the last value: read again, stored as zero
     Octet<EL> v[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i].load(src, (static_cast<size_t>(fr) * 16 + i * 4 + r) * cols + k);
+    for (int i = 0; i < 4; ++i) v[i].template load<true>(src, (static_cast<size_t>(fr) * 16 + i * 4 + r) * cols + k);
     u32 codes[4];
     u32 byte = 127u;
 #pragma unroll
@@ -126,9 +134,10 @@ __global__ __launch_bounds__(256) void mx_pack_kernel(const void* __restrict__ s
     }
     if (k0 < cols) scales = (scales & ~(0xFFu << (8 * s))) | (byte << (8 * s));
     quad_transpose(codes, q);
-    *reinterpret_cast<u32x4*>(out + s * kMxRun + slot * 16) = u32x4{codes[0], codes[1], codes[2], codes[3]};
+    __builtin_nontemporal_store((u32x4{codes[0], codes[1], codes[2], codes[3]}),
+                                reinterpret_cast<u32x4*>(out + s * kMxRun + slot * 16));
   }
-  *reinterpret_cast<u32*>(out + steps * kMxRun + slot * 4) = scales;
+  __builtin_nontemporal_store(scales, reinterpret_cast<u32*>(out + steps * kMxRun + slot * 4));
 }
 
 // One wave per (matrix, 16 rows, group).  Lane l decodes one dword of codes at a time, 8 values of row
@@ -169,13 +178,13 @@ __global__ __launch_bounds__(256) void mx_unpack_kernel(const uint8_t* __restric
       v[2] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[i], 1.0f, 2) * scale;
       v[3] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[i], 1.0f, 3) * scale;
       if constexpr (EL == EL_F32) {
-        float4* p = reinterpret_cast<float4*>(static_cast<float*>(dst) + idx);
-        p[0] = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
-        p[1] = make_float4(v[2].x, v[2].y, v[3].x, v[3].y);
+        f32x4* p = reinterpret_cast<f32x4*>(static_cast<float*>(dst) + idx);
+        __builtin_nontemporal_store((f32x4{v[0].x, v[0].y, v[1].x, v[1].y}), p);
+        __builtin_nontemporal_store((f32x4{v[2].x, v[2].y, v[3].x, v[3].y}), p + 1);
       } else {
-        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(dst) + idx) =
-            make_uint4(bf16x2_bits(v[0].x, v[0].y), bf16x2_bits(v[1].x, v[1].y), bf16x2_bits(v[2].x, v[2].y),
-                       bf16x2_bits(v[3].x, v[3].y));
+        __builtin_nontemporal_store((u32x4{bf16x2_bits(v[0].x, v[0].y), bf16x2_bits(v[1].x, v[1].y),
+                                           bf16x2_bits(v[2].x, v[2].y), bf16x2_bits(v[3].x, v[3].y)}),
+                                    reinterpret_cast<u32x4*>(static_cast<uint16_t*>(dst) + idx));
       }
     }
   }
