@@ -7,9 +7,9 @@
 //
 // One workgroup per row: the row's y, r and gate are read once into registers (kept there
 // through both reductions), so the traffic is the floor: 2 to 3 reads and 1 to 2 writes per
-// value.  Measured, bf16 rows of 4096 with a gate for every value: 8192 rows (336 MB) in 52 us, 6.4 TB/s (a device
-// copy reaches 4.9; 60 us with loads through the caches' ordinary replacement, 57 with stores past it, too);
-// one row in 3 us, a few memory latencies.
+// value.  Measured, bf16 rows of 4096 with a gate for every value: 8192 rows (336 MB) in 58 us, 5.8 TB/s (a device
+// copy reaches 4.9; 60 us with loads through the caches' ordinary replacement; alternating between two such
+// inputs 52 against 60, and 57 with the stores past it, too); one row in 3 us, a few memory latencies.
 #include <type_traits>
 
 #include "common.hpp"

@@ -11,8 +11,8 @@
 // MFMAs per KB and bound both kernels by instruction issue (4.0 TB/s at 4 tokens).
 //
 // Measured, 4 tokens, 8 of 128 experts of D 4096 and I 1024 and a shared bf16 one (221 MB, 33 us at the
-// 6.8 TB/s streaming read): 55 to 58 us; logits 7, gate/up 31 (weights at 6.0 TB/s from 6 us on, after
-// the terms of x, 3, and the selection, 3), down 17 (6.6 TB/s after 3).
+// 6.8 TB/s streaming read): 55 to 57 us; logits 7, gate/up 29 (weights at 6.0 TB/s from 4 to 5 us on, when the
+// experts are known), down 17 (6.6 TB/s after 3).
 //
 // Lane g of a column holds, of a step's 128 values, 16 g .. + 15 and 64 + 16 g .. + 15 in its
 // e4m3 operand, and the scale of values 32 g .. + 31.

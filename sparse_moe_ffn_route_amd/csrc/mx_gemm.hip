@@ -19,12 +19,14 @@
 //             workgroup does one block of channels.
 // Two workgroups of 4 waves per CU cover each other's beginnings and ends.
 //
-// Measured, 64 experts of D 4096 and I 1024 (428 MB of weights).  10 rows each: gate/up 44 us, down 24 us,
-// 6.4 and 6.2 TB/s, bound by the weights' bytes.  160 rows each (258 GFLOP): gate/up 79 us, of which its
+// Measured, 64 experts of D 4096 and I 1024 (428 MB of weights).  10 rows each: gate/up 44 us, down 25 us,
+// 6.5 and 6.0 TB/s, bound by the weights' bytes; 50 rows 47 and 31.  160 rows each (258 GFLOP): gate/up 80 us, of which its
 // MFMAs alone take 45 and everything but them 76; the weights come from memory once and
 // through L2 twice (two M-tiles), and waves wait for the slowest at each group's barrier;
-// down 49 us, 4.8 TB/s of which a third is the rows written.  Deeper rings (8 waves, 4 buffers), another order
-// of the steps per wave and other parts of the channels were no faster.
+// down 48 us, 4.9 TB/s of which a third is the rows written.  Deeper rings (8 waves, 4 buffers), another order
+// of the steps per wave, other parts of the channels, both tiles in one workgroup of 8 waves (83 and 58 us) and
+// 64-row resident tiles (105 and 56) were no faster; one 256-row tile with one wave per SIMD took 75 us for
+// gate/up here and 123 against 101 at 240 rows each.
 // A group's rows are split evenly over the M-tiles it needs, so that no tile streams the
 // weights for a few rows only.
 #include <algorithm>
