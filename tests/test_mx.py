@@ -188,7 +188,7 @@ def _check_rows(got, ref, slack, half_step):
 
 
 FFN = [
-    # (rows of each group, D, I, out): heights of 16, 32 and 128 rows come from the average
+    # (rows of each group, D, I, out): tiles of 32 or 128 rows, by the average and the number of tiles
     ([1], 64, 64, "bf16"),
     ([5, 0, 16, 17, 1, 0, 3], 256, 128, "f32"),
     ([20, 31, 33, 0, 16], 704, 320, "bf16"),
@@ -200,6 +200,12 @@ FFN = [
     ([8, 30], 64, 4224, "f32"),
     ([0, 2, 0, 1] * 256, 64, 64, "bf16"),       # the most groups
     ([40] * 70 + [0] * 5, 64, 64, "f32"),
+    # enough work for the taller tiles: one to four units, one tile of a group or several; rows resident
+    # or through the ring, in either launch
+    ([130, 1, 128, 0, 300, 64, 97, 33, 96, 160, 129, 5] * 2, 576, 576, "bf16"),
+    ([130, 1, 128, 0, 300, 64, 97, 33, 96, 160, 129, 5] * 2, 1088, 576, "f32"),
+    ([70, 128, 31, 200, 0, 160, 257, 65, 96, 40, 100, 150], 128, 1088, "bf16"),
+    ([70, 128, 31, 200, 0, 160, 257, 65, 96, 40, 100, 150], 704, 1088, "f32"),
 ]
 
 
@@ -268,6 +274,7 @@ LAYERS = [
     (40, 256, 16, 3, 128, 64, 0, 16, False),
     (300, 448, 24, 4, 192, 128, 0, 24, False),
     (700, 320, 8, 2, 64, 0, 2, 5, True),
+    (400, 256, 32, 4, 640, 64, 0, 32, False),
 ]
 
 
