@@ -137,13 +137,20 @@ Layout layout(const moe_dims& d) {
   L.hq = take(fp8 ? tk * d.I : 0);
   L.sh = take(fp8 ? tk * 4 : 0);
   L.out_rows = take(tk * d.D * os);
-  L.layer = off;  // all but the few-token layer's parts
-  // h of the few-token layer: fp32, two bf16 planes, or the terms of the 4-bit kernels
-  L.few_h = take(!is_few(d) ? 0 : mx ? few_mx_h_bytes(d.T, d.top_k, d.I) : tk * d.I * 4);
-  L.few_xt = take(is_few(d) && mx ? few_mx_x_bytes(d.T, d.D) : 0);
-  L.few_h_sh = take(is_few(d) ? T * d.I_shared * 4 : 0);
-  L.few_entries = take(is_few(d) ? (1 + tk) * 8 : 0);
-  L.total = off;
+  L.layer = off;  // what every call but the few-token layer touches
+  // The few-token layer's parts lie over those that it does not use.  A workspace for more tokens holds
+  // them too, for as many tokens as that layer takes: it serves every smaller call.
+  off = L.logits_part;
+  moe_dims f = d;
+  f.T = std::min(d.T, kFewMaxT);
+  while (!is_few(f)) --f.T;
+  const size_t few_tk = static_cast<size_t>(f.T) * f.top_k;
+  // h: fp32, two bf16 planes, or the terms of the 4-bit kernels
+  L.few_h = take(mx ? few_mx_h_bytes(f.T, f.top_k, f.I) : few_tk * f.I * 4);
+  L.few_xt = take(mx ? few_mx_x_bytes(f.T, f.D) : 0);
+  L.few_h_sh = take(static_cast<size_t>(f.T) * f.I_shared * 4);
+  L.few_entries = take((1 + few_tk) * 8);
+  L.total = std::max(off, L.layer);
   return L;
 }
 
@@ -640,7 +647,7 @@ int moe_layer_forward_noalloc(const moe_dims* dims, const moe_weights* w, const 
   void* ws = nullptr;
   const int sst = static_scratch(&ws);
   if (sst != MOE_OK) return sst;
-  // the few-token layer's parts lie behind everything that this call touches
+  // the few-token layer's parts, which L.total counts, are not touched
   const int r = moe_layer_forward(dims, w, x, packed_in, logit_bias, y, logits_out, packed_out, ws, L.total,
                                   stage_events, stream);
   if (r != MOE_OK || !bad_ids) return r;
