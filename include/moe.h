@@ -411,6 +411,8 @@ int moe_block_norm(int32_t T, int32_t D, int32_t act_dtype, int32_t y_dtype, con
  *   r, r_out, x_next  act_dtype, as in moe_block_norm
  *   ws           at least moe_block_workspace_bytes(dims) bytes (0 for invalid dims); the layer's
  *                workspace, error word included, is its first part
+ * x_in, the layer's weights and ws are refused (MOE_ERR_UNSUPPORTED) off a 16-byte boundary where the layer call
+ * that is taken refuses them; w_in, r, r_out, x_next and the tensors of n lie anywhere.
  */
 size_t moe_block_workspace_bytes(const moe_dims* dims);
 int moe_block_forward(const moe_dims* dims, const moe_weights* weights, const void* w_in, const void* x_in,

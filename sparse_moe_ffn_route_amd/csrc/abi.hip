@@ -265,7 +265,6 @@ int routed_bm(const moe_dims& d, bool gathered) {
 int mx_experts(const moe_dims& d, void* ws, const Layout& L, const void* a_rows, const int32_t* perm,
                const int32_t* offsets, const void* w_gate, const void* w_up, const void* w_down, void* out_rows,
                bool have_tile_prefix, hipEvent_t ev_gate_up, hipEvent_t ev_down, hipStream_t s) {
-  if (!aligned16(a_rows, w_gate, w_up, w_down, out_rows, ws)) return MOE_ERR_UNSUPPORTED;
   const int bm = mx_bm(d);
   const int tk = d.T * d.top_k;
   int32_t* prefix = at<int32_t>(ws, L.tp_a);
@@ -382,13 +381,20 @@ int check_layer_args(const moe_dims& d, const moe_weights* w, const void* x, con
   return MOE_OK;
 }
 
+// Whether the addresses of a call of the whole layer suit the 4-bit kernels, and those of the few-token
+// layer: asked before the call's first launch.
+bool layer_aligned(const moe_dims& d, const moe_weights* w, const void* x, const void* ws) {
+  return d.w_dtype != MOE_MXFP4 || aligned16(x, ws, w->w_gate, w->w_up, w->w_down);
+}
+bool few_aligned(const moe_dims& d, const moe_weights* w, const void* x, const int32_t* packed_in, const void* ws) {
+  return aligned16(x, ws, packed_in ? nullptr : w->w_router, w->w_gate, w->w_up, w->w_down,
+                   d.I_shared ? w->sh_gate : nullptr, d.I_shared ? w->sh_up : nullptr, d.I_shared ? w->sh_down : nullptr);
+}
+
 // The few-token layer.  norm_r given: x is made of it first, rms(norm_r) * norm_w.
 int few_layer(const moe_dims& d, const Layout& L, const moe_weights* w, const void* x, const int32_t* packed_in,
               const float* logit_bias, void* y, float* logits_out, int32_t* packed_out, void* ws, const void* norm_r,
               const void* norm_w, float norm_eps, hipStream_t stream) {
-  if (!aligned16(x, ws, packed_in ? nullptr : w->w_router, w->w_gate, w->w_up, w->w_down,
-                 d.I_shared ? w->sh_gate : nullptr, d.I_shared ? w->sh_up : nullptr, d.I_shared ? w->sh_down : nullptr))
-    return MOE_ERR_UNSUPPORTED;
   const bool mx = d.w_dtype == MOE_MXFP4;
   const int64_t es = d.w_dtype == MOE_F32 ? 4 : d.w_dtype == MOE_BF16 ? 2 : 1;
   FewLayer p{};
@@ -555,6 +561,7 @@ int moe_grouped_ffn(const moe_dims* dims, const void* a_rows, const float* a_sca
   const Layout L = layout(d);
   if (ws_bytes < L.total) return MOE_ERR_WORKSPACE;
   if (d.T == 0) return MOE_OK;
+  if (d.w_dtype == MOE_MXFP4 && !aligned16(a_rows, w_gate, w_up, w_down, out_rows, ws)) return MOE_ERR_UNSUPPORTED;
   return experts_forward(d, ws, L, a_rows, a_scale, perm_token, offsets, w_gate, w_up, w_down, s_gate, s_up, s_down,
                          out_rows, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, false, nullptr,
                          nullptr, static_cast<hipStream_t>(stream));
@@ -583,6 +590,7 @@ int moe_layer_forward(const moe_dims* dims, const moe_weights* w, const void* x,
   const Layout L = layout(d);
   if (ws_bytes < L.total) return MOE_ERR_WORKSPACE;
   if (d.T == 0) return MOE_OK;
+  if (!layer_aligned(d, w, x, ws)) return MOE_ERR_UNSUPPORTED;
   hipStream_t s = static_cast<hipStream_t>(stream);
   auto mark = [&](int i) -> hipError_t {
     return stage_events ? hipEventRecord(static_cast<hipEvent_t>(stage_events[i]), s) : hipSuccess;
@@ -694,6 +702,7 @@ int moe_layer_forward_few(const moe_dims* dims, const moe_weights* w, const void
   const Layout L = layout(d);
   if (ws_bytes < L.total) return MOE_ERR_WORKSPACE;
   if (d.T == 0) return MOE_OK;
+  if (!few_aligned(d, w, x, packed_in, ws)) return MOE_ERR_UNSUPPORTED;
   return few_layer(d, L, w, x, packed_in, logit_bias, y, logits_out, packed_out, ws, nullptr, nullptr, 0.0f,
                    static_cast<hipStream_t>(stream));
 }
@@ -733,6 +742,7 @@ int moe_block_forward(const moe_dims* dims, const moe_weights* weights, const vo
   const void* x = x_in ? x_in : at<void>(ws, B.x);
   // few tokens: entering is part of the layer's first launch
   const bool few = is_few(d), fused = few && w_in && aligned16(r, w_in);
+  if (few ? !few_aligned(d, weights, x, nullptr, ws) : !layer_aligned(d, weights, x, ws)) return MOE_ERR_UNSUPPORTED;
   if (w_in && !fused) {
     moe_norm enter{};
     enter.w_next = w_in;

@@ -58,3 +58,71 @@ def test_calls_on_the_workspace_of_more_tokens(w):
                 got.append(y)
                 assert guard is None or (guard[bytes_:] == 0xA5).all()
             assert torch.equal(*got)
+
+
+# ---------------------------------------------------------------------------
+# Nothing is launched by a refused call
+# ---------------------------------------------------------------------------
+
+FAKE, OFF = ctypes.c_void_p(256), ctypes.c_void_p(264)
+
+
+def _layer_weights(off):
+    """Router, gate, up and down at 16-byte boundaries but for the one at index `off`."""
+    return moe.moe_weights(*[OFF if i == off else FAKE for i in range(4)], *[None] * 6)
+
+
+def test_the_layer_checks_alignment_before_any_launch():
+    lib = moe.library()
+    for T in (8, 40):
+        d = moe.make_dims(T, 64, 8, 2, 64, act="bf16", w="mxfp4", out="bf16", layout="packed")
+
+        def call(x=FAKE, off=None, ws=FAKE):
+            return lib.moe_layer_forward(ctypes.byref(d), ctypes.byref(_layer_weights(off)), x, None, None, FAKE, None,
+                                         None, ws, 1 << 30, None, None)
+
+        assert call(x=OFF) == call(ws=OFF) == moe.ERR_UNSUPPORTED
+        for i in (1, 2, 3):
+            assert call(off=i) == moe.ERR_UNSUPPORTED
+
+
+def test_the_block_checks_alignment_before_any_launch():
+    lib = moe.library()
+    n = moe.moe_norm(None, None, None, 0, 1.0, 1e-6)
+
+    def call(T, w, off=None, r=FAKE, x_in=None, ws=FAKE):
+        d = moe.make_dims(T, 64, 8, 2, 64, act="bf16", w=w, out="bf16", layout="packed")
+        return lib.moe_block_forward(ctypes.byref(d), ctypes.byref(_layer_weights(off)), None if x_in else FAKE, x_in,
+                                     None, ctypes.byref(n), r, FAKE, None, ws, 1 << 30, None)
+
+    for T, w in ((8, "bf16"), (8, "mxfp4"), (40, "mxfp4")):
+        assert call(T, w, ws=OFF) == moe.ERR_UNSUPPORTED
+        assert call(T, w, x_in=OFF) == moe.ERR_UNSUPPORTED
+        for i in range(0 if T == 8 else 1, 4):
+            assert call(T, w, off=i) == moe.ERR_UNSUPPORTED
+            assert call(T, w, off=i, r=OFF) == moe.ERR_UNSUPPORTED       # r off a boundary: entered before the layer
+
+
+@pytest.mark.gpu
+def test_a_refused_layer_call_writes_nothing():
+    """4-bit images off a 16-byte boundary: logits, blob, output and workspace stay as they were."""
+    rng = np.random.default_rng(3)
+    T, D, E, k, I = 40, 128, 8, 2, 64
+    layer = Layer(rng, D, E, E, I, 0, "mxfp4")
+    layer.on_gpu(True)
+    router, gate, up, down = layer.alive[:4]
+    moved = torch.empty(up.numel() + 8, dtype=torch.uint8, device="cuda")[8:].copy_(up.reshape(-1))
+    d = moe.make_dims(T, D, E, k, I, 0, 0, E, True, "bf16", "mxfp4", "bf16", "packed")
+    x = torch.randn(T, D, device="cuda").to(torch.bfloat16)
+    outs = [torch.full((T, D), 7.0, dtype=torch.bfloat16, device="cuda"), torch.full((T, E), 7.0, device="cuda"),
+            torch.full((T, 2, k), 7, dtype=torch.int32, device="cuda"),
+            torch.full((moe.block_workspace(d).numel(),), 7, dtype=torch.uint8, device="cuda")]
+    y, logits, blob, ws = outs
+    w = moe.make_weights(router, gate, moved, down)
+    with pytest.raises(moe.MoeError, match="unsupported"):
+        moe.moe_layer_forward(d, w, x, None, None, y, logits, blob, ws)
+    with pytest.raises(moe.MoeError, match="unsupported"):
+        moe.moe_block_forward(d, w, x, y, w_in=x[0], ws=ws)
+    assert all((t == 7).all() for t in outs)
+    moe.moe_layer_forward(d, moe.make_weights(router, gate, up, down), x, None, None, y, logits, blob, ws)
+    assert torch.isfinite(y.float()).all() and (y != 7).any()
