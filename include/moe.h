@@ -406,10 +406,12 @@ int moe_block_norm(int32_t T, int32_t D, int32_t act_dtype, int32_t y_dtype, con
  *   y = the layer of x, routed by it: moe_layer_forward_few where it takes the dims (up to
  *       MOE_FEW_MAX_T tokens), else moe_layer_forward, rounded to out_dtype;
  *   r_out, x_next as moe_block_norm(n, y, r).
+ * All experts are local (n_local = E, else MOE_ERR_UNSUPPORTED): an expert slice's y is a partial sum, which goes
+ * through moe_layer_forward and the sum over the devices before moe_block_norm.
  *
  *   w_in, x_in   exactly one of them is given: w_in [D], x_in [T][D] (as the layer's x), act_dtype
  *   r, r_out, x_next  act_dtype, as in moe_block_norm
- *   ws           at least moe_block_workspace_bytes(dims) bytes (0 for invalid dims); the layer's
+ *   ws           at least moe_block_workspace_bytes(dims) bytes (0 for refused dims); the layer's
  *                workspace, error word included, is its first part
  * x_in, the layer's weights and ws are refused (MOE_ERR_UNSUPPORTED) off a 16-byte boundary where the layer call
  * that is taken refuses them; w_in, r, r_out, x_next and the tensors of n lie anywhere.

@@ -439,6 +439,12 @@ int check_norm(int32_t T, int32_t D, int32_t act, int32_t y_dtype, const moe_nor
   return MOE_OK;
 }
 
+// Dims of a whole block: a slice's partial sums are added over the devices before any norm.
+int check_block_dims(const moe_dims* d) {
+  const int st = check_dims(d);
+  return st == MOE_OK && d->n_local != d->E ? MOE_ERR_UNSUPPORTED : st;
+}
+
 // Workspace of a block: the layer's, then its input and output.
 struct BlockLayout {
   size_t y, x, total;
@@ -720,14 +726,14 @@ int moe_block_norm(int32_t T, int32_t D, int32_t act_dtype, int32_t y_dtype, con
 }
 
 size_t moe_block_workspace_bytes(const moe_dims* dims) {
-  if (check_dims(dims) != MOE_OK) return 0;
+  if (check_block_dims(dims) != MOE_OK) return 0;
   return block_layout(*dims).total;
 }
 
 int moe_block_forward(const moe_dims* dims, const moe_weights* weights, const void* w_in, const void* x_in,
                       const float* logit_bias, const moe_norm* n, const void* r, void* r_out, void* x_next, void* ws,
                       size_t ws_bytes, void* stream) {
-  int st = check_dims(dims);
+  int st = check_block_dims(dims);
   if (st != MOE_OK) return st;
   const moe_dims& d = *dims;
   if (!r || !ws || (w_in == nullptr) == (x_in == nullptr)) return MOE_ERR_NULL_ARG;

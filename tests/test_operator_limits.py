@@ -126,3 +126,21 @@ def test_a_refused_layer_call_writes_nothing():
     assert all((t == 7).all() for t in outs)
     moe.moe_layer_forward(d, moe.make_weights(router, gate, up, down), x, None, None, y, logits, blob, ws)
     assert torch.isfinite(y.float()).all() and (y != 7).any()
+
+
+# ---------------------------------------------------------------------------
+# An expert slice
+# ---------------------------------------------------------------------------
+
+def test_the_block_refuses_an_expert_slice():
+    """The layer of a slice gives partial sums, to be added over the devices before any norm."""
+    lib = moe.library()
+    n = moe.moe_norm(None, None, None, 0, 1.0, 1e-6)
+    w = _layer_weights(None)
+    for T in (4, 40):
+        for begin, local in ((0, 4), (4, 4), (1, 7)):
+            d = moe.make_dims(T, 64, 8, 2, 64, 0, begin, local, layout="packed")
+            assert lib.moe_block_forward(ctypes.byref(d), ctypes.byref(w), FAKE, None, None, ctypes.byref(n), FAKE, FAKE,
+                                         None, FAKE, 1 << 30, None) == moe.ERR_UNSUPPORTED
+            assert lib.moe_block_workspace_bytes(ctypes.byref(d)) == 0
+            assert moe.moe_workspace_bytes(d) > 0
