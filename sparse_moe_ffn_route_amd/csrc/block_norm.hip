@@ -10,6 +10,7 @@
 // value.  Measured, bf16 rows of 4096 with a gate for every value: 8192 rows (336 MB) in 58 us, 5.8 TB/s (a device
 // copy reaches 4.9; 60 us with loads through the caches' ordinary replacement; alternating between two such
 // inputs 52 against 60, and 57 with the stores past it, too); one row in 3 us, a few memory latencies.
+#include <algorithm>
 #include <type_traits>
 
 #include "common.hpp"
@@ -62,6 +63,7 @@ __device__ __forceinline__ void store_v(void* base, int64_t idx, const float (&v
 }
 
 constexpr int kThreads = 256;
+constexpr int kGridX = 1 << 20;  // rows per grid row: a grid dimension holds less than 2^32 threads
 
 __device__ __forceinline__ float block_sum(float v, float* red) {
   v = wave_sum(v);
@@ -80,7 +82,8 @@ __global__ __launch_bounds__(kThreads) void block_norm_kernel(BlockNorm p) {
   // Short rows: weights and gate are requested with the row, so that a call of few rows waits for
   // memory once rather than after each sum; longer rows keep the registers.
   constexpr bool kEarly = NC * V <= 16;
-  const int64_t row = blockIdx.x;
+  const int64_t row = static_cast<int64_t>(blockIdx.y) * kGridX + blockIdx.x;
+  if (row >= p.T) return;
   const int64_t base = row * p.D;
   const bool gated = p.gate_kind >= kGateChannel;
   Chunk<YEL, V> yc[NC];
@@ -157,7 +160,8 @@ __global__ __launch_bounds__(kThreads) void block_norm_kernel(BlockNorm p) {
 
 template <int EL, int YEL, int V>
 hipError_t launch_v(const BlockNorm& p, hipStream_t stream) {
-  const dim3 grid(static_cast<uint32_t>(p.T)), block(kThreads);
+  const dim3 grid(static_cast<uint32_t>(std::min(p.T, kGridX)), (static_cast<uint32_t>(p.T) + kGridX - 1) / kGridX);
+  const dim3 block(kThreads);
   const int nc = (p.D + kThreads * V - 1) / (kThreads * V);
 #define MOE_NORM(N_) hipLaunchKernelGGL((block_norm_kernel<EL, YEL, V, N_>), grid, block, 0, stream, p)
   if (nc <= 1) MOE_NORM(1);

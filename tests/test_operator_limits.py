@@ -144,3 +144,32 @@ def test_the_block_refuses_an_expert_slice():
                                          None, FAKE, 1 << 30, None) == moe.ERR_UNSUPPORTED
             assert lib.moe_block_workspace_bytes(ctypes.byref(d)) == 0
             assert moe.moe_workspace_bytes(d) > 0
+
+
+# ---------------------------------------------------------------------------
+# The largest calls
+# ---------------------------------------------------------------------------
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,D", [((1 << 24) + 5, 8), ((1 << 20) + 1, 3)])
+def test_block_norm_of_many_rows(T, D):
+    """2^24 rows are 2^32 threads; the second case ends one row behind a grid row.  Bar as in test_block.py: fp32
+    outputs, one rounding each of y + r and of products with one fp32 root (a sum of at most 8 squares)."""
+    g = torch.Generator(device="cuda").manual_seed(5)
+    y, r = (torch.randn(T, D, generator=g, device="cuda") for _ in range(2))
+    gate = torch.randn(T, generator=g, device="cuda")
+    w = 1 + 0.1 * torch.randn(D, generator=g, device="cuda")
+    r_out, x = (torch.full((T + 1, D), 5.0, device="cuda") for _ in range(2))
+    moe.moe_block_norm(y, r, r_out, w_post=w, gate=gate, gate_kind="token", w_next=w, x_next=x, eps=1e-3)
+    assert (r_out[T] == 5.0).all() and (x[T] == 5.0).all()
+    for a in range(0, T, 1 << 22):
+        b = min(a + (1 << 22), T)
+        rms = lambda v: v / (v.square().mean(1, keepdim=True) + 1e-3).sqrt()  # noqa: E731
+        z = rms(y[a:b].double()) * w * gate[a:b, None]
+        out = r[a:b] + z
+        nxt = rms(out) * w
+        # the roundings of the mean, root, quotient, three products and the sum, and of x's after them
+        lim = 2.0 ** -24 * 24 * (r[a:b].abs() + z.abs())
+        inv = (out.square().mean(1, keepdim=True) + 1e-3).rsqrt()
+        lim_x = lim * inv * w + nxt.abs() * (lim.square().mean(1, keepdim=True).sqrt() * inv + 24 * 2.0 ** -24)
+        assert ((r_out[a:b] - out).abs() <= lim).all() and ((x[a:b] - nxt).abs() <= lim_x).all()
