@@ -334,7 +334,8 @@ int moe_pack_weights(int32_t dtype, int64_t n_mats, int32_t rows, int32_t cols, 
  * with moe_audit on a bf16 layer.
  *
  *   src_dtype / dst_dtype  MOE_F32 or MOE_BF16
- *   n_mats, rows, cols     as in moe_pack_weights: rows a multiple of 16, cols of 64
+ *   n_mats, rows, cols     as in moe_pack_weights: rows a multiple of 16, cols of 64; one matrix below 2^32
+ *                          values, and n_mats * (rows / 16) * ceil(cols / 512) below 2^26 - 3
  *   src, dst               device, at 16-byte aligned addresses (else MOE_ERR_UNSUPPORTED)
  * moe_mx_weight_bytes returns 0 for sizes outside these rules.
  */

@@ -416,12 +416,14 @@ int few_layer(const moe_dims& d, const Layout& L, const moe_weights* w, const vo
 }
 
 // Sizes of 4-bit weight matrices: the kernels address one matrix with 32-bit offsets, and a launch
-// has one workgroup per four (16-row, 512-value) pieces.
+// has one workgroup of 256 threads per four (16-row, 512-value) pieces, of the less than 2^32 threads that
+// a grid dimension holds.
+constexpr int64_t kMxMaxPieces = (1ll << 26) - 4;
 int mx_check(int64_t n_mats, int32_t rows, int32_t cols) {
   if (n_mats < 0 || rows < 0 || cols < 0) return MOE_ERR_BAD_DIMS;
   if (rows % 16 || cols % 64) return MOE_ERR_UNSUPPORTED;
   const int64_t per = static_cast<int64_t>(rows / 16) * mx_groups(cols);
-  if (static_cast<int64_t>(rows) * cols >= (1ll << 32) || (per > 0 && n_mats > (1ll << 32) / per))
+  if (static_cast<int64_t>(rows) * cols >= (1ll << 32) || (per > 0 && n_mats > kMxMaxPieces / per))
     return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }

@@ -173,3 +173,15 @@ def test_block_norm_of_many_rows(T, D):
         inv = (out.square().mean(1, keepdim=True) + 1e-3).rsqrt()
         lim_x = lim * inv * w + nxt.abs() * (lim.square().mean(1, keepdim=True).sqrt() * inv + 24 * 2.0 ** -24)
         assert ((r_out[a:b] - out).abs() <= lim).all() and ((x[a:b] - nxt).abs() <= lim_x).all()
+
+
+def test_pack_and_unpack_refuse_what_a_grid_cannot_hold():
+    """One wave per 16 rows and 512 values: 2^26 of them are 2^32 threads."""
+    lib = moe.library()
+    most = (1 << 26) - 4
+    assert moe.moe_mx_weight_bytes(most, 16, 64) == most * 1280
+    assert moe.moe_mx_weight_bytes(most // 6, 32, 1088) == most // 6 * 2 * (9 * 1024 + 3 * 256)
+    for n, rows, cols in ((most + 1, 16, 64), (1 << 32, 16, 512), (most // 6 + 1, 32, 1088)):
+        assert moe.moe_mx_weight_bytes(n, rows, cols) == 0
+        for f in (lib.moe_mx_pack_weights, lib.moe_mx_unpack_weights):
+            assert f(moe.BF16, n, rows, cols, FAKE, FAKE, None) == moe.ERR_UNSUPPORTED
