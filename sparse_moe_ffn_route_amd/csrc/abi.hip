@@ -244,15 +244,21 @@ int route_tokens(const moe_dims& d, const void* x, const void* w_router, float* 
 // M-tile height of the 4-bit grouped GEMMs, by the average routed rows per expert: up to 16 rows a
 // tile of one unit, above tiles of up to four, so that few experts need a second tile and the weights
 // again (64 experts of 4096 x 1024, gate/up: 25 rows each 45 us with the taller tile, 55 with the
-// shorter; 10 rows 45 both; 10 rows of 1024 x 512 10.1 and 8.6).  Calls that give hardly every CU one of
-// the short tiles' workgroups are bound by how long one takes, and do better with the short ones: 24
-// experts of 704 x 320 at 42 rows 6.1 + 4.7 us against 7.7 + 5.8 (130 workgroups), 8 of 2048 x 1024 at 100 rows
-// 8.9 + 6.2 against 14.2 + 9.8 (230), 16 of 256 x 128 at 625 rows 6.6 + 6.2 against 7.9 + 7.9 (320); but 8 of
-// 4096 x 1024 at 200 rows 24.8 + 16.2 against 19.7 + 13.6 (430).
+// shorter; 10 rows 45 both; 10 rows of 1024 x 512 10.1 and 8.6).  Calls that give the CUs one or two
+// of the short tiles' workgroups each are bound by how long one takes, and do better with the short ones:
+// up to two where the weights fit the L2s (8 x 4 MB), which then serve the second tile, and hardly more
+// than one where they do not.  Short against tall tiles, the whole call in us (workgroups):
+//   below 32 MB: 24 experts of 704 x 320 at 42 rows 13.5 : 15.9 (130), at 210 rows 17.7 : 22.2 (508); 16 of
+//     256 x 128 at 625 rows 15.8 : 19.4 (320); 32 of 1024 x 512 at 110 rows 18.7 : 24.8 (504); past two 128
+//     of 1024 x 256 at 50 rows 27.6 : 27.1 (528), 64 of 1024 x 512 at 50 rows 21.7 : 25.0 (528)
+//   above: 8 of 4096 x 1024 at 100 rows 23.3 : 37.5 (232), at 128 rows 31.4 : 38.6 (288), at 150 rows 32.2 :
+//     30.3 (332), at 300 rows 56.2 : 44.5 (632); 16 at 40 rows 35.5 : 37.0 (224), at 60 rows 49.4 : 39.8
+//     (304, where this rule is wrong), at 120 rows 57.6 : 48.9 (544)
 int mx_bm(const moe_dims& d) {
   const double avg = static_cast<double>(d.T) * d.top_k / d.E;
   const double short_tiles = d.n_local * (avg / 32.0 + 0.5), blocks = (d.I + 127) / 128;  // of gate/up's channels
-  return avg <= 16.0 || short_tiles * blocks <= 320.0 ? 32 : 128;
+  const double weight_bytes = 3.0 * d.n_local * d.D * d.I * 17 / 32;
+  return avg <= 16.0 || short_tiles * blocks <= (weight_bytes <= 32 << 20 ? 512.0 : 320.0) ? 32 : 128;
 }
 
 // M-tile height of the routed grouped GEMMs of these dims.

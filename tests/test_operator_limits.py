@@ -6,9 +6,8 @@ import numpy as np
 import pytest
 import torch
 
-import oracle
 import sparse_moe_ffn_route_amd as moe
-from harness import to_np
+import test_mx
 from test_few import Layer
 
 WORKSPACES = [
@@ -185,3 +184,55 @@ def test_pack_and_unpack_refuse_what_a_grid_cannot_hold():
         assert moe.moe_mx_weight_bytes(n, rows, cols) == 0
         for f in (lib.moe_mx_pack_weights, lib.moe_mx_unpack_weights):
             assert f(moe.BF16, n, rows, cols, FAKE, FAKE, None) == moe.ERR_UNSUPPORTED
+
+
+# ---------------------------------------------------------------------------
+# Tile heights of the 4-bit grouped GEMMs
+# ---------------------------------------------------------------------------
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n,D,I,rows,height", [
+    (64, 4096, 1024, 10, 32), (64, 4096, 1024, 25, 128), (64, 4096, 1024, 160, 128),
+    (24, 704, 320, 42, 32), (16, 256, 128, 625, 32), (32, 1024, 512, 110, 32),   # weights below 32 MB
+    (24, 704, 320, 230, 128),
+    (8, 4096, 1024, 100, 32), (8, 4096, 1024, 128, 32), (8, 4096, 1024, 150, 128),   # above
+])
+def test_tile_height_is_the_faster_one(n, D, I, rows, height):
+    """The grouping writes the M-tile prefix of the height that the GEMMs will take: found in the workspace."""
+    T = n * rows
+    ids = torch.arange(T, dtype=torch.int32) % n
+    ids[: 7 * n] = 0                                           # uneven: the prefixes of the two heights differ
+    blob = torch.stack([ids, torch.ones(T).view(torch.int32)], 1).reshape(T, 2, 1).contiguous().cuda()
+    d = moe.make_dims(T, D, n, 1, I, act="bf16", w="mxfp4", out="bf16", layout="packed")
+    ws = torch.full((moe.moe_workspace_bytes(d),), 0xFF, dtype=torch.uint8, device="cuda")
+    counts, offsets = (torch.empty(n + i, dtype=torch.int32, device="cuda") for i in range(2))
+    perm, inv = (torch.empty(T, dtype=torch.int32, device="cuda") for _ in range(2))
+    moe.moe_permute(d, blob, counts, offsets, perm, inv, ws=ws)
+    words = ws.cpu().numpy().view(np.int32)
+    c = counts.cpu().numpy()
+    found = []
+    for h in (32, 128):
+        want = np.concatenate([[0], np.cumsum(-(-c // h))])
+        places = range(0, len(words) - n, 64)                  # parts of a workspace begin at 256 bytes
+        found.append(any((words[p:p + n + 1] == want).all() for p in places if words[p + n] == want[n]))
+    assert found == [height == 32, height == 128]
+
+
+TALL = [130, 1, 128, 0, 300, 64, 97, 33, 96, 160, 129, 5]          # one to four units, one tile of a group or several
+WIDE = [70, 128, 31, 200, 0, 160, 257, 65, 96, 40, 100, 150]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("gathered", [True, False])
+@pytest.mark.parametrize("counts,D,I,out", [(TALL * 3, 576, 576, "bf16"), (TALL * 3, 1088, 576, "f32"),
+                                            (WIDE * 2, 128, 1088, "bf16"), (WIDE * 2, 704, 1088, "f32")])
+def test_grouped_ffn_in_tall_tiles(counts, D, I, out, gathered):
+    """More than two short tiles' workgroups per CU: rows resident or through the ring, in either launch."""
+    assert len(counts) * (sum(counts) / len(counts) / 32 + 0.5) * -(-I // 128) > 512
+    test_mx.test_grouped_ffn(counts, D, I, out, gathered)
+
+
+@pytest.mark.gpu
+def test_layer_forward_in_tall_tiles():
+    assert 32 * (900 * 4 / 32 / 32 + 0.5) * 5 > 512
+    test_mx.test_layer_forward(900, 256, 32, 4, 640, 64, 0, 32, False)
