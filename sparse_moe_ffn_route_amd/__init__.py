@@ -165,10 +165,22 @@ def _stream(stream) -> int:
     return stream.cuda_stream
 
 
-def _on_current_device(t: torch.Tensor, what: str):
-    """The library launches on the current device: refuse a tensor of another one."""
-    if t.is_cuda and t.get_device() != torch.cuda.current_device():
-        raise ValueError(f"{what} is on cuda:{t.get_device()}, the current device is cuda:{torch.cuda.current_device()}")
+def _device() -> int:
+    """The current device, on which the library launches (-2 before any tensor can be on one)."""
+    return torch._C._cuda_getDevice() if torch.cuda.is_initialized() else -2
+
+
+def _here(t: Optional[torch.Tensor], what: str, device: int):
+    """_ptr of a tensor that has to be on this device, the current one."""
+    if t is None:
+        return None
+    if t.get_device() != device:
+        if t.is_cuda:
+            raise ValueError(f"{what} is on cuda:{t.get_device()}, the current device is cuda:{device}")
+        raise ValueError("tensors must live in GPU memory")
+    if not t.is_contiguous():
+        raise ValueError("tensors must be contiguous")
+    return t.data_ptr()
 
 
 def _check(status: int, what: str):
@@ -366,7 +378,6 @@ def moe_mx_weight_bytes(n_mats: int, rows: int, cols: int) -> int:
 
 def moe_mx_pack_weights(src: torch.Tensor, dst: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Round [n][rows][cols] (or [rows][cols]) fp32 or bf16 weights to microscaled FP4 images, uint8 [n][bytes]."""
-    _on_current_device(src, "src")
     n, rows, cols = _mats(src)
     if src.dtype not in (torch.float32, torch.bfloat16):
         raise ValueError("weights must be float32 or bfloat16")
@@ -374,15 +385,15 @@ def moe_mx_pack_weights(src: torch.Tensor, dst: Optional[torch.Tensor] = None, s
     if dst is None:
         dst = torch.empty(n, nbytes, dtype=torch.uint8, device=src.device)
     _need(dst, n * nbytes, "images")
-    _check(library().moe_mx_pack_weights(_CODE_OF_TORCH[src.dtype], n, rows, cols, _ptr(src), _ptr(dst),
-                                         _stream(stream)), "moe_mx_pack_weights")
+    at = _device()
+    _check(library().moe_mx_pack_weights(_CODE_OF_TORCH[src.dtype], n, rows, cols, _here(src, "src", at),
+                                         _here(dst, "dst", at), _stream(stream)), "moe_mx_pack_weights")
     return dst
 
 
 def moe_mx_unpack_weights(images: torch.Tensor, rows: int, cols: int, dtype: torch.dtype = torch.bfloat16,
                           dst: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """The values of n images (uint8 [n][bytes]) as [n][rows][cols] of float32 or bfloat16."""
-    _on_current_device(images, "images")
     nbytes = moe_mx_weight_bytes(1, rows, cols)
     n = images.numel() // nbytes if nbytes else images.shape[0]
     if dst is None:
@@ -392,25 +403,28 @@ def moe_mx_unpack_weights(images: torch.Tensor, rows: int, cols: int, dtype: tor
     if images.dtype != torch.uint8 or images.numel() != n * nbytes:
         raise ValueError(f"images must be uint8, {nbytes} bytes each")
     _need(dst, n * rows * cols * dst.element_size(), "values")
-    _check(library().moe_mx_unpack_weights(_CODE_OF_TORCH[dst.dtype], n, rows, cols, _ptr(images), _ptr(dst),
-                                           _stream(stream)), "moe_mx_unpack_weights")
+    at = _device()
+    _check(library().moe_mx_unpack_weights(_CODE_OF_TORCH[dst.dtype], n, rows, cols, _here(images, "images", at),
+                                           _here(dst, "dst", at), _stream(stream)), "moe_mx_unpack_weights")
     return dst
 
 
 def moe_layer_forward_few(dims, weights: moe_weights, x, packed_in, logit_bias, y, logits_out=None, packed_out=None,
                           ws=None, stream=None):
     """moe_layer_forward for up to FEW_MAX_T tokens, in two launches after the router's."""
-    _on_current_device(x, "x")
     _check_io(dims, x=x, logits=logits_out, packed=packed_in, bias=logit_bias, y=y)
     _need(packed_out, dims.T * 2 * dims.top_k * 4, "packed_out")
-    _check(library().moe_layer_forward_few(ctypes.byref(dims), ctypes.byref(weights), _ptr(x), _ptr(packed_in),
-                                           _ptr(logit_bias), _ptr(y), _ptr(logits_out), _ptr(packed_out), _ptr(ws),
+    at = _device()
+    _check(library().moe_layer_forward_few(ctypes.byref(dims), ctypes.byref(weights), _here(x, "x", at),
+                                           _here(packed_in, "packed_in", at), _here(logit_bias, "logit_bias", at),
+                                           _here(y, "y", at), _here(logits_out, "logits_out", at),
+                                           _here(packed_out, "packed_out", at), _here(ws, "ws", at),
                                            ws.numel() if ws is not None else 0, _stream(stream)),
            "moe_layer_forward_few")
 
 
-def _make_norm(T, D, act, w_post, gate, gate_kind, res_scale, eps, w_next) -> moe_norm:
-    """moe_norm after checks of its tensors' types and sizes."""
+def _check_norm(T, D, act, w_post, gate, gate_kind, w_next) -> int:
+    """Checks of the types and sizes of moe_norm's tensors; the gate's kind."""
     if gate_kind is None:
         if gate is not None and gate.dim() != 2:
             raise ValueError("a one-dimensional gate needs gate_kind 'token' or 'channel'")
@@ -425,7 +439,12 @@ def _make_norm(T, D, act, w_post, gate, gate_kind, res_scale, eps, w_next) -> mo
         _need(gate, T * 4, "gate")
     elif gate is not None:
         _need_like(gate, row if kind == GATE_CHANNEL else T * row, act, "gate")
-    return moe_norm(_ptr(w_post), _ptr(gate), _ptr(w_next), kind, res_scale, eps)
+    return kind
+
+
+def _make_norm(w_post, gate, w_next, kind, res_scale, eps, at) -> moe_norm:
+    return moe_norm(_here(w_post, "w_post", at), _here(gate, "gate", at), _here(w_next, "w_next", at), kind, res_scale,
+                    eps)
 
 
 def _need_like(t: Optional[torch.Tensor], nbytes: int, dtype: torch.dtype, what: str):
@@ -442,18 +461,21 @@ def moe_block_norm(y, r, r_out=None, w_post=None, gate=None, gate_kind=None, res
     """Leave a block and enter the next on the residual stream r [T][D]; y None: only enter."""
     if r.dim() != 2:
         raise ValueError("r must be [T][D]")
-    _on_current_device(r, "r")
     T, D = r.shape
     act = r.dtype
-    n = _make_norm(T, D, act, w_post, gate, gate_kind, res_scale, eps, w_next)
+    kind = _check_norm(T, D, act, w_post, gate, gate_kind, w_next)
     _need_like(r_out, r.nbytes, act, "r_out")
     _need_like(x_next, r.nbytes, act, "x_next")
     y_code = F32
     if y is not None:
         y_code = _CODE_OF_TORCH.get(y.dtype, -1)
         _need(y, T * D * y.element_size(), "y")
-    _check(library().moe_block_norm(T, D, _CODE_OF_TORCH.get(act, -1), y_code, ctypes.byref(n), _ptr(y), _ptr(r),
-                                    _ptr(r_out), _ptr(x_next), _stream(stream)), "moe_block_norm")
+    at = _device()
+    n = _make_norm(w_post, gate, w_next, kind, res_scale, eps, at)
+    _check(library().moe_block_norm(T, D, _CODE_OF_TORCH.get(act, -1), y_code, ctypes.byref(n), _here(y, "y", at),
+                                    _here(r, "r", at), _here(r_out, "r_out", at), _here(x_next, "x_next", at),
+                                    _stream(stream)),
+           "moe_block_norm")
 
 
 def block_workspace(dims: moe_dims, device="cuda") -> torch.Tensor:
@@ -468,17 +490,19 @@ def moe_block_forward(dims, weights: moe_weights, r, r_out, w_in=None, x_in=None
                       gate=None, gate_kind=None, res_scale=1.0, eps=1e-6, w_next=None, x_next=None, ws=None,
                       stream=None):
     """Pre-norm (or x_in), the layer, and moe_block_norm on the residual stream r."""
-    _on_current_device(r, "r")
     T, D, act = dims.T, dims.D, _TORCH_OF.get(dims.act_dtype)
-    n = _make_norm(T, D, act, w_post, gate, gate_kind, res_scale, eps, w_next)
+    kind = _check_norm(T, D, act, w_post, gate, gate_kind, w_next)
     row = D * _ELEM_BYTES.get(dims.act_dtype, 0)
     for t, what in ((r, "r"), (r_out, "r_out"), (x_next, "x_next"), (x_in, "x_in")):
         _need_like(t, T * row, act, what)
     _need_like(w_in, row, act, "w_in")
     _need(logit_bias, dims.E * 4, "logit bias")
-    _check(library().moe_block_forward(ctypes.byref(dims), ctypes.byref(weights), _ptr(w_in), _ptr(x_in),
-                                       _ptr(logit_bias), ctypes.byref(n), _ptr(r), _ptr(r_out), _ptr(x_next),
-                                       _ptr(ws), ws.numel() if ws is not None else 0, _stream(stream)),
+    at = _device()
+    n = _make_norm(w_post, gate, w_next, kind, res_scale, eps, at)
+    _check(library().moe_block_forward(ctypes.byref(dims), ctypes.byref(weights), _here(w_in, "w_in", at),
+                                       _here(x_in, "x_in", at), _here(logit_bias, "logit_bias", at), ctypes.byref(n),
+                                       _here(r, "r", at), _here(r_out, "r_out", at), _here(x_next, "x_next", at), _here(ws, "ws", at),
+                                       ws.numel() if ws is not None else 0, _stream(stream)),
            "moe_block_forward")
 
 

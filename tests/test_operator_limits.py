@@ -236,3 +236,78 @@ def test_grouped_ffn_in_tall_tiles(counts, D, I, out, gathered):
 def test_layer_forward_in_tall_tiles():
     assert 32 * (900 * 4 / 32 / 32 + 0.5) * 5 > 512
     test_mx.test_layer_forward(900, 256, 32, 4, 640, 64, 0, 32, False)
+
+
+# ---------------------------------------------------------------------------
+# Tensors of another device
+# ---------------------------------------------------------------------------
+
+class _On0(torch.Tensor):
+    """A host tensor that says it lives on device 0: host checks only."""
+
+    def get_device(self):
+        return 0
+
+    is_cuda = True
+
+
+class _On1(_On0):
+    def get_device(self):
+        return 1
+
+
+class _Calls:
+    """In place of the library: counts what reaches it."""
+
+    def __init__(self):
+        self.n = 0
+
+    def moe_mx_weight_bytes(self, n, rows, cols):
+        return n * (rows // 16) * 1280
+
+    def __getattr__(self, name):
+        def call(*args):
+            self.n += 1
+            return moe.OK
+        return call
+
+
+def _bf(*shape):
+    return torch.zeros(shape, dtype=torch.bfloat16)
+
+
+def _device_cases():
+    d = moe.make_dims(4, 64, 8, 2, 64)
+    i32, f32, u8 = torch.int32, torch.float32, torch.uint8
+    w = moe.moe_weights()
+    few = dict(x=_bf(4, 64), packed_in=torch.zeros(4, 2, 2, dtype=i32), logit_bias=torch.zeros(8), y=_bf(4, 64),
+               logits_out=torch.zeros(4, 8), packed_out=torch.zeros(4, 2, 2, dtype=i32), ws=torch.zeros(64, dtype=u8))
+    norm = dict(y=_bf(4, 64), r=_bf(4, 64), r_out=_bf(4, 64), w_post=_bf(64), gate=torch.zeros(4, dtype=f32),
+                w_next=_bf(64), x_next=_bf(4, 64))
+    block = dict(r=_bf(4, 64), r_out=_bf(4, 64), w_in=_bf(64), x_in=_bf(4, 64), logit_bias=torch.zeros(8), w_post=_bf(64),
+                 gate=torch.zeros(4, dtype=f32), w_next=_bf(64), x_next=_bf(4, 64), ws=torch.zeros(64, dtype=u8))
+    return [
+        (lambda **t: moe.moe_layer_forward_few(d, w, **t), few),
+        (lambda **t: moe.moe_block_norm(**t, gate_kind="token"), norm),
+        (lambda **t: moe.moe_block_forward(d, w, **t, gate_kind="token"), block),
+        (moe.moe_mx_pack_weights, dict(src=_bf(16, 64), dst=torch.zeros(1280, dtype=u8))),
+        (lambda **t: moe.moe_mx_unpack_weights(rows=16, cols=64, **t), dict(images=torch.zeros(1280, dtype=u8), dst=_bf(16, 64))),
+    ]
+
+
+@pytest.mark.parametrize("case", range(5))
+def test_every_tensor_is_on_the_current_device(case, monkeypatch):
+    calls = _Calls()
+    monkeypatch.setattr(moe, "library", lambda: calls)
+    monkeypatch.setattr(moe, "_stream", lambda stream: 0)
+    monkeypatch.setattr(moe, "_device", lambda: 0)
+    call, tensors = _device_cases()[case]
+    near = {k: v.as_subclass(_On0) for k, v in tensors.items()}
+    call(**near)
+    assert calls.n == 1
+    for name, t in tensors.items():
+        with pytest.raises(ValueError, match=f"{name} .*cuda:1"):
+            call(**{**near, name: t.as_subclass(_On1)})
+    assert calls.n == 1
+    with pytest.raises(ValueError, match="GPU memory"):
+        call(**{**near, next(iter(tensors)): next(iter(tensors.values()))})
