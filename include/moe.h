@@ -58,7 +58,9 @@ enum moe_dtype {
   MOE_BF16 = 1, /* bfloat16 */
   MOE_E4M3 = 2, /* OCP FP8 E4M3 (max 448, no infinities), weights only, with fp32 scales */
   MOE_MXFP4 = 3 /* OCP microscaled FP4: E2M1 codes, one power of two per 32 values of the reduction
-                   dimension; routed expert weights only, as images written by moe_mx_pack_weights */
+                   dimension; routed expert weights only, as images written by moe_mx_pack_weights.
+                   moe_grouped_ffn, moe_layer_forward and moe_layer_forward_noalloc round x and h
+                   of the routed experts to the same 4 bits, moe_layer_forward_few does not */
 };
 
 /* Return codes. */
@@ -405,7 +407,9 @@ int moe_block_norm(int32_t T, int32_t D, int32_t act_dtype, int32_t y_dtype, con
  * A whole block around the residual stream r:
  *   x = rms(r) * w_in (rounded to act_dtype), or x_in, the x_next of the block before;
  *   y = the layer of x, routed by it: moe_layer_forward_few where it takes the dims (up to
- *       MOE_FEW_MAX_T tokens), else moe_layer_forward, rounded to out_dtype;
+ *       MOE_FEW_MAX_T tokens), else moe_layer_forward, rounded to out_dtype.  The two differ in what they
+ *       round: above MOE_FEW_MAX_T tokens h and the experts' rows are rounded as in moe_layer_forward, and
+ *       with MOE_E4M3 or MOE_MXFP4 experts x and h to 8 or 4 bits;
  *   r_out, x_next as moe_block_norm(n, y, r).
  * All experts are local (n_local = E, else MOE_ERR_UNSUPPORTED): an expert slice's y is a partial sum, which goes
  * through moe_layer_forward and the sum over the devices before moe_block_norm.
@@ -485,7 +489,8 @@ int moe_last_hip_error(void);
 
 /* ABI version of this header: 4 (3: MOE_STAGE_EVENTS became 7, with a mark after the shared
  * expert; moe_audit and moe_audit_workspace_bytes were added; 4: the workspace error word,
- * moe_layer_forward_noalloc and moe_mfma_peak_probe). */
+ * moe_layer_forward_noalloc and moe_mfma_peak_probe).  MOE_MXFP4, moe_layer_forward_few, moe_block_norm and
+ * moe_block_forward came later within 4: they change no call that was there. */
 int moe_abi_version(void);
 
 #ifdef __cplusplus

@@ -10,6 +10,7 @@
 // value.  Measured, bf16 rows of 4096 with a gate for every value: 8192 rows (336 MB) in 58 us, 5.8 TB/s (a device
 // copy reaches 4.9; 60 us with loads through the caches' ordinary replacement; alternating between two such
 // inputs 52 against 60, and 57 with the stores past it, too); one row in 3 us, a few memory latencies.
+// Rows of a width that is no multiple of 8, or off a 16-byte boundary, one value per access: 8192 rows of 4095 134 us.
 #include <algorithm>
 #include <type_traits>
 

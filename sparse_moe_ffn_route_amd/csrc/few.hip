@@ -18,14 +18,21 @@
 // own (few_mx.hip).
 //
 // The weights' bytes bound all of it, so both large kernels are built as streams: each wave
-// works through its blocks of weight runs with a ring of register buffers, the next blocks'
-// loads in flight over the ends of units, their reductions and barriers.
+// works through its blocks of weight runs with register buffers, the next blocks' loads requested
+// before the ends of units, their reductions and barriers.  In the down kernel they are a ring; in
+// gate/up, as compiled, a batch: the compiler requests a workgroup's first R steps in another order than
+// the later ones, and so waits at the first of every R steps for all loads in flight.
 //
 // Measured, one token of D 4096 and I 1024, 10 of 512 bf16 experts and a shared one (281 MB, 41 us at
 // the chip's 6.8 TB/s streaming read): 59 us; logits 7, gate/up 34, down 17.5.  Inside gate/up
 // the weights stream at 6.5 TB/s from 6 us after the start on: launch and x 1.5, the logits'
 // latency and the selection 4.5.  13 tokens at 16 or so of 64 local e4m3 experts (182 MB, 27 us): 39 to
-// 45 us, by where the allocator puts the matrices.
+// 45 us, by where the allocator puts the matrices.  Row-major weights: 68 us for that token, and 91 against 81
+// for 4 tokens of 8 of 128 e4m3 experts.
+//
+// x of more tokens than the LDS holds beside the reductions is read from memory at each product, behind every
+// weight load in flight: 8 fp32 tokens of 4 of 64 experts (1.30 GB) 231 us, 9 of them (1.42 GB) 314; bf16 at D 7168,
+// 9 tokens (1.24 GB) 229, 10 (1.34 GB) 273.
 #include "few.hpp"
 #include "mx.hpp"
 

@@ -23,7 +23,7 @@ constexpr int kLdsBytes = 160 * 1024;
 // Weight type W (EL_F32, EL_BF16 or EL_E4M3): a "step" is what 16 bytes per lane cover
 // of 16 rows, EPS values of the reduction dimension, of which lane group g holds the
 // EPS / 4 from g * EPS / 4 on.  NX: 16-byte pieces of the other operand per lane and step.
-// Gate/up keeps R steps of both matrices in flight; down blocks are DB steps of one matrix with
+// Gate/up requests R steps of both matrices ahead; down blocks are DB steps of one matrix with
 // their pieces of h, DN of them in the ring: 2 waves per SIMD have 256 registers each.
 template <int W> struct Wt;
 template <> struct Wt<EL_F32> {
@@ -99,7 +99,8 @@ __device__ __forceinline__ void lds_barrier() {
 
 // 16 waves split the width: at D = 4096 each has all its loads (8 steps of 16 experts) in flight at
 // once, so the launch is a few memory latencies long.  (The shared expert's gate/up beside the logits, on CUs
-// that are idle here, made this launch 1.5 us longer and the next hardly shorter.)
+// that are idle here, made this launch 1.5 us longer: one bf16 token 59.0 -> 59.9 us in all, four on 4-bit experts
+// 58.2 -> 56.4.)
 constexpr int kLogitWaves = 16;
 constexpr int kNormWaves = 4;  // parts of a row's sum of squares: the waves of block_norm.hip
 
@@ -472,8 +473,9 @@ template <int W> __host__ __device__ constexpr int x_row_bytes(int D) {
 }
 
 // Units [u0, u1) of 16 channels, one after another by the whole workgroup: wave w multiplies its
-// eighth of the reduction dimension, the parts are added in wave order in LDS.  Each wave keeps
-// R steps in flight: the last R of a unit are replaced by the next unit's first.
+// eighth of the reduction dimension, the parts are added in wave order in LDS.  Each wave requests
+// R steps ahead, the last R of a unit being followed by the next unit's first; as compiled, the first
+// step of each R waits for all of them (few.hip).
 // SHARED: the shared expert, every token a column; else units of entry u / (I / 16), its members
 // the columns.
 template <int W, bool PACKED, bool XLDS, bool SHARED>

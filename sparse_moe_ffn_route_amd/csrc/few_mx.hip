@@ -11,8 +11,11 @@
 // MFMAs per KB and bound both kernels by instruction issue (4.0 TB/s at 4 tokens).
 //
 // Measured, 4 tokens, 8 of 128 experts of D 4096 and I 1024 and a shared bf16 one (221 MB, 33 us at the
-// 6.8 TB/s streaming read): 55 to 57 us; logits 7, gate/up 29 (weights at 6.0 TB/s from 4 to 5 us on, when the
-// experts are known), down 17 (6.6 TB/s after 3).
+// 6.8 TB/s streaming read): 55 to 57 us; traced, logits 7.6, gate/up 30.9 (145 MB; the experts are known 4 to 5 us
+// after its start, 5.5 TB/s from there on), down 17.3 (74 MB; 5.2 TB/s after the first 3).  Gate/up works in batches
+// as the other weights' does (few.hip), and waits a second time in each, where the byte-sized scales of the
+// next one are widened.  Terms past the LDS are read from memory at each product: 8 of 128 experts at D 7168, 8
+// tokens (606 MB) 132 us, 10 (714 MB) 161, 16 (966 MB) 208.
 //
 // Lane g of a column holds, of a step's 128 values, 16 g .. + 15 and 64 + 16 g .. + 15 in its
 // e4m3 operand, and the scale of values 32 g .. + 31.

@@ -13,8 +13,9 @@
 // group) ahead, each reloaded as soon as it has been used; token records are in LDS as the
 // B operand, shared by the workgroup's waves, where they arrive straight from memory.
 //   resident: the tile's rows stay in LDS over their whole width, and the workgroup runs over a
-//             range of channels without a barrier, its weight stream unbroken from one block of
-//             channels to the next;
+//             range of channels without a barrier, the next block's weights requested before the
+//             last one's results are stored (in the down launch's tall tiles, 22 to 24 spilled registers
+//             are reloaded before the stores, which waits for those requests);
 //   ring:     rows too wide for that pass through a ring of LDS buffers, one group each; a
 //             workgroup does one block of channels.
 // Two workgroups of 4 waves per CU cover each other's beginnings and ends.
