@@ -489,7 +489,7 @@ def block_workspace(dims: moe_dims, device="cuda") -> torch.Tensor:
 def moe_block_forward(dims, weights: moe_weights, r, r_out, w_in=None, x_in=None, logit_bias=None, w_post=None,
                       gate=None, gate_kind=None, res_scale=1.0, eps=1e-6, w_next=None, x_next=None, ws=None,
                       stream=None):
-    """Pre-norm (or x_in), the layer, and moe_block_norm on the residual stream r."""
+    """Pre-norm (or x_in), the layer (all experts local), and moe_block_norm on the residual stream r."""
     T, D, act = dims.T, dims.D, _TORCH_OF.get(dims.act_dtype)
     kind = _check_norm(T, D, act, w_post, gate, gate_kind, w_next)
     row = D * _ELEM_BYTES.get(dims.act_dtype, 0)

@@ -26,7 +26,7 @@
 // Measured, one token of D 4096 and I 1024, 10 of 512 bf16 experts and a shared one (281 MB, 41 us at
 // the chip's 6.8 TB/s streaming read): 59 us; logits 7, gate/up 34, down 17.5.  Inside gate/up
 // the weights stream at 6.5 TB/s from 6 us after the start on: launch and x 1.5, the logits'
-// latency and the selection 4.5.  13 tokens at 16 or so of 64 local e4m3 experts (182 MB, 27 us): 39 to
+// latency and the selection 4.5.  13 tokens at 16 or so of 64 local e4m3 experts (182 MB, 27 us): 38 to
 // 45 us, by where the allocator puts the matrices.  Row-major weights: 68 us for that token, and 91 against 81
 // for 4 tokens of 8 of 128 e4m3 experts.
 //
