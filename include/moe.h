@@ -427,6 +427,149 @@ int moe_block_forward(const moe_dims* dims, const moe_weights* weights, const vo
                       size_t ws_bytes, void* stream);
 
 /*
+ * Training the layer.  The calls below are the gradients of the path's steps and the products they are made of; a
+ * whole backward pass, with the rows in the order of moe_permute, is
+ *   moe_unpermute_combine_backward   dy -> d_rows of the expert outputs, d_weights of the routing weights
+ *   moe_grouped_gemm_backward_rows / _weights (down), moe_swiglu_backward, the same for gate and up
+ *   moe_permute_backward             rows' gradients -> d_x
+ *   moe_route_backward               d_weights and the router's losses -> d_logits, which goes through
+ *                                    the two products with one group (the router's matrix)
+ * Tensors of at least 16-byte alignment where a call says so (else MOE_ERR_UNSUPPORTED).
+ */
+
+/* Ragged groups of rows, each with a weight matrix [N][K] of its own, stored [out][in]. */
+typedef struct moe_groups {
+  int32_t n_groups;  /* 1 .. 1024 */
+  int32_t rows;      /* rows that the grouped tensors hold, at most 2^30 */
+  int32_t N, K;      /* multiples of 8, at most 2^20 */
+  int32_t in_dtype;  /* of operands: MOE_F32 or MOE_BF16 */
+  int32_t out_dtype; /* of the result: MOE_F32, or MOE_BF16 with in_dtype MOE_BF16 */
+} moe_groups;
+
+/*
+ * Products grouped by expert with ragged sizes, and both gradients, with fp32 sums and one rounding at the end.  Rows
+ * [offsets[e], offsets[e + 1]) belong to group e:
+ *   moe_grouped_gemm                   out[r][n]    = sum_k a[r][k] w[e][n][k]             (+ add)
+ *   moe_grouped_gemm_backward_rows     d_a[r][k]    = sum_n d_out[r][n] w[e][n][k]         (+ add)
+ *   moe_grouped_gemm_backward_weights  d_w[e][n][k] = sum_{r of e} d_out[r][n] a[r][k]     (+ add)
+ * Rows behind offsets[n_groups] are left as they were; an empty group's d_w is zero (or add).
+ *
+ *   a          [rows][K], or with index [a_rows][K], row r being a[index[r]] (an index outside [0, a_rows) stands for a
+ *              row of zeros; a below 2 GiB then, else MOE_ERR_UNSUPPORTED).  a_rows is not read without index
+ *   index      [rows] int32 or NULL, e.g. moe_permute's perm_token with a = x
+ *   offsets    [n_groups + 1] int32 (device), not decreasing, from 0 to at most rows (values outside are taken as the
+ *              nearest allowed)
+ *   w          [n_groups][N][K]
+ *   d_out      [rows][N]
+ *   add        as the result, or NULL; may be the result's own memory (a running sum of gradients)
+ *   out, d_a, d_w  [rows][N], [rows][K], [n_groups][N][K] of out_dtype; no other overlap with inputs
+ *   ws         at least moe_grouped_gemm_workspace_bytes(groups) bytes (enough for all three; 0 for refused groups)
+ * All tensors but index and offsets at 16-byte aligned addresses.  The order of a sum depends on the sizes in `groups`
+ * alone: calls with the same sizes and rows of a group give the same bits.
+ */
+size_t moe_grouped_gemm_workspace_bytes(const moe_groups* groups);
+int moe_grouped_gemm(const moe_groups* groups, const void* a, int32_t a_rows, const int32_t* index,
+                     const int32_t* offsets, const void* w, const void* add, void* out, void* ws, size_t ws_bytes,
+                     void* stream);
+int moe_grouped_gemm_backward_rows(const moe_groups* groups, const void* d_out, const int32_t* offsets, const void* w,
+                                   const void* add, void* d_a, void* ws, size_t ws_bytes, void* stream);
+int moe_grouped_gemm_backward_weights(const moe_groups* groups, const void* d_out, const void* a, int32_t a_rows,
+                                      const int32_t* index, const int32_t* offsets, const void* add, void* d_w,
+                                      void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Dropout whose mask is made from a counter and never stored.  Philox-4x32-10 (Salmon, Moraes, Dror, Shaw, 2011) with
+ * the seed rng[0] as key and (b, rng[1]) as counter gives 128 bits for block b of 8 consecutive elements of a
+ * tensor (row-major, [rows][I] below); element i of the block is dropped where its 16 bits (word i / 2, low half
+ * first) are below low = round(65536 p), half to even.  A kept element is multiplied by 65536 / (65536 - low); a dropped
+ * one's result is 0 whatever its inputs hold.  So a backward call with the forward call's p and rng has the forward's
+ * mask; give every tensor of a step an rng[1] of its own.
+ *
+ *   p     probability, 0 <= p <= 1 (0: nothing is dropped, rng is not read and may be NULL)
+ *   rng   uint64 [2] in device memory, read when the call runs: a captured graph's replays see new values
+ *
+ * moe_swiglu, the experts' activation between their products:
+ *   h = drop(silu(gate) * up)
+ * moe_swiglu_backward, with the same gate, up, p and rng:
+ *   d_gate = drop(d_h) * up * s (1 + gate (1 - s)),  s = 1 / (1 + e^-gate);   d_up = drop(d_h) * silu(gate)
+ *   and h again, for the gradient of the down projection's weights, unless NULL
+ *   rows, I    any rows >= 0, I >= 1
+ *   ld         elements between rows of gate, up, d_gate and d_up, at least I (two halves of one [rows][2 I] tensor:
+ *              2 I); d_h and h are [rows][I]
+ *   dtype      of every tensor: MOE_F32 or MOE_BF16; fp32 inside, each result rounded once
+ *   n_rows     int32 in device memory or NULL: only the first min(*n_rows, rows) rows are read and written, e.g.
+ *              offsets + n_groups
+ *   d_gate may be gate, d_up may be up and h may be d_h; no other overlap of outputs with inputs.
+ *
+ * moe_dropout, a branch that joins a residual stream (residual NULL: the branch alone, and the gradient of either):
+ *   out = residual + drop(x)
+ *   n elements; out may be x or residual.
+ * Any alignment of their type; 16-byte aligned tensors with I and ld multiples of 8 are read 16 bytes at a time.
+ */
+int moe_swiglu(int64_t rows, int32_t I, int64_t ld, int32_t dtype, const int32_t* n_rows, const void* gate,
+               const void* up, double p, const uint64_t* rng, void* h, void* stream);
+int moe_swiglu_backward(int64_t rows, int32_t I, int64_t ld, int32_t dtype, const int32_t* n_rows, const void* d_h,
+                        const void* gate, const void* up, double p, const uint64_t* rng, void* d_gate, void* d_up,
+                        void* h, void* stream);
+int moe_dropout(int64_t n, int32_t dtype, const void* x, const void* residual, double p, const uint64_t* rng, void* out,
+                void* stream);
+
+/*
+ * Gradient of moe_unpermute_combine:
+ *   d_rows[inv_pos[t][j]] = w[t][j] * dy[t];   d_weights[t][j] = <dy[t], out_rows[inv_pos[t][j]]>, 0 where inv_pos < 0
+ * with fp32 sums.  Rows of d_rows that no slot names are left as they were.  The shared expert's gradient is dy.
+ *
+ *   dy         [T][D] out_dtype
+ *   packed     [T][2][top_k] int32 (weights are read from plane 1)
+ *   inv_pos    [T][top_k] int32, distinct or -1
+ *   out_rows   [T * top_k][D] out_dtype, or NULL (then d_weights is NULL, too)
+ *   d_rows     [T * top_k][D] act_dtype, the operand type of the products that take it; not out_rows' memory
+ *   d_weights  [T][top_k] fp32
+ * dy, out_rows and d_rows at 16-byte aligned addresses.
+ *
+ * moe_permute_backward, the gradient of moe_permute's x_perm (and of products that gather x by perm_token):
+ *   d_x[t] = sum_{j : inv_pos[t][j] >= 0} d_x_perm[inv_pos[t][j]]  (+ add[t])
+ * summed in fp32 in slot order, add last, rounded once.  d_x_perm [T * top_k][D], add [T][D] or NULL and d_x [T][D]
+ * are act_dtype at 16-byte aligned addresses; d_x may be add.
+ */
+int moe_unpermute_combine_backward(const moe_dims* dims, const void* dy, const int32_t* packed, const int32_t* inv_pos,
+                                   const void* out_rows, void* d_rows, float* d_weights, void* stream);
+int moe_permute_backward(const moe_dims* dims, const void* d_x_perm, const int32_t* inv_pos, const void* add, void* d_x,
+                         void* stream);
+
+/*
+ * The router's losses and the gradient of its logits.  With key = logits + logit_bias, prob[t] = softmax of a token's
+ * keys over all E, lse[t] the log of the sum of their exponentials, n the tokens whose mask is set and load[e] the
+ * slots of those tokens that name expert e:
+ *   loss[0] = E sum_e load[e] / (top_k n) * (1/n) sum_t prob[t][e]      (load balance, 1 if all are equal)
+ *   loss[1] = (1/n) sum_t lse[t]^2                                      (size of the logits)
+ * over the tokens of the mask; both 0 if there are none.  moe_route_backward adds up, per logit,
+ *   renormalize = 1:  w_j (dw_j - sum_i w_i dw_i) at the expert of slot j;
+ *   renormalize = 0:  prob_e (dw of e's slot, or 0, - sum_i w_i dw_i)
+ *   d_loss[0] * E / (top_k n^2) * prob_e (load_e - sum_f prob_f load_f) + d_loss[1] * (2/n) lse prob_e
+ *                                                                       (tokens of the mask; load held fixed)
+ * dims' T, E, top_k and renormalize are used (all E experts, whatever the local slice).
+ *
+ *   logits     [T][E] fp32 as moe_route wrote or took them;  logit_bias [E] fp32 or NULL.  -inf keys have probability 0;
+ *              a token without a finite key adds nothing.  Masked tokens' logits are not used by the losses
+ *   packed     [T][2][top_k] int32, the routing (ids outside [0, E) count for no expert)
+ *   mask       [T] bytes, 0 = not counted (padding), or NULL: all tokens
+ *   loss       [2] fp32 out;  load [E + 1] int32 out: the loads, then n.  To balance over several devices' tokens, add up
+ *              load over them before moe_route_backward (and scale d_loss as the loss is averaged)
+ *   d_weights  [T][top_k] fp32, or NULL: no gradient from the routing weights (also of masked tokens, as given)
+ *   d_loss     [2] fp32 (device), or NULL: none from the losses, load is not read
+ *   d_logits   [T][E] of d_logits_dtype, MOE_F32 or MOE_BF16
+ *   ws         at least moe_route_loss_workspace_bytes(dims) bytes at a 16-byte aligned address
+ * Sums have a fixed order.  T = 0: losses and load are 0.
+ */
+size_t moe_route_loss_workspace_bytes(const moe_dims* dims);
+int moe_route_loss(const moe_dims* dims, const float* logits, const float* logit_bias, const int32_t* packed,
+                   const uint8_t* mask, float* loss, int32_t* load, void* ws, size_t ws_bytes, void* stream);
+int moe_route_backward(const moe_dims* dims, const float* logits, const float* logit_bias, const int32_t* packed,
+                       const uint8_t* mask, const float* d_weights, const int32_t* load, const float* d_loss,
+                       int32_t d_logits_dtype, void* d_logits, void* stream);
+
+/*
  * Numerical audit: an fp32 shadow of the layer on sampled tokens, compared with the
  * layer's output.  For each sampled token t the reference is
  *   ref[t] = sum_j w[t][j] * W_down (silu(W_gate x_t) * (W_up x_t)) over the local slots
@@ -490,7 +633,7 @@ int moe_last_hip_error(void);
 /* ABI version of this header: 4 (3: MOE_STAGE_EVENTS became 7, with a mark after the shared
  * expert; moe_audit and moe_audit_workspace_bytes were added; 4: the workspace error word,
  * moe_layer_forward_noalloc and moe_mfma_peak_probe).  MOE_MXFP4, moe_layer_forward_few, moe_block_norm and
- * moe_block_forward came later within 4: they change no call that was there. */
+ * moe_block_forward, then the calls for training came later within 4: they change no call that was there. */
 int moe_abi_version(void);
 
 #ifdef __cplusplus

@@ -467,6 +467,69 @@ BlockLayout block_layout(const moe_dims& d) {
   return B;
 }
 
+// Products grouped by expert: rows and matrices are addressed from 64-bit bases with 32-bit offsets inside a tile.
+constexpr int32_t kGroupMaxWidth = 1 << 20;
+int check_groups(const moe_groups* g) {
+  if (!g) return MOE_ERR_NULL_ARG;
+  if (g->n_groups < 1 || g->rows < 0 || g->N < 1 || g->K < 1) return MOE_ERR_BAD_DIMS;
+  if (g->n_groups > kMaxLocalExperts || g->rows > (1 << 30)) return MOE_ERR_UNSUPPORTED;
+  if (g->N % 8 || g->K % 8 || g->N > kGroupMaxWidth || g->K > kGroupMaxWidth) return MOE_ERR_UNSUPPORTED;
+  const bool f32 = g->in_dtype == MOE_F32 && g->out_dtype == MOE_F32;
+  const bool bf16 = g->in_dtype == MOE_BF16 && (g->out_dtype == MOE_BF16 || g->out_dtype == MOE_F32);
+  return f32 || bf16 ? MOE_OK : MOE_ERR_UNSUPPORTED;
+}
+
+GroupGemm group_problem(const moe_groups& g, int dir) {
+  GroupGemm p{};
+  p.n_groups = g.n_groups;
+  p.rows = g.rows;
+  p.w_stride = static_cast<int64_t>(g.N) * g.K;
+  p.cols = dir == kForward ? g.N : g.K;
+  p.red = dir == kForward ? g.K : g.N;
+  p.out_rows = g.N;
+  p.ldp = dir == kForward ? g.K : g.N;
+  p.ldq = g.K;
+  return p;
+}
+
+// dir, its operands p and q as GroupGemm has them; index and src_rows: of a.
+int grouped_gemm(const moe_groups* g, int dir, const void* p, const void* q, int32_t src_rows, const int32_t* index,
+                 const int32_t* offsets, const void* add, void* out, void* ws, size_t ws_bytes, void* stream) {
+  const int st = check_groups(g);
+  if (st != MOE_OK) return st;
+  if (g->rows == 0 && dir != kWeights) return MOE_OK;  // an empty tensor's address may be NULL
+  if (!offsets || !out || (g->rows > 0 && (!p || !q))) return MOE_ERR_NULL_ARG;
+  if (index) {
+    if (src_rows < 0) return MOE_ERR_BAD_DIMS;
+    if (static_cast<int64_t>(src_rows) * g->K * act_size(g->in_dtype) >= (1ll << 31)) return MOE_ERR_UNSUPPORTED;
+  }
+  if (!aligned16(p, q, out, add, ws)) return MOE_ERR_UNSUPPORTED;
+  GroupGemm m = group_problem(*g, dir);
+  const size_t need = group_gemm_workspace(dir, g->in_dtype, m);
+  if (need && !ws) return MOE_ERR_NULL_ARG;
+  if (ws_bytes < need) return MOE_ERR_WORKSPACE;
+  m.p = p; m.q = q; m.out = out; m.add = add; m.offsets = offsets; m.index = index; m.src_rows = src_rows;
+  if (!group_gemm_fits(dir, g->in_dtype, m)) return MOE_ERR_UNSUPPORTED;
+  return hip_status(launch_group_gemm(dir, g->in_dtype, g->out_dtype, m, ws, static_cast<hipStream_t>(stream)));
+}
+
+// What 16 random bits have to reach to keep an element dropped with probability p, and the factor of one that is kept.
+int drop_terms(double p, const uint64_t* rng, int* low, float* factor) {
+  if (!(p >= 0.0 && p <= 1.0)) return MOE_ERR_BAD_DIMS;
+  *low = static_cast<int>(std::nearbyint(p * 65536.0));
+  *factor = *low == 65536 ? 0.0f : static_cast<float>(65536.0 / (65536 - *low));
+  return *low && !rng ? MOE_ERR_NULL_ARG : MOE_OK;
+}
+
+// Sizes and pointers that both directions of the activation share.
+int swiglu_terms(int64_t rows, int32_t I, int64_t ld, int32_t dtype, double p, const uint64_t* rng, SwigluDrop* s) {
+  if (rows < 0 || I < 1 || ld < I) return MOE_ERR_BAD_DIMS;
+  if (dtype != MOE_F32 && dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED;
+  if (rows > (1ll << 40) / ld) return MOE_ERR_UNSUPPORTED;
+  s->rows = rows; s->I = I; s->ld = ld; s->rng = rng;
+  return drop_terms(p, rng, &s->low, &s->factor);
+}
+
 // Static scratch of moe_layer_forward_noalloc.  In host code `scratch` names a host-side
 // stand-in, not device memory: kernels only ever see the device address that
 // hipGetSymbolAddress returns for the current device, looked up once per device.
@@ -769,6 +832,127 @@ int moe_block_forward(const moe_dims* dims, const moe_weights* weights, const vo
            : moe_layer_forward(dims, weights, x, nullptr, logit_bias, y, nullptr, nullptr, ws, B.y, nullptr, stream);
   if (st != MOE_OK) return st;
   return moe_block_norm(d.T, d.D, d.act_dtype, d.out_dtype, n, y, r, r_out, x_next, stream);
+}
+
+size_t moe_grouped_gemm_workspace_bytes(const moe_groups* groups) {
+  if (check_groups(groups) != MOE_OK) return 0;
+  size_t n = 256;
+  for (const int dir : {kForward, kRows, kWeights})
+    n = std::max(n, group_gemm_workspace(dir, groups->in_dtype, group_problem(*groups, dir)));
+  return align_up(n);
+}
+
+int moe_grouped_gemm(const moe_groups* groups, const void* a, int32_t a_rows, const int32_t* index,
+                     const int32_t* offsets, const void* w, const void* add, void* out, void* ws, size_t ws_bytes,
+                     void* stream) {
+  return grouped_gemm(groups, kForward, a, w, a_rows, index, offsets, add, out, ws, ws_bytes, stream);
+}
+
+int moe_grouped_gemm_backward_rows(const moe_groups* groups, const void* d_out, const int32_t* offsets, const void* w,
+                                   const void* add, void* d_a, void* ws, size_t ws_bytes, void* stream) {
+  return grouped_gemm(groups, kRows, d_out, w, 0, nullptr, offsets, add, d_a, ws, ws_bytes, stream);
+}
+
+int moe_grouped_gemm_backward_weights(const moe_groups* groups, const void* d_out, const void* a, int32_t a_rows,
+                                      const int32_t* index, const int32_t* offsets, const void* add, void* d_w,
+                                      void* ws, size_t ws_bytes, void* stream) {
+  return grouped_gemm(groups, kWeights, d_out, a, a_rows, index, offsets, add, d_w, ws, ws_bytes, stream);
+}
+
+int moe_swiglu(int64_t rows, int32_t I, int64_t ld, int32_t dtype, const int32_t* n_rows, const void* gate,
+               const void* up, double p, const uint64_t* rng, void* h, void* stream) {
+  SwigluDrop s{};
+  const int st = swiglu_terms(rows, I, ld, dtype, p, rng, &s);
+  if (st != MOE_OK) return st;
+  if (rows == 0) return MOE_OK;
+  if (!gate || !up || !h) return MOE_ERR_NULL_ARG;
+  s.gate = gate; s.up = up; s.h = h; s.n_rows = n_rows;
+  return hip_status(launch_swiglu(dtype, false, s, static_cast<hipStream_t>(stream)));
+}
+
+int moe_swiglu_backward(int64_t rows, int32_t I, int64_t ld, int32_t dtype, const int32_t* n_rows, const void* d_h,
+                        const void* gate, const void* up, double p, const uint64_t* rng, void* d_gate, void* d_up,
+                        void* h, void* stream) {
+  SwigluDrop s{};
+  const int st = swiglu_terms(rows, I, ld, dtype, p, rng, &s);
+  if (st != MOE_OK) return st;
+  if (rows == 0) return MOE_OK;
+  if (!d_h || !gate || !up || !d_gate || !d_up) return MOE_ERR_NULL_ARG;
+  s.d_h = d_h; s.gate = gate; s.up = up; s.d_gate = d_gate; s.d_up = d_up; s.h = h; s.n_rows = n_rows;
+  return hip_status(launch_swiglu(dtype, true, s, static_cast<hipStream_t>(stream)));
+}
+
+int moe_dropout(int64_t n, int32_t dtype, const void* x, const void* residual, double p, const uint64_t* rng, void* out,
+                void* stream) {
+  if (n < 0) return MOE_ERR_BAD_DIMS;
+  if (dtype != MOE_F32 && dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED;
+  Dropout d{};
+  const int st = drop_terms(p, rng, &d.low, &d.factor);
+  if (st != MOE_OK) return st;
+  if (n == 0) return MOE_OK;
+  if (!x || !out) return MOE_ERR_NULL_ARG;
+  d.x = x; d.residual = residual; d.out = out; d.rng = rng; d.n = n;
+  return hip_status(launch_dropout(dtype, d, static_cast<hipStream_t>(stream)));
+}
+
+int moe_unpermute_combine_backward(const moe_dims* dims, const void* dy, const int32_t* packed, const int32_t* inv_pos,
+                                   const void* out_rows, void* d_rows, float* d_weights, void* stream) {
+  const int st = check_dims(dims);
+  if (st != MOE_OK) return st;
+  const moe_dims& d = *dims;
+  if (d.T == 0) return MOE_OK;
+  if (!dy || !packed || !inv_pos || !d_rows || (out_rows == nullptr) != (d_weights == nullptr)) return MOE_ERR_NULL_ARG;
+  if (!aligned16(dy, out_rows, d_rows)) return MOE_ERR_UNSUPPORTED;
+  CombineGrad p{};
+  p.dy = dy; p.packed = packed; p.inv_pos = inv_pos; p.rows = out_rows; p.d_rows = d_rows; p.d_w = d_weights;
+  p.T = d.T; p.D = d.D; p.k = d.top_k;
+  return hip_status(launch_combine_grad(d.out_dtype, d.act_dtype, p, static_cast<hipStream_t>(stream)));
+}
+
+int moe_permute_backward(const moe_dims* dims, const void* d_x_perm, const int32_t* inv_pos, const void* add, void* d_x,
+                         void* stream) {
+  const int st = check_dims(dims);
+  if (st != MOE_OK) return st;
+  const moe_dims& d = *dims;
+  if (d.T == 0) return MOE_OK;
+  if (!d_x_perm || !inv_pos || !d_x) return MOE_ERR_NULL_ARG;
+  if (!aligned16(d_x_perm, add, d_x)) return MOE_ERR_UNSUPPORTED;
+  return hip_status(launch_combine(d.act_dtype, d_x_perm, nullptr, inv_pos, add, d.T, d.D, d.top_k, d_x,
+                                   static_cast<hipStream_t>(stream)));
+}
+
+size_t moe_route_loss_workspace_bytes(const moe_dims* dims) {
+  return check_dims(dims) == MOE_OK ? route_loss_workspace(dims->T, dims->E) : 0;
+}
+
+int moe_route_loss(const moe_dims* dims, const float* logits, const float* logit_bias, const int32_t* packed,
+                   const uint8_t* mask, float* loss, int32_t* load, void* ws, size_t ws_bytes, void* stream) {
+  const int st = check_dims(dims);
+  if (st != MOE_OK) return st;
+  const moe_dims& d = *dims;
+  if (!loss || !load || !ws || (d.T > 0 && (!logits || !packed))) return MOE_ERR_NULL_ARG;
+  if (ws_bytes < route_loss_workspace(d.T, d.E)) return MOE_ERR_WORKSPACE;
+  if (!aligned16(ws)) return MOE_ERR_UNSUPPORTED;
+  RouteGrad p{};
+  p.logits = logits; p.bias = logit_bias; p.packed = packed; p.mask = mask; p.loss = loss; p.load = load;
+  p.T = d.T; p.E = d.E; p.k = d.top_k;
+  return hip_status(launch_route_loss(p, ws, static_cast<hipStream_t>(stream)));
+}
+
+int moe_route_backward(const moe_dims* dims, const float* logits, const float* logit_bias, const int32_t* packed,
+                       const uint8_t* mask, const float* d_weights, const int32_t* load, const float* d_loss,
+                       int32_t d_logits_dtype, void* d_logits, void* stream) {
+  const int st = check_dims(dims);
+  if (st != MOE_OK) return st;
+  const moe_dims& d = *dims;
+  if (d_logits_dtype != MOE_F32 && d_logits_dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED;
+  if (d.T == 0) return MOE_OK;
+  if (!logits || !packed || !d_logits || (!d_weights && !d_loss) || (d_loss && !load)) return MOE_ERR_NULL_ARG;
+  RouteGrad p{};
+  p.logits = logits; p.bias = logit_bias; p.packed = packed; p.mask = mask; p.d_w = d_weights; p.d_loss = d_loss;
+  p.load = const_cast<int32_t*>(load); p.d_logits = d_logits;
+  p.T = d.T; p.E = d.E; p.k = d.top_k; p.renormalize = d.renormalize;
+  return hip_status(launch_route_grad(d_logits_dtype, p, static_cast<hipStream_t>(stream)));
 }
 
 size_t moe_audit_workspace_bytes(const moe_dims* dims, int32_t n_sample) {

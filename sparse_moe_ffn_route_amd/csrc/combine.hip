@@ -69,7 +69,8 @@ __device__ __forceinline__ void store8(void* base, size_t idx, const float v[8])
   }
 }
 
-template <int OUT>
+// UNIT: every weight is one and packed is not read (the gradient of the permutation).
+template <int OUT, bool UNIT>
 __global__ __launch_bounds__(256) void combine_kernel(const void* __restrict__ out_rows,
                                                       const int32_t* __restrict__ packed,
                                                       const int32_t* __restrict__ inv_pos,
@@ -84,7 +85,7 @@ __global__ __launch_bounds__(256) void combine_kernel(const void* __restrict__ o
   const int col = (wid % chunks) * 512 + lane * 8;
   if (col >= D) return;
   float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  const int32_t* wbits = packed + static_cast<size_t>(t) * 2 * k + k;
+  const int32_t* wbits = UNIT ? nullptr : packed + static_cast<size_t>(t) * 2 * k + k;
   const int32_t* rows = inv_pos + static_cast<size_t>(t) * k;
   // Branch-free issue: every row is read through a resource of its own, and a missing
   // row (no shared expert, a slot without a local row, a slot past k) gets the empty
@@ -115,7 +116,7 @@ __global__ __launch_bounds__(256) void combine_kernel(const void* __restrict__ o
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
       if (r[u] < 0) continue;
-      const float w = __int_as_float(wbits[j0 + u]);
+      const float w = UNIT ? 1.0f : __int_as_float(wbits[j0 + u]);
       float v[8];
       unpack8<OUT>(pc[u], v);
 #pragma unroll
@@ -139,12 +140,11 @@ hipError_t launch_combine(int out_el, const void* out_rows, const int32_t* packe
   const int chunks = (D + 511) / 512;
   const int waves = T * chunks;
   dim3 grid((waves + 3) / 4);
-  if (out_el == EL_BF16)
-    hipLaunchKernelGGL(combine_kernel<EL_BF16>, grid, dim3(256), 0, stream, out_rows, packed, inv_pos, shared_out,
-                       T, D, k, chunks, y);
-  else
-    hipLaunchKernelGGL(combine_kernel<EL_F32>, grid, dim3(256), 0, stream, out_rows, packed, inv_pos, shared_out,
-                       T, D, k, chunks, y);
+  auto launch = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, grid, dim3(256), 0, stream, out_rows, packed, inv_pos, shared_out, T, D, k, chunks, y);
+  };
+  if (out_el == EL_BF16) packed ? launch(combine_kernel<EL_BF16, false>) : launch(combine_kernel<EL_BF16, true>);
+  else packed ? launch(combine_kernel<EL_F32, false>) : launch(combine_kernel<EL_F32, true>);
   return hipGetLastError();
 }
 

@@ -185,4 +185,83 @@ struct BlockNorm {
 };
 hipError_t launch_block_norm(int el, int y_el, const BlockNorm& p, hipStream_t stream);
 
+// Products grouped by expert and their gradients (see group_gemm.hip).  Output tile rows are rows of the groups
+// (kForward, kRows) or of the weight matrices (kWeights).
+enum : int { kForward = 0, kRows = 1, kWeights = 2 };
+struct GroupGemm {
+  const void* p;           // operand of the output's rows: a, d_out, d_out
+  const void* q;           // operand of its columns: w, w, a
+  void* out;
+  const void* add;         // as out, or NULL
+  const int32_t* offsets;  // [n_groups + 1]
+  const int32_t* index;    // source row of each row of a, or NULL (kForward, kWeights)
+  int n_groups, rows, src_rows;  // rows: most rows of all groups; src_rows: rows of a
+  int ldp, ldq;            // elements per row of p and q
+  int64_t w_stride;        // elements per matrix of q (kForward, kRows)
+  int cols;                // output columns
+  int red;                 // reduction length (kForward, kRows)
+  int out_rows;            // rows of an output matrix (kWeights)
+  float* partial;          // set by the launcher: sums of parts of the reduction
+  int64_t part_stride;
+  int parts;
+};
+size_t group_gemm_workspace(int dir, int el, const GroupGemm& p);
+bool group_gemm_fits(int dir, int el, const GroupGemm& p);  // one launch holds the call's tiles
+hipError_t launch_group_gemm(int dir, int el, int out_el, GroupGemm p, void* ws, hipStream_t stream);
+
+// SwiGLU with dropout, its gradient, and dropout on a residual branch (see dropout.hip).
+struct SwigluDrop {
+  const void* gate;     // rows of ld elements
+  const void* up;
+  const void* d_h;      // [rows][I], gradient only
+  void* h;              // [rows][I]; of the gradient: or NULL
+  void* d_gate;         // rows of ld elements
+  void* d_up;
+  const int32_t* n_rows;  // rows in use (device), or NULL: all
+  const uint64_t* rng;    // seed, offset (device)
+  int64_t rows, I, ld;
+  int low;                // of 65536: what the generator's 16 bits have to reach to keep an element
+  float factor;           // of a kept element
+};
+hipError_t launch_swiglu(int el, bool grad, const SwigluDrop& p, hipStream_t stream);
+struct Dropout {
+  const void* x;
+  const void* residual;  // or NULL
+  void* out;
+  const uint64_t* rng;
+  int64_t n;
+  int low;
+  float factor;
+};
+hipError_t launch_dropout(int el, const Dropout& p, hipStream_t stream);
+
+// Gradient of the weighted unpermute-combine (see combine_grad.hip).
+struct CombineGrad {
+  const void* dy;          // [T][D] of y_el
+  const int32_t* packed;   // [T][2][k]
+  const int32_t* inv_pos;  // [T][k]
+  const void* rows;        // [T * k][D] of y_el, or NULL
+  void* d_rows;            // [T * k][D] of row_el
+  float* d_w;              // [T][k] (with rows)
+  int T, D, k;
+};
+hipError_t launch_combine_grad(int y_el, int row_el, const CombineGrad& p, hipStream_t stream);
+
+// Router losses and the gradient of the logits (see route_grad.hip).
+struct RouteGrad {
+  const float* logits;     // [T][E]
+  const float* bias;       // [E] or NULL
+  const int32_t* packed;   // [T][2][k]
+  const uint8_t* mask;     // [T] or NULL
+  const float* d_w;        // [T][k] or NULL
+  const float* d_loss;     // [2] or NULL
+  int32_t* load;           // [E + 1]
+  float* loss;             // [2]
+  void* d_logits;          // [T][E]
+  int T, E, k, renormalize;
+};
+size_t route_loss_workspace(int T, int E);
+hipError_t launch_route_loss(const RouteGrad& p, void* ws, hipStream_t stream);
+hipError_t launch_route_grad(int out_el, const RouteGrad& p, hipStream_t stream);
+
 }  // namespace moe
