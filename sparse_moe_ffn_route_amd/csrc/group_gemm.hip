@@ -11,6 +11,8 @@
 // lane, and only the read from LDS differs: 16 bytes of 8 consecutive reduction indexes, or two transposing
 // reads that each hand 16 lanes the four reduction indexes of their own column.
 #include <algorithm>
+#include <cmath>
+#include <type_traits>
 
 #include "common.hpp"
 #include "kernels.hpp"
@@ -24,13 +26,12 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 
 constexpr uint32_t kOut = 0x80000000u;  // a lane offset past every range: reads zeros, touches no memory
 
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t range_rsrc(const uint8_t* base, int64_t bytes) {
+// Buffer resource of `bytes` bytes from base on, both the same for the whole wave.
+__device__ __forceinline__ u32x4 range_rsrc(const uint8_t* base, int64_t bytes) {
   const uint64_t a = reinterpret_cast<uint64_t>(base);
-  const uint32_t lo = static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<uint32_t>(a)));
-  const uint32_t hi = static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<uint32_t>(a >> 32)));
-  const int n = __builtin_amdgcn_readfirstlane(static_cast<int>(bytes));
-  return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>((static_cast<uint64_t>(hi) << 32) | lo), 0, n,
-                                           0x00020000);
+  return u32x4{static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<uint32_t>(a))),
+               static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<uint32_t>(a >> 32))) & 0xFFFFu,
+               static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<uint32_t>(bytes))), 0x00020000u};
 }
 
 // Waits until this wave's reads of LDS have returned and at most N of its loads are under way.
@@ -38,6 +39,23 @@ template <int N>
 __device__ __forceinline__ void wait_step() {
   static_assert(N >= 0 && N <= 63, "vmcnt is 6 bits");
   __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4));
+}
+
+// buffer_load16_to_lds with the LDS address as a number, as an instruction that the compiler does not count: told of it,
+// the compiler waits for all such loads before every transposing read, which it cannot tell apart from them, and
+// with that for the step that was only just asked for.  The kernel waits for its steps itself.  The first wait is
+// for the scalars' writers, the second for m0's; no other instruction of the kernels here takes m0.
+template <bool NT = false>
+__device__ __forceinline__ void load16_to_lds(const u32x4& r, uint32_t lds_at, uint32_t voff, uint32_t soff) {
+  auto scalar = [](uint32_t v) { return static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(v)); };
+  const uint32_t lds = scalar(lds_at), s = scalar(soff);
+  const u32x4 rs{scalar(r[0]), scalar(r[1]), scalar(r[2]), scalar(r[3])};
+  if constexpr (NT)
+    asm volatile("s_nop 4\n\ts_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen nt lds"
+                 :: "s"(lds), "v"(voff), "s"(rs), "s"(s) : "memory");
+  else
+    asm volatile("s_nop 4\n\ts_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+                 :: "s"(lds), "v"(voff), "s"(rs), "s"(s) : "memory");
 }
 
 // One operand's tile of W tile-index values by a step of RB reduction bytes (along) or RB / ES reduction
@@ -60,7 +78,7 @@ struct Operand {
 
   static __device__ __forceinline__ int turn(int row) {  // in units of 16 values (across) or 16 bytes
     if constexpr (!ACROSS) {
-      return RB == 128 ? row & 7 : (row >> 1) & 3;
+      return RB >= 128 ? row & 7 : (row >> 1) & 3;
     } else if constexpr (EL == EL_F32) {
       return (row >> 2) & 3;
     } else {
@@ -80,26 +98,34 @@ struct Operand {
     else byte = (c ^ turn(row)) * 16;
   }
 
-  // Fragment of tile columns (or rows) 16 * f .. + 15 and reduction chunk ks: lane (g, i) holds 16 bytes of
-  // index 16 * f + i, the reduction values g * (16 / ES) .. of the chunk.
-  static __device__ __forceinline__ u32x4 frag(const uint8_t* lds, int f, int ks) {
+  // Where in the stored tile this lane's part of a fragment lies.  Fragment f is tile indexes 16 * f .. + 15, reduction
+  // chunk ks 64 bytes of each: lane (g, i) holds 16 bytes of index 16 * f + i, the reduction values
+  // g * (16 / ES) .. of the chunk.  The part of the place that the swizzle mixes with f (across) or ks (along) is in
+  // `at`; the rest is a constant that the read's instruction adds.  A wave has the fragments first, first + BY, ...
+  template <int BY, int N>
+  static __device__ __forceinline__ void places(int first, uint32_t (&at)[N]) {
     const int lane = lane_id(), i = lane & 15, g = lane >> 4;
+#pragma unroll
+    for (int x = 0; x < N; ++x) {
+      if constexpr (!ACROSS) at[x] = (first * 16 + i) * RB + (((x * 4 + g) ^ turn(i)) * 16);
+      else if constexpr (EL == EL_F32) at[x] = g * 4 * kRow + (((first + x * BY) ^ turn(g * 4)) * 64) + i * 4;
+      else at[x] = (g * 8 + i / 4) * kRow + (((first + x * BY) ^ turn(g * 8 + i / 4)) * 32) + (i & 3) * 8;
+    }
+  }
+  template <int BY, int N>
+  static __device__ __forceinline__ u32x4 frag(const uint8_t* lds, const uint32_t (&at)[N], int f, int ks) {
     if constexpr (!ACROSS) {
-      return *reinterpret_cast<const u32x4*>(lds + (f * 16 + i) * RB + (((ks * 4 + g) ^ turn(i)) * 16));
+      return *reinterpret_cast<const u32x4*>(lds + at[ks] + f * BY * 16 * RB);
     } else if constexpr (EL == EL_F32) {
       u32x4 v;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int r = ks * 16 + g * 4 + j;
-        v[j] = *reinterpret_cast<const uint32_t*>(lds + r * kRow + ((f ^ turn(r)) * 64) + i * 4);
-      }
+      for (int j = 0; j < 4; ++j) v[j] = *reinterpret_cast<const uint32_t*>(lds + at[f] + (ks * 16 + j) * kRow);
       return v;
     } else {
       typedef __attribute__((address_space(3))) s16x4* lds_ptr;
-      const int r = ks * 32 + g * 8 + i / 4;
-      const uint8_t* at = lds + r * kRow + ((f ^ turn(r)) * 32) + (i & 3) * 8;
-      const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)at);
-      const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(at + 4 * kRow));
+      const uint8_t* p = lds + at[f] + ks * 32 * kRow;
+      const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)p);
+      const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(p + 4 * kRow));
       return __builtin_bit_cast(u32x4, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
     }
   }
@@ -110,6 +136,8 @@ struct Place {
   int g, begin, end;  // group and its rows
   int row0, col0;     // of the tile: kForward, kRows from the group's first row; kWeights within the matrix
   int part;           // of the reduction
+  int high;           // most rows of the tile
+  bool once;          // no other tile reads this one's matrix columns: they bypass the caches' replacement
 };
 
 // Rows of group g, kept inside [0, rows] and in order whatever the offsets hold.
@@ -118,22 +146,26 @@ __device__ __forceinline__ int2 group_rows(const GroupGemm& p, int g) {
   return make_int2(b, min(max(p.offsets[g + 1], b), p.rows));
 }
 
+// Tile row and column of tile i of a group: columns of 8 tile rows at a time, so that the tiles that an XCD has at
+// work together share both operands in its L2.
+__device__ __forceinline__ void tile_at(int i, int m_tiles, int n_tiles, int& row, int& col) {
+  const int block = i / (8 * n_tiles), high = min(8, m_tiles - block * 8), in = i - block * 8 * n_tiles;
+  row = block * 8 + in % high;
+  col = in / high;
+}
+
 // Ragged tile rows: each wave counts the groups' tiles itself (lane l those of groups l * per ..), so that
 // no launch has to come before this one.  False past the last tile.
-template <int BM>
 __device__ __forceinline__ bool find_rows(const GroupGemm& p, int n_tiles, int block, Place& at) {
-  constexpr int kPer = 16;  // 1024 groups over 64 lanes
   const int lane = lane_id(), per = (p.n_groups + 63) / 64;
-  int cnt[kPer], mine = 0;
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    cnt[i] = 0;
-    if (i < per) {  // wave-uniform
-      const int g = lane * per + i;
-      const int2 r = group_rows(p, min(g, p.n_groups - 1));
-      cnt[i] = g < p.n_groups ? (r.y - r.x + BM - 1) / BM : 0;
-      mine += cnt[i];
-    }
+  auto tiles_of = [&](int2 r) { return (r.y - r.x + p.high - 1) / p.high; };
+  int2 r = make_int2(0, 0);  // of the lane's first group
+  int mine = 0;
+  for (int i = 0; i < per; ++i) {
+    const int g = lane * per + i;
+    const int2 v = group_rows(p, min(g, p.n_groups - 1));
+    if (i == 0) r = v;
+    if (g < p.n_groups) mine += tiles_of(v);
   }
   int upto = mine;
 #pragma unroll
@@ -141,35 +173,36 @@ __device__ __forceinline__ bool find_rows(const GroupGemm& p, int n_tiles, int b
     const int v = __shfl_up(upto, o, kWave);
     if (lane >= o) upto += v;
   }
-  const int m_tiles = __builtin_amdgcn_readlane(upto, 63);
-  const int total = m_tiles * n_tiles * p.parts;
+  const int total = __builtin_amdgcn_readlane(upto, 63) * n_tiles * p.parts;
   if (block >= total) return false;
   int L = xcd_remap(block, total);
   at.part = L % p.parts;
   L /= p.parts;
-  const int q = L / n_tiles;  // a group's tiles: columns, then rows, so that q is inside its tile rows
+  const int q = L / n_tiles;  // a group's tiles follow each other, so that q is inside its tile rows
   const int who = __popcll(__ballot(upto <= q));
-  int before = who ? __builtin_amdgcn_readlane(upto, who ? who - 1 : 0) : 0;
-  int g = 0, m = 0, seen = 0;
-  // the lane that holds the group looks through its own
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    if (q - before >= seen && q - before < seen + cnt[i]) { g = lane * per + i; m = cnt[i]; before += seen; seen = 1 << 30; }
-    seen += cnt[i];
+  int before = __builtin_amdgcn_readlane(upto - mine, who), mt = __builtin_amdgcn_readlane(mine, who);
+  at.g = who * per;
+  at.begin = __builtin_amdgcn_readlane(r.x, who);
+  at.end = __builtin_amdgcn_readlane(r.y, who);
+  if (per > 1) {  // the lane's groups in turn, by the whole wave
+    mt = tiles_of(make_int2(at.begin, at.end));
+    while (q >= before + mt) {
+      before += mt;
+      const int2 v = group_rows(p, ++at.g);
+      at.begin = __builtin_amdgcn_readfirstlane(v.x);
+      at.end = __builtin_amdgcn_readfirstlane(v.y);
+      mt = tiles_of(make_int2(at.begin, at.end));
+    }
   }
-  at.g = __builtin_amdgcn_readlane(g, who);
-  const int mt = __builtin_amdgcn_readlane(m, who);
-  const int first = __builtin_amdgcn_readlane(before, who);
-  const int local = L - first * n_tiles;
-  const int2 r = group_rows(p, at.g);
-  at.begin = __builtin_amdgcn_readfirstlane(r.x);
-  at.end = __builtin_amdgcn_readfirstlane(r.y);
-  at.row0 = local % mt * BM;
-  at.col0 = local / mt;
+  at.once = mt == 1;
+  tile_at(L - before * n_tiles, mt, n_tiles, at.row0, at.col0);
+  // a group's tiles share its rows evenly, in steps of a fragment
+  at.high = ((at.end - at.begin + mt - 1) / mt + 15) / 16 * 16;
+  at.row0 *= at.high;
   return true;
 }
 
-template <int EL, int OEL, int DIR, int BM, int BN, int RB, int WM, int WN, int ST, int MINB>
+template <int EL, int OEL, int DIR, int BM, int BN, int RB, int WM, int WN, int ST, int MINB, bool TURNS>
 __global__ __launch_bounds__(WM * WN * 64, MINB) void group_gemm_kernel(GroupGemm p) {
   constexpr int NT = WM * WN * 64;
   constexpr int ES = EL == EL_F32 ? 4 : 2;
@@ -188,17 +221,18 @@ __global__ __launch_bounds__(WM * WN * 64, MINB) void group_gemm_kernel(GroupGem
     int L = xcd_remap(blockIdx.x, gridDim.x);
     at.part = L % p.parts;
     L /= p.parts;
-    at.row0 = L % m_tiles * BM;
-    at.col0 = L / m_tiles % n_tiles;
-    at.g = L / m_tiles / n_tiles;
+    at.g = L / (m_tiles * n_tiles);
+    tile_at(L - at.g * m_tiles * n_tiles, m_tiles, n_tiles, at.row0, at.col0);
+    at.row0 *= BM;
+    at.high = BM;
     const int2 r = group_rows(p, at.g);
     at.begin = __builtin_amdgcn_readfirstlane(r.x);
     at.end = __builtin_amdgcn_readfirstlane(r.y);
   } else {
-    if (!find_rows<BM>(p, n_tiles, blockIdx.x, at)) return;
+    if (!find_rows(p, n_tiles, blockIdx.x, at)) return;
   }
   at.col0 *= BN;
-  const int tile_rows = min(BM, (DIR == kWeights ? p.out_rows : at.end - at.begin) - at.row0);
+  const int tile_rows = min(at.high, (DIR == kWeights ? p.out_rows : at.end - at.begin) - at.row0);
   const int tile_cols = min(BN, p.cols - at.col0);
 
   // this part of the reduction: r0 .. r1
@@ -257,132 +291,235 @@ __global__ __launch_bounds__(WM * WN * 64, MINB) void group_gemm_kernel(GroupGem
     }
   }
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const u32x4 whole_p = range_rsrc(pp, p_bytes), whole_q = range_rsrc(pq, DIR == kWeights ? p.src_rows * ldq : q_bytes);
 
-  // Loads of step s into its LDS buffer.  Steps past the last read nothing and write zeros, so that every step is as
-  // many loads.
-  auto load = [&](int s) {
-    uint8_t* buf = lds + s % ST * kStage + wave * 1024;
-    const int r = r0 + s * STEP;          // first reduction index of the step
-    const int left = max(0, r1 - r);      // reduction indexes left
-    if constexpr (DIR != kWeights) {
-      const __amdgpu_buffer_rsrc_t rp = range_rsrc(pp, p_bytes);
-      const bool in = op.kc < left;
+  // Loads of step s into an LDS buffer.  Steps past the last read nothing and write zeros, so that every
+  // step is as many loads.
+  const uint32_t lds0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) uint8_t*)lds));
+  struct Step {
+    u32x4 rp, rq;
+    uint32_t buf, soff;
+    int r, left;  // first reduction index of the step, indexes from there on
+  };
+  auto step_at = [&](int s, uint32_t buf) {
+    Step t;
+    t.buf = buf + lds0 + wave * 1024;
+    t.r = r0 + s * STEP;
+    t.left = r1 > t.r ? r1 - t.r : 0;
+    t.soff = t.left ? t.r * ES : 0;
+    auto bytes = [&](int64_t ld) { return t.left >= STEP ? STEP * ld : t.left * ld; };
+    t.rp = DIR == kWeights ? range_rsrc(pp + (at.begin + t.r) * ldp, bytes(ldp)) : whole_p;
+    t.rq = DIR == kForward || (DIR == kWeights && p.index) ? whole_q
+           : range_rsrc(pq + (DIR == kWeights ? at.begin + t.r : t.r) * ldq, bytes(ldq));
+    return t;
+  };
+  // kWeights with an index: a wave's load of Q is of kPer whole rows (64 lanes, kChunks lanes a row), whose sources are
+  // the same for the whole wave; they are asked for a step ahead.
+  constexpr int kPer = 64 / Q::kChunks > 0 ? 64 / Q::kChunks : 1;
+  uint32_t row_at[Q::kLoads * kPer];
+  auto rows_ahead = [&](int s) {
+    const int r = r0 + s * STEP, left = r1 > r ? r1 - r : 0;
 #pragma unroll
-      for (int j = 0; j < P::kLoads; ++j)
-        buffer_load16_to_lds(rp, buf + j * NT * 16, in ? op.voff[j] : kOut, left ? r * ES : 0);
-    } else {
-      const __amdgpu_buffer_rsrc_t rp = range_rsrc(pp + (at.begin + r) * ldp, min(left, STEP) * ldp);
-#pragma unroll
-      for (int j = 0; j < P::kLoads; ++j) buffer_load16_to_lds(rp, buf + j * NT * 16, op.voff[j], 0);
+    for (int x = 0; x < Q::kLoads * kPer; ++x) {
+      const int row = (x / kPer * NT + wave * 64) / Q::kChunks + x % kPer;
+      const int v = left ? ld_scalar(p.index + at.begin + r + min(row, left - 1)) : -1;
+      row_at[x] = row < left && static_cast<uint32_t>(v) < static_cast<uint32_t>(p.src_rows) ? v : kOut;
     }
-    uint8_t* qbuf = buf + P::kBytes;
+  };
+  if (DIR == kWeights && p.index) rows_ahead(0);
+  auto load_one = [&](const Step& t, int j) {
+    if (j < P::kLoads) {
+      const uint32_t to = t.buf + j * NT * 16;
+      if constexpr (DIR != kWeights) load16_to_lds(t.rp, to, op.kc < t.left ? op.voff[j] : kOut, t.soff);
+      else load16_to_lds(t.rp, to, op.voff[j], 0);
+      return;
+    }
+    j -= P::kLoads;
+    const uint32_t to = t.buf + P::kBytes + j * NT * 16;
     if constexpr (DIR == kForward) {
-      const __amdgpu_buffer_rsrc_t rq = range_rsrc(pq, q_bytes);
-      const bool in = oq.kc < left;
-#pragma unroll
-      for (int j = 0; j < Q::kLoads; ++j)
-        buffer_load16_to_lds(rq, qbuf + j * NT * 16, in ? oq.voff[j] : kOut, left ? r * ES : 0);
-    } else if constexpr (DIR == kRows) {
-      const __amdgpu_buffer_rsrc_t rq = range_rsrc(pq + r * ldq, min(left, STEP) * ldq);
-#pragma unroll
-      for (int j = 0; j < Q::kLoads; ++j) buffer_load16_to_lds(rq, qbuf + j * NT * 16, oq.voff[j], 0);
-    } else if (!p.index) {
-      const __amdgpu_buffer_rsrc_t rq = range_rsrc(pq + (at.begin + r) * ldq, min(left, STEP) * ldq);
-#pragma unroll
-      for (int j = 0; j < Q::kLoads; ++j) buffer_load16_to_lds(rq, qbuf + j * NT * 16, oq.voff[j], 0);
+      if (RB >= 128 && at.once) load16_to_lds<true>(t.rq, to, oq.kc < t.left ? oq.voff[j] : kOut, t.soff);
+      else load16_to_lds(t.rq, to, oq.kc < t.left ? oq.voff[j] : kOut, t.soff);
     } else {
-      // A wave's load is of kPer whole rows (64 lanes, kChunks lanes a row): their indexes are wave-uniform.
-      constexpr int kPer = 64 / Q::kChunks > 0 ? 64 / Q::kChunks : 1;
-      const __amdgpu_buffer_rsrc_t rq = range_rsrc(pq, p.src_rows * ldq);
-#pragma unroll
-      for (int j = 0; j < Q::kLoads; ++j) {
-        const int row = (j * NT + wave * 64) / Q::kChunks;
+      uint32_t voff = oq.voff[j];
+      if (DIR == kWeights && p.index) {
         const int mine = lane_id() / Q::kChunks;
         uint32_t src = 0;
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-          const int v = left ? ld_scalar(p.index + at.begin + r + min(row + i, left - 1)) : -1;
-          const uint32_t u = row + i < left && static_cast<uint32_t>(v) < static_cast<uint32_t>(p.src_rows) ? v : kOut;
-          src = mine == i ? u : src;
-        }
+        for (int i = 0; i < kPer; ++i) src = mine == i ? row_at[j * kPer + i] : src;
         // voff holds the row's place within the step, too
-        const uint32_t col = oq.voff[j] - static_cast<uint32_t>((row + mine) * ldq);
-        buffer_load16_to_lds(rq, qbuf + j * NT * 16,
-                             src == kOut || oq.voff[j] == kOut ? kOut : static_cast<uint32_t>(src * ldq) + col, 0);
+        const uint32_t col = voff - static_cast<uint32_t>(((j * NT + wave * 64) / Q::kChunks + mine) * ldq);
+        voff = src == kOut || voff == kOut ? kOut : static_cast<uint32_t>(src * ldq) + col;
       }
+      if (DIR == kRows && at.once) load16_to_lds<true>(t.rq, to, voff, 0);
+      else load16_to_lds(t.rq, to, voff, 0);
     }
+  };
+  auto load = [&](int s, uint32_t buf) {
+    const Step t = step_at(s, buf);
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j) load_one(t, j);
+    if (DIR == kWeights && p.index) rows_ahead(s + 1);
   };
 
   // ---- the loop ----------------------------------------------------------------
   const int wm = wave % WM, wn = wave / WM;
+  constexpr int PP = DIR == kWeights ? MF : KS, QP = DIR != kForward ? NF : KS;
+  uint32_t p_at[PP], q_at[QP];
+  P::template places<WM>(wm, p_at);
+  Q::template places<1>(wn * NF, q_at);
+  // Row fragments are dealt to the waves in turn, and those behind the tile's last row are left out.
+  const int live = (tile_rows + 15) / 16 > wm ? ((tile_rows + 15) / 16 - wm + WM - 1) / WM : 0;
   f32x4 acc[MF][NF];
 #pragma unroll
   for (int m = 0; m < MF; ++m)
 #pragma unroll
     for (int n = 0; n < NF; ++n) acc[m][n] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-  for (int s = 0; s < ST - 1; ++s) load(s);
-  for (int s = 0; s < steps; ++s) {
+  for (int s = 0; s < ST - 1; ++s) load(s, s * kStage);
+  uint32_t now = 0, next = (ST - 1) * kStage;  // buffers of this step, and of the one asked for beside it
+  u32x4 fp[MF], fq[NF];
+  auto read = [&](int ks) {
+    const uint8_t* buf = lds + now;
+#pragma unroll
+    for (int n = 0; n < NF; ++n) fq[n] = Q::template frag<1>(buf + P::kBytes, q_at, n, ks);
+#pragma unroll
+    for (int m = 0; m < MF; ++m) fp[m] = P::template frag<WM>(buf, p_at, m, ks);
+  };
+  auto multiply = [&] {
+#pragma unroll
+    for (int m = 0; m < MF; ++m) {
+      if (DIR != kWeights && m >= live) break;
+#pragma unroll
+      for (int n = 0; n < NF; ++n) acc[m][n] = mfma_chunk<EL>(fq[n], fp[m], acc[m][n]);
+    }
+  };
+  auto turn_buffers = [&] {
+    next = now;
+    now = now == (ST - 1) * kStage ? 0 : now + kStage;
+  };
+  if constexpr (TURNS) {
+    const bool second = wave >= WM * WN / 2;
     wait_step<(ST - 2) * kLoads>();
-    bare_barrier();  // the step is in LDS, and every wave is done with the buffer that is filled next
-    load(s + ST - 1);
-    const uint8_t* buf = lds + s % ST * kStage;
+    bare_barrier();
+    if (second) bare_barrier();
+    for (int s = 0; s < steps; ++s) {
 #pragma unroll
-    for (int ks = 0; ks < KS; ++ks) {
-      u32x4 fp[MF], fq[NF];
+      for (int ks = 0; ks < KS; ++ks) {
+        read(ks);
+        if (ks == 0) load(s + ST - 1, next);
+        if (ks == KS - 1 && second) wait_step<(ST - 2) * kLoads>();
+        else wait_step<63>();
+        bare_barrier();
+        __builtin_amdgcn_s_setprio(1);
+        multiply();
+        __builtin_amdgcn_s_setprio(0);
+        if (ks == KS - 1 && !second) wait_step<(ST - 2) * kLoads>();
+        bare_barrier();
+      }
+      turn_buffers();
+    }
+    if (!second) bare_barrier();
+  } else {
+    for (int s = 0; s < steps; ++s) {
+      wait_step<(ST - 2) * kLoads>();
+      bare_barrier();  // the step is in LDS, and every wave is done with the buffer that is filled next
+      load(s + ST - 1, next);
 #pragma unroll
-      for (int n = 0; n < NF; ++n) fq[n] = Q::frag(buf + P::kBytes, wn * NF + n, ks);
-#pragma unroll
-      for (int m = 0; m < MF; ++m) fp[m] = P::frag(buf, wm * MF + m, ks);
-#pragma unroll
-      for (int m = 0; m < MF; ++m)
-#pragma unroll
-        for (int n = 0; n < NF; ++n) acc[m][n] = mfma_chunk<EL>(fq[n], fp[m], acc[m][n]);
+      for (int ks = 0; ks < KS; ++ks) {
+        read(ks);
+        multiply();
+      }
+      turn_buffers();
     }
   }
-  wait_vmcnt<0>();  // no load writes LDS after the workgroup has ended
+  wait_step<0>();   // no load writes LDS any more
+  bare_barrier();
 
-  // ---- out: lane (g, i) holds columns g * 4 .. + 3 of row i of each fragment ------
+  // ---- out -----------------------------------------------------------------------
+  // A lane has four columns of a row in each fragment.  Each wave turns its rows around in a part of LDS of its own, a
+  // few at a time, so that whole lines are added to and written: 16 bytes a lane, consecutive lanes along the row.
+  constexpr int WC = NF * 16;                            // columns of a wave
+  constexpr int kTurnRow = WC * 4 + 16;                  // bytes of a turned row
+  constexpr int kTurnMax = ST * kStage / (WM * WN) / (16 * kTurnRow);
+  constexpr int TF = kTurnMax >= MF ? MF : kTurnMax >= 4 && MF % 4 == 0 ? 4 : kTurnMax >= 2 && MF % 2 == 0 ? 2 : 1;
+  static_assert(kTurnMax >= 1, "a fragment's rows fit the wave's part of LDS");
+  uint8_t* turn = lds + wave * (TF * 16 * kTurnRow);
   const int lane = lane_id(), i = lane & 15, g = lane >> 4;
   const int64_t base = DIR == kWeights ? static_cast<int64_t>(at.g) * p.out_rows : at.begin;
+  const bool whole = p.parts == 1;
+  // Values of a 16-byte piece: of the result, or of a part of the sum in fp32.
+  auto rows_out = [&](auto width) {
+    constexpr int V = decltype(width)::value, kLanes = WC / V, kRows = 64 / kLanes, kPieces = TF * 16 / kRows;
+    const int c = lane % kLanes * V, col = wn * WC + c;
+    const bool here = col < tile_cols;
+    auto row_of = [&](int m0, int x) {
+      const int r = x * kRows + lane / kLanes;
+      return ((m0 + r / 16) * WM + wm) * 16 + r % 16;
+    };
+    auto place = [&](int row) { return (base + at.row0 + row) * p.cols + at.col0 + col; };
+    // what is added is asked for one pass ahead
+    u32x4 more[2][kPieces];
+    const bool adds = whole && p.add;
+    auto fetch = [&](int m0, u32x4 (&to)[kPieces]) {
+      if (!adds) return;
 #pragma unroll
-  for (int m = 0; m < MF; ++m) {
-    const int r = (wm * MF + m) * 16 + i;
-    if (r >= tile_rows) continue;
-    const int64_t row = (base + at.row0 + r) * p.cols + at.col0;
-#pragma unroll
-    for (int n = 0; n < NF; ++n) {
-      const int c = (wn * NF + n) * 16 + g * 4;
-      if (c >= tile_cols) continue;
-      const f32x4 v = acc[m][n];
-      if (p.parts > 1) {
-        *reinterpret_cast<f32x4*>(p.partial + at.part * p.part_stride + row + c) = v;
-      } else if constexpr (OEL == EL_F32) {
-        f32x4 o = v;
-        if (p.add) o += *reinterpret_cast<const f32x4*>(static_cast<const float*>(p.add) + row + c);
-        *reinterpret_cast<f32x4*>(static_cast<float*>(p.out) + row + c) = o;
-      } else {
-        f32x4 o = v;
-        if (p.add) {
-          const uint2 b = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p.add) + row + c);
-          o += f32x4{bf16_bits_to_f32(b.x & 0xFFFFu), __uint_as_float(b.x & 0xFFFF0000u), bf16_bits_to_f32(b.y & 0xFFFFu),
-                     __uint_as_float(b.y & 0xFFFF0000u)};
-        }
-        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + row + c) =
-            make_uint2(bf16x2_bits(o[0], o[1]), bf16x2_bits(o[2], o[3]));
+      for (int x = 0; x < kPieces; ++x) {
+        const int row = row_of(m0, x);
+        to[x] = here && row < tile_rows ? *reinterpret_cast<const u32x4*>(static_cast<const uint8_t*>(p.add) + place(row) * (16 / V)) : u32x4{};
       }
+    };
+    fetch(0, more[0]);
+#pragma unroll
+    for (int m0 = 0; m0 < MF; m0 += TF) {
+#pragma unroll
+      for (int m = 0; m < TF; ++m)
+#pragma unroll
+        for (int n = 0; n < NF; ++n)
+          *reinterpret_cast<f32x4*>(turn + (m * 16 + i) * kTurnRow + (n * 16 + g * 4) * 4) = acc[m0 + m][n];
+      if (m0 + TF < MF) fetch(m0 + TF, more[(m0 / TF + 1) % 2]);
+      asm volatile("" ::: "memory");  // the wave's other lanes read what this one wrote: LDS keeps a wave's order
+#pragma unroll
+      for (int x = 0; x < kPieces; ++x) {
+        const int row = row_of(m0, x);
+        if (!here || row >= tile_rows) continue;
+        const u32x4 b = more[m0 / TF % 2][x];
+        const f32x4* from = reinterpret_cast<const f32x4*>(turn + (x * kRows + lane / kLanes) * kTurnRow + c * 4);
+        if constexpr (V == 4) {
+          f32x4 v = from[0];
+          if (adds) v += __builtin_bit_cast(f32x4, b);
+          float* out = whole ? static_cast<float*>(p.out) : p.partial + at.part * p.part_stride;
+          *reinterpret_cast<f32x4*>(out + place(row)) = v;
+        } else {
+          f32x4 v[2] = {from[0], from[1]};
+          if (adds) {
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+              v[q / 4][q % 4] += q % 2 ? __uint_as_float(b[q / 2] & 0xFFFF0000u) : bf16_bits_to_f32(b[q / 2] & 0xFFFFu);
+          }
+          *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(p.out) + place(row)) =
+              u32x4{bf16x2_bits(v[0][0], v[0][1]), bf16x2_bits(v[0][2], v[0][3]), bf16x2_bits(v[1][0], v[1][1]),
+                    bf16x2_bits(v[1][2], v[1][3])};
+        }
+      }
+      asm volatile("" ::: "memory");
     }
-  }
+  };
+  if (OEL == EL_F32 || !whole) rows_out(std::integral_constant<int, 4>{});
+  else rows_out(std::integral_constant<int, 8>{});
 }
 
-// Sum of the parts in order, the added tensor, one rounding.  n4: groups of four values; with n_rows (device) only
-// the first *n_rows rows of row4 groups each.
+// Sum of the parts in order, the added tensor, one rounding.  n4: fours of values, row4 a row's; with offsets (device)
+// only the rows from the first group's first to the last one's last.
 template <int OEL>
 __global__ __launch_bounds__(256) void join_kernel(const float* __restrict__ partial, int parts, int64_t part_stride,
-                                                   const int32_t* __restrict__ n_rows, int64_t row4, int64_t n4,
-                                                   const void* add, void* out) {
-  if (n_rows) n4 = min(n4, static_cast<int64_t>(max(*n_rows, 0)) * row4);
-  for (int64_t q = blockIdx.x * 256ll + threadIdx.x; q < n4; q += gridDim.x * 256ll) {
+                                                   const int32_t* __restrict__ offsets, int n_groups, int64_t row4,
+                                                   int64_t n4, const void* add, void* out) {
+  int64_t q0 = 0;
+  if (offsets) {
+    q0 = max(offsets[0], 0) * row4;
+    n4 = min(n4, max(offsets[n_groups], 0) * row4);
+  }
+  for (int64_t q = q0 + blockIdx.x * 256ll + threadIdx.x; q < n4; q += gridDim.x * 256ll) {
     f32x4 v = *reinterpret_cast<const f32x4*>(partial + q * 4);
     for (int s = 1; s < parts; ++s) v += *reinterpret_cast<const f32x4*>(partial + s * part_stride + q * 4);
     if constexpr (OEL == EL_F32) {
@@ -399,55 +536,102 @@ __global__ __launch_bounds__(256) void join_kernel(const float* __restrict__ par
   }
 }
 
-enum Shape { kFew, kMiddle, kBig };
-constexpr int kShapeM[] = {32, 128, 256};
-constexpr int kShapeN[] = {128, 128, 256};
+// Tile shapes.  What a call of each is expected to take, in us: `call` once; per tile and CU `ends` (first loads, last
+// products, stores) and, per 64 indexes of a bf16 reduction (32 fp32), `alone` where a CU has one tile at a time and
+// `full` where its other tiles fill the gaps; and no less than the matrices at the TB/s that kForward and kRows stream
+// them with.
+struct Shape {
+  int bm, bn;
+  double call, ends, alone, full, forward, rows;
+};
+enum : int { kSmall, kNarrow, kMiddle, kWide, kBig, kFew, kShapes };
+constexpr Shape kBf16Shapes[kShapes] = {{64, 64, 4.0, 0.9, 0.26, 0.21, 5.5, 5.4},
+                                        {64, 128, 4.5, 1.2, 0.38, 0.34, 5.2, 5.9},
+                                        {128, 128, 5.0, 2.0, 0.53, 0.55, 4.4, 5.5},
+                                        {128, 256, 5.0, 3.0, 0.66, 1.05, 4.2, 6.6},
+                                        {256, 256, 6.0, 10.0, 1.40, 1.40, 4.1, 5.2},
+                                        {32, 64, 4.0, 0.9, 0.21, 0.19, 6.3, 5.5}};
+constexpr Shape kF32Shapes[2] = {{64, 64, 4.0, 1.0, 0.55, 0.50, 5.5, 5.4}, {64, 128, 4.5, 1.5, 1.00, 0.95, 5.2, 5.9}};
+
+template <int EL, int OEL, int DIR, int BM, int BN, int RB, int WM, int WN, int ST, int MINB, bool TURNS>
+void launch(const GroupGemm& p, int blocks, hipStream_t s) {
+  hipLaunchKernelGGL((group_gemm_kernel<EL, OEL, DIR, BM, BN, RB, WM, WN, ST, MINB, TURNS>), dim3(blocks),
+                     dim3(WM * WN * 64), 0, s, p);
+}
 
 template <int EL, int OEL, int DIR>
-void launch_shape(Shape shape, const GroupGemm& p, int blocks, hipStream_t s) {
-  switch (shape) {
-    case kFew:
-      if constexpr (DIR != kWeights)
-        hipLaunchKernelGGL((group_gemm_kernel<EL, OEL, DIR, 32, 128, 128, 1, 4, 3, 2>), dim3(blocks), dim3(256), 0, s, p);
-      break;
-    case kMiddle:
-      hipLaunchKernelGGL((group_gemm_kernel<EL, OEL, DIR, 128, 128, 128, 2, 2, 2, 2>), dim3(blocks), dim3(256), 0, s, p);
-      break;
-    case kBig:
-      hipLaunchKernelGGL((group_gemm_kernel<EL, OEL, DIR, 256, 256, 128, 2, 4, 2, 1>), dim3(blocks), dim3(512), 0, s, p);
-      break;
+void launch_shape(int shape, const GroupGemm& p, int blocks, hipStream_t s) {
+  if (shape == kSmall) return launch<EL, OEL, DIR, 64, 64, 128, 2, 2, 3, 3, false>(p, blocks, s);
+  if (shape == kNarrow) return launch<EL, OEL, DIR, 64, 128, 128, 2, 2, 3, 2, false>(p, blocks, s);
+  if constexpr (EL == EL_BF16) {
+    if constexpr (DIR != kWeights)
+      if (shape == kFew) return launch<EL, OEL, DIR, 32, 64, 256, 1, 4, 3, 2, false>(p, blocks, s);
+    if (shape == kMiddle) return launch<EL, OEL, DIR, 128, 128, 128, 2, 2, 2, 2, false>(p, blocks, s);
+    if (shape == kWide) return launch<EL, OEL, DIR, 128, 256, 64, 2, 4, 3, 2, false>(p, blocks, s);
+    if (DIR == kWeights) return launch<EL, OEL, DIR, 256, 256, 128, 2, 4, 2, 1, true>(p, blocks, s);
+    return launch<EL, OEL, DIR, 256, 256, 64, 2, 4, 5, 1, true>(p, blocks, s);
   }
 }
 
 template <int DIR>
-void launch_types(int el, int oel, Shape shape, const GroupGemm& p, int blocks, hipStream_t s) {
+void launch_types(int el, int oel, int shape, const GroupGemm& p, int blocks, hipStream_t s) {
   if (el == EL_F32) launch_shape<EL_F32, EL_F32, DIR>(shape, p, blocks, s);
   else if (oel == EL_F32) launch_shape<EL_BF16, EL_F32, DIR>(shape, p, blocks, s);
   else launch_shape<EL_BF16, EL_BF16, DIR>(shape, p, blocks, s);
 }
 
 struct Plan {
-  Shape shape;
-  int parts;
+  int shape, parts, high;
   int64_t blocks;
 };
 
-// Shape, parts of the reduction and most workgroups of a call.
+constexpr double kCus = 256;
+constexpr int64_t kPartialBytes = 64 << 20;  // most that the parts of a call take of a workspace
+
+// Shape, parts of the reduction and most workgroups of a call: the least of what the shapes are expected to take,
+// where groups share the rows evenly, whole or in parts that a second launch adds up.
 Plan plan(int dir, const GroupGemm& p, int el) {
-  const double avg = static_cast<double>(p.rows) / p.n_groups;
-  Plan r{};
-  if (dir == kWeights) {
-    r.shape = p.out_rows > 128 && p.cols > 128 ? kBig : kMiddle;
-  } else {
-    r.shape = avg <= 32.0 ? kFew : avg <= 128.0 || p.cols <= 128 ? kMiddle : kBig;
+  const int shapes = el == EL_F32 ? 2 : dir == kWeights ? kFew : kShapes;
+  const int step = el == EL_F32 ? 32 : 64;
+  const double busy = std::max(1.0, std::min<double>(p.n_groups, p.rows)), avg = p.rows / busy;
+  // groups are seldom of one size, and the largest one's sum is what a call waits for
+  const double red = dir == kWeights ? std::min<double>(p.rows, 1.5 * avg) : p.red;
+  const double out_rows = dir == kWeights ? static_cast<double>(p.n_groups) * p.out_rows : p.rows;
+  const double steps = std::max(1.0, std::ceil(red / step));
+  const double matrices = busy * p.w_stride * (el == EL_F32 ? 4 : 2);
+  Plan best{};
+  double least = 0;
+  for (int i = 0; i < shapes; ++i) {
+    const Shape& h = el == EL_F32 ? kF32Shapes[i] : kBf16Shapes[i];
+    const double nt = std::ceil(static_cast<double>(p.cols) / h.bn);
+    // a group's rows end inside a tile
+    const double mt = dir == kWeights ? p.n_groups * std::ceil(static_cast<double>(p.out_rows) / h.bm)
+                      : busy == 1 || avg <= h.bm * 0.75 ? busy * std::ceil(avg / h.bm) : busy * (avg / h.bm + 0.5);
+    const double used = dir == kWeights ? 1.0 : 0.6 + 0.4 * std::min(1.0, avg / h.bm);  // rows that are not there are not read
+    for (int parts = 1; parts <= 16; parts *= 2) {
+      const double partial = out_rows * p.cols * 4 * parts;
+      if (parts > 1 && (steps / parts < 4 || partial > kPartialBytes)) break;
+      const double tiles = mt * nt * parts / kCus;  // of a CU
+      const double one = std::ceil(steps / parts) * h.alone * used + h.ends;
+      const double full = std::ceil(steps / parts) * h.full * used + h.ends;
+      double us = h.call + std::max(one, i == kBig && el != EL_F32 ? std::ceil(tiles) * one : tiles * full);
+      if (dir != kWeights) us = std::max(us, matrices / (dir == kForward ? h.forward : h.rows) / 1e6);
+      if (parts > 1) us += 2.0 + partial * 2 / 8e6;
+      if (best.parts == 0 || us < least) {
+        least = us;
+        best.shape = i;
+        best.parts = parts;
+      }
+    }
   }
-  const int bm = kShapeM[r.shape], bn = kShapeN[r.shape];
-  const int64_t nt = (p.cols + bn - 1) / bn;
-  const int64_t mt = dir == kWeights ? static_cast<int64_t>(p.n_groups) * ((p.out_rows + bm - 1) / bm)
-                                     : (static_cast<int64_t>(p.rows) + static_cast<int64_t>(p.n_groups) * (bm - 1)) / bm;
-  r.parts = 1;
-  r.blocks = mt * nt * r.parts;
-  return r;
+  const Shape& h = el == EL_F32 ? kF32Shapes[best.shape] : kBf16Shapes[best.shape];
+  const int64_t nt = (p.cols + h.bn - 1) / h.bn;
+  const int64_t mt = dir == kWeights
+                         ? static_cast<int64_t>(p.n_groups) * ((p.out_rows + h.bm - 1) / h.bm)
+                         : (static_cast<int64_t>(p.rows) + static_cast<int64_t>(p.n_groups) * (h.bm - 1)) / h.bm;
+  best.high = h.bm;
+  best.blocks = mt * nt * best.parts;
+  return best;
 }
 
 }  // namespace
@@ -467,6 +651,7 @@ hipError_t launch_group_gemm(int dir, int el, int oel, GroupGemm p, void* ws, hi
   if (r.blocks == 0) return hipSuccess;
   const int64_t rows = dir == kWeights ? static_cast<int64_t>(p.n_groups) * p.out_rows : p.rows;
   p.parts = r.parts;
+  p.high = r.high;
   p.partial = static_cast<float*>(ws);
   p.part_stride = rows * p.cols;
   const int blocks = static_cast<int>(r.blocks);
@@ -476,13 +661,13 @@ hipError_t launch_group_gemm(int dir, int el, int oel, GroupGemm p, void* ws, hi
   if (r.parts > 1) {
     const int64_t n4 = rows * p.cols / 4;
     const dim3 grid(static_cast<unsigned>(std::min<int64_t>((n4 + 255) / 256, 4096)));
-    const int32_t* n_rows = dir == kWeights ? nullptr : p.offsets + p.n_groups;
+    const int32_t* ragged = dir == kWeights ? nullptr : p.offsets;
     if (oel == EL_F32)
-      hipLaunchKernelGGL(join_kernel<EL_F32>, grid, dim3(256), 0, s, p.partial, r.parts, p.part_stride, n_rows, p.cols / 4,
-                         n4, p.add, p.out);
+      hipLaunchKernelGGL(join_kernel<EL_F32>, grid, dim3(256), 0, s, p.partial, r.parts, p.part_stride, ragged,
+                         p.n_groups, p.cols / 4, n4, p.add, p.out);
     else
-      hipLaunchKernelGGL(join_kernel<EL_BF16>, grid, dim3(256), 0, s, p.partial, r.parts, p.part_stride, n_rows,
-                         p.cols / 4, n4, p.add, p.out);
+      hipLaunchKernelGGL(join_kernel<EL_BF16>, grid, dim3(256), 0, s, p.partial, r.parts, p.part_stride, ragged,
+                         p.n_groups, p.cols / 4, n4, p.add, p.out);
   }
   return hipGetLastError();
 }

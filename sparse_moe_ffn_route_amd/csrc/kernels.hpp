@@ -204,6 +204,7 @@ struct GroupGemm {
   float* partial;          // set by the launcher: sums of parts of the reduction
   int64_t part_stride;
   int parts;
+  int high;                // set by the launcher: most rows of a tile (kForward, kRows)
 };
 size_t group_gemm_workspace(int dir, int el, const GroupGemm& p);
 bool group_gemm_fits(int dir, int el, const GroupGemm& p);  // one launch holds the call's tiles

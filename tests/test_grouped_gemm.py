@@ -98,6 +98,59 @@ def test_whole_numbers_are_exact(dir, counts, N, K, dtype, out):
         assert torch.equal(got, ref.to(DT[out])), (gather, add)
 
 
+# Sizes that take the other tile shapes, and reductions in parts, in one direction or another: ends of tiles in every
+# dimension, a group that ends a few rows into a tile, empty ones.
+LARGE = [([4100], 4104, 1032), ([2100, 0, 2200], 2056, 4104), ([700, 0, 130, 1100, 3, 40], 1032, 2056), ([9000], 520, 1032),
+         ([5003], 264, 264), ([3, 1, 5, 0, 2], 1544, 2056), ([3] * 60 + [0, 17, 1], 1032, 1032)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,out", [("bf16", "bf16"), ("bf16", "f32"), ("f32", "f32")])
+@pytest.mark.parametrize("counts,N,K", LARGE)
+@pytest.mark.parametrize("dir", DIRS)
+def test_whole_numbers_are_exact_at_large_sizes(dir, counts, N, K, dtype, out):
+    add = gather = dir != "rows"
+    got, ref, _ = run(dir, counts, N, K, dtype, out, gather, add or out == "f32")
+    used = sum(counts)
+    if dir != "weights":
+        assert (got[used:] == 777.0).all()
+        got, ref = got[:used], ref[:used]
+    assert torch.equal(got, ref.to(DT[out]))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+@pytest.mark.parametrize("dir", DIRS)
+def test_whole_numbers_are_exact_at_the_largest_tiles(dir, out):
+    """All three directions in their largest tiles; the float64 products on the GPU."""
+    counts, N, K = [2000, 0, 300, 5700], 4104, 4104
+    c, shape, rows = case(dir, counts, N, K, "bf16", out, False, False)
+    gpu = {k: None if v is None else v.cuda() for k, v in c.items()}
+    got = torch.full(shape, 777.0, dtype=DT[out], device="cuda")
+    call(dir, moe.make_groups(4, rows, N, K, "bf16", out), gpu["a"], gpu["d_out"], gpu["w"], offsets_of(counts).cuda(), got)
+    at = offsets_of(counts).tolist()
+    for e, (b, t) in enumerate(zip(at, at[1:])):
+        a, d, w = gpu["a"][b:t].double(), gpu["d_out"][b:t].double(), gpu["w"][e].double()
+        ref = d.T @ a if dir == "weights" else a @ w.T if dir == "fwd" else d @ w
+        assert torch.equal(got[e] if dir == "weights" else got[b:t], ref.to(DT[out]))
+
+
+@pytest.mark.gpu
+def test_a_slice_of_the_groups():
+    """Offsets that start behind the first row: rows of the groups before and after stay, a reduction in parts, too."""
+    counts, N, K = [70, 5003, 40], 264, 264
+    c, _, rows = case("fwd", counts, N, K, "bf16", "f32", False, False)
+    for dir in ("fwd", "rows"):
+        out = torch.full((rows, N), 777.0, device="cuda")
+        off = offsets_of(counts)
+        call(dir, moe.make_groups(1, rows, N, K, "bf16", "f32"), c["a"].cuda(), c["d_out"].cuda(), c["w"][1:2].cuda(),
+             off[1:3].clone().cuda(), out)
+        out = out.cpu()
+        assert (out[:70] == 777).all() and (out[5073:] == 777).all()
+        ref = c["a"].double() @ c["w"][1].double().T if dir == "fwd" else c["d_out"].double() @ c["w"][1].double()
+        assert torch.equal(out[70:5073].double(), ref[70:5073])
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("dir", DIRS)
 @pytest.mark.parametrize("dtype,out,N,K,counts", [
