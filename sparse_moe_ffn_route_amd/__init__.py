@@ -542,13 +542,17 @@ def make_groups(n_groups, rows, N, K, dtype="bf16", out=None) -> moe_groups:
     return moe_groups(n_groups, rows, N, K, _DTYPE_CODE[dtype], _DTYPE_CODE[out or dtype])
 
 
-def _typed(t: Optional[torch.Tensor], what: str, dtype: torch.dtype, count: int):
-    """Refuse a tensor of another type or of fewer than `count` elements."""
-    if t is not None:
+def _arg(t: Optional[torch.Tensor], what: str, dtype, count: int, at: int):
+    """Pointer of a contiguous tensor of this type, of at least `count` elements, on device `at`, the current one."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.numel() < count or t.get_device() != at or not t.is_contiguous():
         if t.dtype != dtype:
             raise ValueError(f"{what}: {t.dtype}, not {dtype}")
         if t.numel() < count:
             raise ValueError(f"{what}: {t.numel()} elements, the dims need {count}")
+        return _here(t, what, at)
+    return t.data_ptr()
 
 
 def grouped_gemm_workspace(groups: moe_groups, device="cuda") -> torch.Tensor:
@@ -559,144 +563,144 @@ def grouped_gemm_workspace(groups: moe_groups, device="cuda") -> torch.Tensor:
     return torch.empty(n, dtype=torch.uint8, device=device)
 
 
-def _check_groups(g, offsets, index=None, a=None, d_out=None, w=None, add=None, result=None, shape=None, what=""):
-    dt, out = _TORCH_OF.get(g.in_dtype), _TORCH_OF.get(g.out_dtype)
-    _typed(offsets, "offsets", torch.int32, g.n_groups + 1)
-    _typed(index, "index", torch.int32, g.rows)
-    if a is not None and index is not None and a.dim() != 2:
-        raise ValueError("a must be [a_rows][K] with an index")
-    _typed(a, "a", dt, (a.shape[0] if index is not None else g.rows) * g.K if a is not None else 0)
-    _typed(d_out, "d_out", dt, g.rows * g.N)
-    _typed(w, "w", dt, g.n_groups * g.N * g.K)
-    _typed(add, "add", out, shape)
-    _typed(result, what, out, shape)
-
-
 def _ws(t: Optional[torch.Tensor], at: int):
-    return _here(t, "ws", at), t.nbytes if t is not None else 0
+    return (None, 0) if t is None else (_here(t, "ws", at), t.nbytes)
+
+
+def _group_types(g: moe_groups):
+    return _TORCH_OF.get(g.in_dtype), _TORCH_OF.get(g.out_dtype)
+
+
+def _rows_arg(g: moe_groups, a, index, dtype, at: int):
+    """a, a_rows and index: [rows][K], or [a_rows][K] that the index picks from."""
+    if index is None:
+        return _arg(a, "a", dtype, g.rows * g.K, at), 0, None
+    if a.dim() != 2 or a.shape[1] != g.K:
+        raise ValueError("a must be [a_rows][K] with an index")
+    return _arg(a, "a", dtype, 0, at), a.shape[0], _arg(index, "index", torch.int32, g.rows, at)
 
 
 def moe_grouped_gemm(groups: moe_groups, a, offsets, w, out, index=None, add=None, ws=None, stream=None):
     """out[r] = W_e a[r] (+ add) for each row r of each group e; with index row r is a[index[r]]."""
-    g = groups
-    _check_groups(g, offsets, index, a=a, w=w, add=add, result=out, shape=g.rows * g.N, what="out")
-    at = _device()
-    _check(library().moe_grouped_gemm(ctypes.byref(g), _here(a, "a", at), a.shape[0] if index is not None else 0,
-                                      _here(index, "index", at), _here(offsets, "offsets", at), _here(w, "w", at),
-                                      _here(add, "add", at), _here(out, "out", at), *_ws(ws, at), _stream(stream)),
-           "moe_grouped_gemm")
+    g, at = groups, _device()
+    dt, to = _group_types(g)
+    n = g.rows * g.N
+    _check(library().moe_grouped_gemm(ctypes.byref(g), *_rows_arg(g, a, index, dt, at),
+                                      _arg(offsets, "offsets", torch.int32, g.n_groups + 1, at),
+                                      _arg(w, "w", dt, g.n_groups * g.N * g.K, at), _arg(add, "add", to, n, at),
+                                      _arg(out, "out", to, n, at), *_ws(ws, at), _stream(stream)), "moe_grouped_gemm")
 
 
 def moe_grouped_gemm_backward_rows(groups: moe_groups, d_out, offsets, w, d_a, add=None, ws=None, stream=None):
     """d_a[r] = W_e^T d_out[r] (+ add) for each row r of each group e."""
-    g = groups
-    _check_groups(g, offsets, d_out=d_out, w=w, add=add, result=d_a, shape=g.rows * g.K, what="d_a")
-    at = _device()
-    _check(library().moe_grouped_gemm_backward_rows(ctypes.byref(g), _here(d_out, "d_out", at),
-                                                    _here(offsets, "offsets", at), _here(w, "w", at),
-                                                    _here(add, "add", at), _here(d_a, "d_a", at), *_ws(ws, at),
-                                                    _stream(stream)), "moe_grouped_gemm_backward_rows")
+    g, at = groups, _device()
+    dt, to = _group_types(g)
+    n = g.rows * g.K
+    _check(library().moe_grouped_gemm_backward_rows(ctypes.byref(g), _arg(d_out, "d_out", dt, g.rows * g.N, at),
+                                                    _arg(offsets, "offsets", torch.int32, g.n_groups + 1, at),
+                                                    _arg(w, "w", dt, g.n_groups * g.N * g.K, at),
+                                                    _arg(add, "add", to, n, at), _arg(d_a, "d_a", to, n, at),
+                                                    *_ws(ws, at), _stream(stream)), "moe_grouped_gemm_backward_rows")
 
 
 def moe_grouped_gemm_backward_weights(groups: moe_groups, d_out, a, offsets, d_w, index=None, add=None, ws=None,
                                       stream=None):
     """d_w[e] = sum over the rows r of group e of d_out[r] a[r]^T (+ add); zeros (or add) for an empty group."""
-    g = groups
-    _check_groups(g, offsets, index, a=a, d_out=d_out, add=add, result=d_w, shape=g.n_groups * g.N * g.K, what="d_w")
-    at = _device()
-    _check(library().moe_grouped_gemm_backward_weights(ctypes.byref(g), _here(d_out, "d_out", at), _here(a, "a", at),
-                                                       a.shape[0] if index is not None else 0, _here(index, "index", at),
-                                                       _here(offsets, "offsets", at), _here(add, "add", at),
-                                                       _here(d_w, "d_w", at), *_ws(ws, at), _stream(stream)),
+    g, at = groups, _device()
+    dt, to = _group_types(g)
+    n = g.n_groups * g.N * g.K
+    _check(library().moe_grouped_gemm_backward_weights(ctypes.byref(g), _arg(d_out, "d_out", dt, g.rows * g.N, at),
+                                                       *_rows_arg(g, a, index, dt, at),
+                                                       _arg(offsets, "offsets", torch.int32, g.n_groups + 1, at),
+                                                       _arg(add, "add", to, n, at), _arg(d_w, "d_w", to, n, at),
+                                                       *_ws(ws, at), _stream(stream)),
            "moe_grouped_gemm_backward_weights")
 
 
-def _check_rng(rng: Optional[torch.Tensor]):
-    if rng is not None and (rng.dtype not in (torch.int64, torch.uint64) or rng.numel() < 2):
+_RNG_TYPES = (torch.int64, torch.uint64)
+
+
+def _rng(rng: Optional[torch.Tensor], at: int):
+    if rng is None:
+        return None
+    if rng.dtype not in _RNG_TYPES or rng.numel() < 2:
         raise ValueError("rng must hold two 64-bit whole numbers, the seed and the offset")
+    return _here(rng, "rng", at)
 
 
-def _rows_of(t: torch.Tensor, what: str, shape, dtype, ld: int, at: int):
-    """Pointer of [rows][I] values whose rows are ld elements apart (a half of a wider tensor, say)."""
-    if t.shape != shape or t.dtype != dtype:
-        raise ValueError(f"{what}: {tuple(t.shape)} {t.dtype}, not {tuple(shape)} {dtype}")
-    if t.numel() and (t.stride(1) != 1 and shape[1] > 1 or t.stride(0) != ld and shape[0] > 1):
-        raise ValueError(f"{what}: strides {t.stride()}, gate's rows are {ld} elements apart")
-    if t.get_device() != at:
-        return _here(t, what, at)
-    return t.data_ptr()
+def _halves(ld: int, at: int, shape, dtype, **tensors):
+    """Pointers of [rows][I] tensors whose rows are ld elements apart (halves of a wider tensor, say)."""
+    out = []
+    for what, t in tensors.items():
+        if t.shape != shape or t.dtype is not dtype:
+            raise ValueError(f"{what}: {tuple(t.shape)} {t.dtype}, not {tuple(shape)} {dtype}")
+        by_row, by_value = t.stride()
+        if (by_value != 1 and shape[1] > 1 or by_row != ld and shape[0] > 1) and t.numel():
+            raise ValueError(f"{what}: strides {t.stride()}, rows of {ld} elements are needed")
+        if t.get_device() != at:
+            _here(t, what, at)
+        out.append(t.data_ptr())
+    return out
 
 
-def _swiglu_args(gate, p, rng, n_rows, at):
+def _row_stride(gate) -> int:
     if gate.dim() != 2:
         raise ValueError("gate must be [rows][I]")
-    _check_rng(rng)
-    ld = gate.stride(0) if gate.shape[0] > 1 else max(gate.stride(0), gate.shape[1])
-    _typed(n_rows, "n_rows", torch.int32, 1)
-    return (gate.shape[0], gate.shape[1], ld, _CODE_OF_TORCH.get(gate.dtype, -1), _here(n_rows, "n_rows", at)), ld
+    rows, I = gate.shape
+    return gate.stride(0) if rows > 1 and I > 1 else max(gate.stride(0), I)
 
 
 def moe_swiglu(gate, up, h, n_rows=None, p=0.0, rng=None, stream=None):
     """h = drop(silu(gate) * up); gate and up [rows][I] may be halves of one tensor, h is contiguous."""
-    at = _device()
-    args, ld = _swiglu_args(gate, p, rng, n_rows, at)
-    _typed(h, "h", gate.dtype, gate.numel())
-    _check(library().moe_swiglu(*args, _rows_of(gate, "gate", gate.shape, gate.dtype, ld, at),
-                                _rows_of(up, "up", gate.shape, gate.dtype, ld, at), p, _here(rng, "rng", at), _here(h, "h", at),
-                                _stream(stream)), "moe_swiglu")
+    at, ld, dt = _device(), _row_stride(gate), gate.dtype
+    rows, I = shape = gate.shape
+    seed = _rng(rng, at)
+    g, u = _halves(ld, at, shape, dt, gate=gate, up=up)
+    _check(library().moe_swiglu(rows, I, ld, _CODE_OF_TORCH.get(dt, -1), _arg(n_rows, "n_rows", torch.int32, 1, at), g,
+                                u, p, seed, _arg(h, "h", dt, rows * I, at), _stream(stream)), "moe_swiglu")
 
 
 def moe_swiglu_backward(d_h, gate, up, d_gate, d_up, h=None, n_rows=None, p=0.0, rng=None, stream=None):
     """Gradients of moe_swiglu's gate and up, and (h given) its result again."""
-    at = _device()
-    args, ld = _swiglu_args(gate, p, rng, n_rows, at)
-    _typed(d_h, "d_h", gate.dtype, gate.numel())
-    _typed(h, "h", gate.dtype, gate.numel())
-    rows = [_rows_of(t, what, gate.shape, gate.dtype, ld, at)
-            for t, what in ((gate, "gate"), (up, "up"), (d_gate, "d_gate"), (d_up, "d_up"))]
-    _check(library().moe_swiglu_backward(*args, _here(d_h, "d_h", at), rows[0], rows[1], p, _here(rng, "rng", at), rows[2],
-                                         rows[3], _here(h, "h", at), _stream(stream)), "moe_swiglu_backward")
+    at, ld, dt = _device(), _row_stride(gate), gate.dtype
+    rows, I = shape = gate.shape
+    seed = _rng(rng, at)
+    g, u, dg, du = _halves(ld, at, shape, dt, gate=gate, up=up, d_gate=d_gate, d_up=d_up)
+    _check(library().moe_swiglu_backward(rows, I, ld, _CODE_OF_TORCH.get(dt, -1),
+                                         _arg(n_rows, "n_rows", torch.int32, 1, at), _arg(d_h, "d_h", dt, rows * I, at),
+                                         g, u, p, seed, dg, du, _arg(h, "h", dt, rows * I, at), _stream(stream)),
+           "moe_swiglu_backward")
 
 
 def moe_dropout(x, out, p, rng=None, residual=None, stream=None):
     """out = residual + drop(x); without residual the branch alone, and the gradient of either."""
-    at = _device()
-    _check_rng(rng)
-    _typed(out, "out", x.dtype, x.numel())
-    _typed(residual, "residual", x.dtype, x.numel())
-    _check(library().moe_dropout(x.numel(), _CODE_OF_TORCH.get(x.dtype, -1), _here(x, "x", at),
-                                 _here(residual, "residual", at), p, _here(rng, "rng", at), _here(out, "out", at),
+    at, n, dt = _device(), x.numel(), x.dtype
+    seed = _rng(rng, at)
+    r, o = _arg(residual, "residual", dt, n, at), _arg(out, "out", dt, n, at)
+    _check(library().moe_dropout(n, _CODE_OF_TORCH.get(dt, -1), _arg(x, "x", dt, n, at), r, p, seed, o,
                                  _stream(stream)), "moe_dropout")
 
 
 def moe_unpermute_combine_backward(dims, dy, packed, inv_pos, out_rows, d_rows, d_weights, stream=None):
     """Gradients of moe_unpermute_combine's rows and (out_rows given) routing weights."""
-    T, D, k = dims.T, dims.D, dims.top_k
+    T, D, k, at = dims.T, dims.D, dims.top_k, _device()
     y, act = _TORCH_OF.get(dims.out_dtype), _TORCH_OF.get(dims.act_dtype)
-    _typed(dy, "dy", y, T * D)
-    _typed(packed, "packed", torch.int32, T * 2 * k)
-    _typed(inv_pos, "inv_pos", torch.int32, T * k)
-    _typed(out_rows, "out_rows", y, T * k * D)
-    _typed(d_rows, "d_rows", act, T * k * D)
-    _typed(d_weights, "d_weights", torch.float32, T * k)
-    at = _device()
-    _check(library().moe_unpermute_combine_backward(ctypes.byref(dims), _here(dy, "dy", at), _here(packed, "packed", at),
-                                                    _here(inv_pos, "inv_pos", at), _here(out_rows, "out_rows", at),
-                                                    _here(d_rows, "d_rows", at), _here(d_weights, "d_weights", at),
+    _check(library().moe_unpermute_combine_backward(ctypes.byref(dims), _arg(dy, "dy", y, T * D, at),
+                                                    _arg(packed, "packed", torch.int32, T * 2 * k, at),
+                                                    _arg(inv_pos, "inv_pos", torch.int32, T * k, at),
+                                                    _arg(out_rows, "out_rows", y, T * k * D, at),
+                                                    _arg(d_rows, "d_rows", act, T * k * D, at),
+                                                    _arg(d_weights, "d_weights", torch.float32, T * k, at),
                                                     _stream(stream)), "moe_unpermute_combine_backward")
 
 
 def moe_permute_backward(dims, d_x_perm, inv_pos, d_x, add=None, stream=None):
     """d_x[t] = the sum of the gradients of the token's rows (+ add[t])."""
-    T, D, k = dims.T, dims.D, dims.top_k
+    T, D, k, at = dims.T, dims.D, dims.top_k, _device()
     act = _TORCH_OF.get(dims.act_dtype)
-    _typed(d_x_perm, "d_x_perm", act, T * k * D)
-    _typed(inv_pos, "inv_pos", torch.int32, T * k)
-    _typed(add, "add", act, T * D)
-    _typed(d_x, "d_x", act, T * D)
-    at = _device()
-    _check(library().moe_permute_backward(ctypes.byref(dims), _here(d_x_perm, "d_x_perm", at),
-                                          _here(inv_pos, "inv_pos", at), _here(add, "add", at), _here(d_x, "d_x", at),
+    _check(library().moe_permute_backward(ctypes.byref(dims), _arg(d_x_perm, "d_x_perm", act, T * k * D, at),
+                                          _arg(inv_pos, "inv_pos", torch.int32, T * k, at),
+                                          _arg(add, "add", act, T * D, at), _arg(d_x, "d_x", act, T * D, at),
                                           _stream(stream)), "moe_permute_backward")
 
 
@@ -708,40 +712,40 @@ def route_loss_workspace(dims: moe_dims, device="cuda") -> torch.Tensor:
     return torch.empty(n, dtype=torch.uint8, device=device)
 
 
-def _check_route(dims, logits, logit_bias, packed, mask, load):
-    T, E, k = dims.T, dims.E, dims.top_k
-    _typed(logits, "logits", torch.float32, T * E)
-    _typed(logit_bias, "logit bias", torch.float32, E)
-    _typed(packed, "packed", torch.int32, T * 2 * k)
-    _typed(load, "load", torch.int32, E + 1)
-    if mask is not None and mask.dtype not in (torch.uint8, torch.bool):
+def _mask(mask: Optional[torch.Tensor], T: int, at: int):
+    if mask is None:
+        return None
+    if mask.dtype not in (torch.uint8, torch.bool):
         raise ValueError(f"mask: {mask.dtype}, not uint8 or bool")
-    _need(mask, T, "mask")
+    return _arg(mask, "mask", mask.dtype, T, at)
+
+
+def _route_args(dims, logits, logit_bias, packed, mask, at: int):
+    T, E, k = dims.T, dims.E, dims.top_k
+    return (ctypes.byref(dims), _arg(logits, "logits", torch.float32, T * E, at),
+            _arg(logit_bias, "logit bias", torch.float32, E, at), _arg(packed, "packed", torch.int32, T * 2 * k, at),
+            _mask(mask, T, at))
 
 
 def moe_route_loss(dims, logits, logit_bias, packed, loss, load, mask=None, ws=None, stream=None):
     """loss[0] the load balance, loss[1] the z loss of the masked tokens; load[e] their slots on e, load[E] their number."""
-    _check_route(dims, logits, logit_bias, packed, mask, load)
-    _typed(loss, "loss", torch.float32, 2)
     at = _device()
-    _check(library().moe_route_loss(ctypes.byref(dims), _here(logits, "logits", at), _here(logit_bias, "logit bias", at),
-                                    _here(packed, "packed", at), _here(mask, "mask", at), _here(loss, "loss", at),
-                                    _here(load, "load", at), *_ws(ws, at), _stream(stream)), "moe_route_loss")
+    _check(library().moe_route_loss(*_route_args(dims, logits, logit_bias, packed, mask, at),
+                                    _arg(loss, "loss", torch.float32, 2, at),
+                                    _arg(load, "load", torch.int32, dims.E + 1, at), *_ws(ws, at), _stream(stream)),
+           "moe_route_loss")
 
 
 def moe_route_backward(dims, logits, logit_bias, packed, d_weights, load, d_loss, d_logits, mask=None, stream=None):
     """Gradient of the logits from the routing weights' (d_weights) and the losses' (d_loss, with moe_route_loss's load)."""
-    _check_route(dims, logits, logit_bias, packed, mask, load)
-    _typed(d_weights, "d_weights", torch.float32, dims.T * dims.top_k)
-    _typed(d_loss, "d_loss", torch.float32, 2)
-    _need(d_logits, dims.T * dims.E * d_logits.element_size(), "d_logits")
-    at = _device()
-    _check(library().moe_route_backward(ctypes.byref(dims), _here(logits, "logits", at),
-                                        _here(logit_bias, "logit bias", at), _here(packed, "packed", at),
-                                        _here(mask, "mask", at), _here(d_weights, "d_weights", at),
-                                        _here(load, "load", at), _here(d_loss, "d_loss", at),
-                                        _CODE_OF_TORCH.get(d_logits.dtype, -1), _here(d_logits, "d_logits", at),
-                                        _stream(stream)), "moe_route_backward")
+    at, T, E = _device(), dims.T, dims.E
+    _check(library().moe_route_backward(*_route_args(dims, logits, logit_bias, packed, mask, at),
+                                        _arg(d_weights, "d_weights", torch.float32, T * dims.top_k, at),
+                                        _arg(load, "load", torch.int32, E + 1, at),
+                                        _arg(d_loss, "d_loss", torch.float32, 2, at),
+                                        _CODE_OF_TORCH.get(d_logits.dtype, -1),
+                                        _arg(d_logits, "d_logits", d_logits.dtype, T * E, at), _stream(stream)),
+           "moe_route_backward")
 
 
 HBM_PROBE_SINK_WORDS = 16384

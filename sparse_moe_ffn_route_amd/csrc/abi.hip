@@ -505,11 +505,11 @@ int grouped_gemm(const moe_groups* g, int dir, const void* p, const void* q, int
   }
   if (!aligned16(p, q, out, add, ws)) return MOE_ERR_UNSUPPORTED;
   GroupGemm m = group_problem(*g, dir);
-  const size_t need = group_gemm_workspace(dir, g->in_dtype, m);
+  const size_t need = group_gemm_workspace(dir, g->in_dtype, g->out_dtype, m);
   if (need && !ws) return MOE_ERR_NULL_ARG;
   if (ws_bytes < need) return MOE_ERR_WORKSPACE;
   m.p = p; m.q = q; m.out = out; m.add = add; m.offsets = offsets; m.index = index; m.src_rows = src_rows;
-  if (!group_gemm_fits(dir, g->in_dtype, m)) return MOE_ERR_UNSUPPORTED;
+  if (!group_gemm_fits(dir, g->in_dtype, g->out_dtype, m)) return MOE_ERR_UNSUPPORTED;
   return hip_status(launch_group_gemm(dir, g->in_dtype, g->out_dtype, m, ws, static_cast<hipStream_t>(stream)));
 }
 
@@ -838,7 +838,7 @@ size_t moe_grouped_gemm_workspace_bytes(const moe_groups* groups) {
   if (check_groups(groups) != MOE_OK) return 0;
   size_t n = 256;
   for (const int dir : {kForward, kRows, kWeights})
-    n = std::max(n, group_gemm_workspace(dir, groups->in_dtype, group_problem(*groups, dir)));
+    n = std::max(n, group_gemm_workspace(dir, groups->in_dtype, groups->out_dtype, group_problem(*groups, dir)));
   return align_up(n);
 }
 

@@ -68,11 +68,11 @@ struct Eight {
   __device__ __forceinline__ void store(void* base, int64_t at) const {
     if constexpr (EL == EL_F32) {
       f32x4* p = reinterpret_cast<f32x4*>(static_cast<float*>(base) + at);
-      p[0] = f32x4{v[0], v[1], v[2], v[3]};
-      p[1] = f32x4{v[4], v[5], v[6], v[7]};
+      __builtin_nontemporal_store(f32x4{v[0], v[1], v[2], v[3]}, p);
+      __builtin_nontemporal_store(f32x4{v[4], v[5], v[6], v[7]}, p + 1);
     } else {
-      *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(base) + at) =
-          u32x4{bf16x2_bits(v[0], v[1]), bf16x2_bits(v[2], v[3]), bf16x2_bits(v[4], v[5]), bf16x2_bits(v[6], v[7])};
+      const u32x4 w{bf16x2_bits(v[0], v[1]), bf16x2_bits(v[2], v[3]), bf16x2_bits(v[4], v[5]), bf16x2_bits(v[6], v[7])};
+      __builtin_nontemporal_store(w, reinterpret_cast<u32x4*>(static_cast<uint16_t*>(base) + at));
     }
   }
   static __device__ __forceinline__ float one(const void* base, int64_t at) {

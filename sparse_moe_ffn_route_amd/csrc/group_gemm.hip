@@ -465,7 +465,7 @@ __global__ __launch_bounds__(WM * WN * 64, MINB) void group_gemm_kernel(GroupGem
 #pragma unroll
       for (int x = 0; x < kPieces; ++x) {
         const int row = row_of(m0, x);
-        to[x] = here && row < tile_rows ? *reinterpret_cast<const u32x4*>(static_cast<const uint8_t*>(p.add) + place(row) * (16 / V)) : u32x4{};
+        to[x] = here && row < tile_rows ? __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(static_cast<const uint8_t*>(p.add) + place(row) * (16 / V))) : u32x4{};
       }
     };
     fetch(0, more[0]);
@@ -488,7 +488,9 @@ __global__ __launch_bounds__(WM * WN * 64, MINB) void group_gemm_kernel(GroupGem
           f32x4 v = from[0];
           if (adds) v += __builtin_bit_cast(f32x4, b);
           float* out = whole ? static_cast<float*>(p.out) : p.partial + at.part * p.part_stride;
-          *reinterpret_cast<f32x4*>(out + place(row)) = v;
+          f32x4* to = reinterpret_cast<f32x4*>(out + place(row));
+          if (DIR == kWeights) __builtin_nontemporal_store(v, to);
+          else *to = v;
         } else {
           f32x4 v[2] = {from[0], from[1]};
           if (adds) {
@@ -496,9 +498,11 @@ __global__ __launch_bounds__(WM * WN * 64, MINB) void group_gemm_kernel(GroupGem
             for (int q = 0; q < 8; ++q)
               v[q / 4][q % 4] += q % 2 ? __uint_as_float(b[q / 2] & 0xFFFF0000u) : bf16_bits_to_f32(b[q / 2] & 0xFFFFu);
           }
-          *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(p.out) + place(row)) =
-              u32x4{bf16x2_bits(v[0][0], v[0][1]), bf16x2_bits(v[0][2], v[0][3]), bf16x2_bits(v[1][0], v[1][1]),
+          const u32x4 o{bf16x2_bits(v[0][0], v[0][1]), bf16x2_bits(v[0][2], v[0][3]), bf16x2_bits(v[1][0], v[1][1]),
                     bf16x2_bits(v[1][2], v[1][3])};
+          u32x4* to = reinterpret_cast<u32x4*>(static_cast<uint16_t*>(p.out) + place(row));
+          if (DIR == kWeights) __builtin_nontemporal_store(o, to);
+          else *to = o;
         }
       }
       asm volatile("" ::: "memory");
@@ -549,7 +553,7 @@ constexpr Shape kBf16Shapes[kShapes] = {{64, 64, 4.0, 0.9, 0.26, 0.21, 5.5, 5.4}
                                         {64, 128, 4.5, 1.2, 0.38, 0.34, 5.2, 5.9},
                                         {128, 128, 5.0, 2.0, 0.53, 0.55, 4.4, 5.5},
                                         {128, 256, 5.0, 3.0, 0.66, 1.05, 4.2, 6.6},
-                                        {256, 256, 6.0, 10.0, 1.40, 1.40, 4.1, 5.2},
+                                        {256, 256, 6.0, 3.0, 1.40, 1.40, 4.1, 5.2},
                                         {32, 64, 4.0, 0.9, 0.21, 0.19, 6.3, 5.5}};
 constexpr Shape kF32Shapes[2] = {{64, 64, 4.0, 1.0, 0.55, 0.50, 5.5, 5.4}, {64, 128, 4.5, 1.5, 1.00, 0.95, 5.2, 5.9}};
 
@@ -590,7 +594,7 @@ constexpr int64_t kPartialBytes = 64 << 20;  // most that the parts of a call ta
 
 // Shape, parts of the reduction and most workgroups of a call: the least of what the shapes are expected to take,
 // where groups share the rows evenly, whole or in parts that a second launch adds up.
-Plan plan(int dir, const GroupGemm& p, int el) {
+Plan plan(int dir, const GroupGemm& p, int el, int oel) {
   const int shapes = el == EL_F32 ? 2 : dir == kWeights ? kFew : kShapes;
   const int step = el == EL_F32 ? 32 : 64;
   const double busy = std::max(1.0, std::min<double>(p.n_groups, p.rows)), avg = p.rows / busy;
@@ -612,7 +616,9 @@ Plan plan(int dir, const GroupGemm& p, int el) {
       const double partial = out_rows * p.cols * 4 * parts;
       if (parts > 1 && (steps / parts < 4 || partial > kPartialBytes)) break;
       const double tiles = mt * nt * parts / kCus;  // of a CU
-      const double one = std::ceil(steps / parts) * h.alone * used + h.ends;
+      // the one tile of a CU stores its values, and reads some to add, with nothing beside it: 20 GB/s a CU
+      const double stores = i == kBig && el != EL_F32 ? h.bm * h.bn * (oel == EL_F32 ? 4 : 2) * 1.5 / 20e3 : 0.0;
+      const double one = std::ceil(steps / parts) * h.alone * used + h.ends + stores;
       const double full = std::ceil(steps / parts) * h.full * used + h.ends;
       double us = h.call + std::max(one, i == kBig && el != EL_F32 ? std::ceil(tiles) * one : tiles * full);
       if (dir != kWeights) us = std::max(us, matrices / (dir == kForward ? h.forward : h.rows) / 1e6);
@@ -636,18 +642,18 @@ Plan plan(int dir, const GroupGemm& p, int el) {
 
 }  // namespace
 
-size_t group_gemm_workspace(int dir, int el, const GroupGemm& p) {
-  const Plan r = plan(dir, p, el);
+size_t group_gemm_workspace(int dir, int el, int oel, const GroupGemm& p) {
+  const Plan r = plan(dir, p, el, oel);
   const int64_t rows = dir == kWeights ? static_cast<int64_t>(p.n_groups) * p.out_rows : p.rows;
   return r.parts > 1 ? static_cast<size_t>(rows) * p.cols * r.parts * 4 : 0;
 }
 
-bool group_gemm_fits(int dir, int el, const GroupGemm& p) {
-  return plan(dir, p, el).blocks < (1ll << 32) / 512;  // of threads, which a grid dimension counts
+bool group_gemm_fits(int dir, int el, int oel, const GroupGemm& p) {
+  return plan(dir, p, el, oel).blocks < (1ll << 32) / 512;  // of threads, which a grid dimension counts
 }
 
 hipError_t launch_group_gemm(int dir, int el, int oel, GroupGemm p, void* ws, hipStream_t s) {
-  const Plan r = plan(dir, p, el);
+  const Plan r = plan(dir, p, el, oel);
   if (r.blocks == 0) return hipSuccess;
   const int64_t rows = dir == kWeights ? static_cast<int64_t>(p.n_groups) * p.out_rows : p.rows;
   p.parts = r.parts;

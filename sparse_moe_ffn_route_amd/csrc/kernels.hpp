@@ -206,8 +206,8 @@ struct GroupGemm {
   int parts;
   int high;                // set by the launcher: most rows of a tile (kForward, kRows)
 };
-size_t group_gemm_workspace(int dir, int el, const GroupGemm& p);
-bool group_gemm_fits(int dir, int el, const GroupGemm& p);  // one launch holds the call's tiles
+size_t group_gemm_workspace(int dir, int el, int out_el, const GroupGemm& p);
+bool group_gemm_fits(int dir, int el, int out_el, const GroupGemm& p);  // one launch holds the call's tiles
 hipError_t launch_group_gemm(int dir, int el, int out_el, GroupGemm p, void* ws, hipStream_t stream);
 
 // SwiGLU with dropout, its gradient, and dropout on a residual branch (see dropout.hip).

@@ -280,7 +280,8 @@ def test_refusals():
     assert lib.moe_dropout(8, moe.F32, None, None, 0.5, FAKE, FAKE, None) == moe.ERR_NULL_ARG
 
 
-def test_binding_refusals():
+def test_binding_refusals(monkeypatch):
+    monkeypatch.setattr(moe, "_device", lambda: -1)   # where these tensors are: types and sizes are what is refused
     g = torch.zeros(4, 16)
     h = torch.zeros(4, 16)
     for args in ((g, g[:3], h), (g, g.bfloat16(), h), (g, torch.zeros(4, 32)[:, :16], h), (g.t(), g.t(), h)):
@@ -292,5 +293,6 @@ def test_binding_refusals():
         moe.moe_dropout(g, h, 0.5, torch.zeros(2, dtype=torch.int32))
     with pytest.raises(ValueError, match="residual"):
         moe.moe_dropout(g, h, 0.5, residual=g.bfloat16())
+    monkeypatch.undo()
     with pytest.raises(ValueError, match="GPU"):
         moe.moe_dropout(g, h, 0.0)

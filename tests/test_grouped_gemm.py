@@ -326,7 +326,8 @@ def test_refusals():
     assert lib.moe_grouped_gemm_workspace_bytes(ctypes.byref(moe.make_groups(1, 1, 64, 64))) >= 256
 
 
-def test_binding_refusals():
+def test_binding_refusals(monkeypatch):
+    monkeypatch.setattr(moe, "_device", lambda: -1)   # where these tensors are: types and sizes are what is refused
     g = moe.make_groups(2, 8, 64, 32)
     a, w, out = torch.zeros(8, 32).bfloat16(), torch.zeros(2, 64, 32).bfloat16(), torch.zeros(8, 64).bfloat16()
     off = torch.zeros(3, dtype=torch.int32)
@@ -339,9 +340,12 @@ def test_binding_refusals():
         moe.moe_grouped_gemm(g, a, off, w, out, index=off)
     with pytest.raises(ValueError, match="add"):
         moe.moe_grouped_gemm(g, a, off, w, out, add=out[:1])
-    with pytest.raises(ValueError, match="GPU"):
-        moe.moe_grouped_gemm(g, a, off, w, out)
     with pytest.raises(ValueError, match="d_a"):
         moe.moe_grouped_gemm_backward_rows(g, out, off, w, a.float())
     with pytest.raises(ValueError, match="d_w"):
         moe.moe_grouped_gemm_backward_weights(g, out, a, off, w[0])
+    with pytest.raises(ValueError, match=r"\[a_rows\]\[K\]"):
+        moe.moe_grouped_gemm(g, a[:, :16].contiguous(), off, w, out, index=torch.zeros(8, dtype=torch.int32))
+    monkeypatch.undo()
+    with pytest.raises(ValueError, match="GPU"):
+        moe.moe_grouped_gemm(g, a, off, w, out)

@@ -252,7 +252,8 @@ def test_refusals():
     assert grad(dt=moe.E4M3) == moe.ERR_UNSUPPORTED
 
 
-def test_binding_refusals():
+def test_binding_refusals(monkeypatch):
+    monkeypatch.setattr(moe, "_device", lambda: -1)   # where these tensors are: types and sizes are what is refused
     d = moe.make_dims(8, 64, 16, 2, 64)
     lg, pk = torch.zeros(8, 16), torch.zeros(8, 2, 2, dtype=torch.int32)
     loss, load = torch.zeros(2), torch.zeros(17, dtype=torch.int32)

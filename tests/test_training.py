@@ -250,7 +250,8 @@ def test_refusals():
         assert permute(**bad) == moe.ERR_UNSUPPORTED, bad
 
 
-def test_binding_refusals():
+def test_binding_refusals(monkeypatch):
+    monkeypatch.setattr(moe, "_device", lambda: -1)   # where these tensors are: types and sizes are what is refused
     d = moe.make_dims(4, 64, 8, 2, 64)
     dy, rows = torch.zeros(4, 64).bfloat16(), torch.zeros(8, 64).bfloat16()
     pk, inv, dw = torch.zeros(4, 2, 2, dtype=torch.int32), torch.zeros(4, 2, dtype=torch.int32), torch.zeros(4, 2)
