@@ -166,6 +166,7 @@ __device__ __forceinline__ bool find_rows(const GroupGemm& p, int n_tiles, int b
     const int2 v = group_rows(p, min(g, p.n_groups - 1));
     if (i == 0) r = v;
     if (g < p.n_groups) mine += tiles_of(v);
+    mine = min(mine, 1 << 24);  // more than any launch has: offsets that overlap must not overflow
   }
   int upto = mine;
 #pragma unroll
@@ -173,7 +174,8 @@ __device__ __forceinline__ bool find_rows(const GroupGemm& p, int n_tiles, int b
     const int v = __shfl_up(upto, o, kWave);
     if (lane >= o) upto += v;
   }
-  const int total = __builtin_amdgcn_readlane(upto, 63) * n_tiles * p.parts;
+  const int64_t all = static_cast<int64_t>(__builtin_amdgcn_readlane(upto, 63)) * n_tiles * p.parts;
+  const int total = static_cast<int>(min<int64_t>(all, 0x7fffffff));
   if (block >= total) return false;
   int L = xcd_remap(block, total);
   at.part = L % p.parts;
@@ -186,7 +188,7 @@ __device__ __forceinline__ bool find_rows(const GroupGemm& p, int n_tiles, int b
   at.end = __builtin_amdgcn_readlane(r.y, who);
   if (per > 1) {  // the lane's groups in turn, by the whole wave
     mt = tiles_of(make_int2(at.begin, at.end));
-    while (q >= before + mt) {
+    while (q >= before + mt && at.g + 1 < p.n_groups) {
       before += mt;
       const int2 v = group_rows(p, ++at.g);
       at.begin = __builtin_amdgcn_readfirstlane(v.x);
@@ -540,22 +542,24 @@ __global__ __launch_bounds__(256) void join_kernel(const float* __restrict__ par
   }
 }
 
-// Tile shapes.  What a call of each is expected to take, in us: `call` once; per tile and CU `ends` (first loads, last
-// products, stores) and, per 64 indexes of a bf16 reduction (32 fp32), `alone` where a CU has one tile at a time and
-// `full` where its other tiles fill the gaps; and no less than the matrices at the TB/s that kForward and kRows stream
-// them with.
+// Tile shapes, and what a call of each is expected to take, in us, as measured over sizes from one tile to thousands:
+// `call` once; per tile and CU `ends` (first loads, last products, stores) and, per 64 indexes of a bf16 reduction (32
+// of an fp32 one), [0] `alone` where a CU has one tile at a time and `full` where its other tiles fill the gaps ([1]: of
+// kWeights, both of whose operands are read across); and no less than the matrices at the TB/s that kForward and kRows
+// stream them with.
 struct Shape {
   int bm, bn;
-  double call, ends, alone, full, forward, rows;
+  double call, ends, alone[2], full[2], forward, rows;
 };
 enum : int { kSmall, kNarrow, kMiddle, kWide, kBig, kFew, kShapes };
-constexpr Shape kBf16Shapes[kShapes] = {{64, 64, 4.0, 0.9, 0.26, 0.21, 5.5, 5.4},
-                                        {64, 128, 4.5, 1.2, 0.38, 0.34, 5.2, 5.9},
-                                        {128, 128, 5.0, 2.0, 0.53, 0.55, 4.4, 5.5},
-                                        {128, 256, 5.0, 3.0, 0.66, 1.05, 4.2, 6.6},
-                                        {256, 256, 6.0, 3.0, 1.40, 1.40, 4.1, 5.2},
-                                        {32, 64, 4.0, 0.9, 0.21, 0.19, 6.3, 5.5}};
-constexpr Shape kF32Shapes[2] = {{64, 64, 4.0, 1.0, 0.55, 0.50, 5.5, 5.4}, {64, 128, 4.5, 1.5, 1.00, 0.95, 5.2, 5.9}};
+constexpr Shape kBf16Shapes[kShapes] = {{64, 64, 4.0, 0.9, {0.26, 0.34}, {0.21, 0.21}, 5.5, 5.4},
+                                        {64, 128, 4.5, 1.2, {0.38, 0.49}, {0.34, 0.30}, 5.2, 5.9},
+                                        {128, 128, 5.0, 2.0, {0.53, 0.65}, {0.55, 0.42}, 4.4, 5.5},
+                                        {128, 256, 5.0, 3.0, {0.66, 1.00}, {1.05, 0.80}, 4.2, 6.6},
+                                        {256, 256, 6.0, 3.0, {1.40, 1.47}, {1.40, 1.47}, 4.1, 5.2},
+                                        {32, 64, 4.0, 0.9, {0.21, 0.21}, {0.19, 0.19}, 6.3, 5.5}};
+constexpr Shape kF32Shapes[2] = {{64, 64, 4.0, 1.0, {0.55, 0.55}, {0.50, 0.50}, 5.5, 5.4},
+                                 {64, 128, 4.5, 1.5, {1.00, 1.00}, {0.95, 0.95}, 5.2, 5.9}};
 
 template <int EL, int OEL, int DIR, int BM, int BN, int RB, int WM, int WN, int ST, int MINB, bool TURNS>
 void launch(const GroupGemm& p, int blocks, hipStream_t s) {
@@ -598,8 +602,9 @@ Plan plan(int dir, const GroupGemm& p, int el, int oel) {
   const int shapes = el == EL_F32 ? 2 : dir == kWeights ? kFew : kShapes;
   const int step = el == EL_F32 ? 32 : 64;
   const double busy = std::max(1.0, std::min<double>(p.n_groups, p.rows)), avg = p.rows / busy;
-  // groups are seldom of one size, and the largest one's sum is what a call waits for
-  const double red = dir == kWeights ? std::min<double>(p.rows, 1.5 * avg) : p.red;
+  // groups are seldom of one size, and the largest one's sum is what a call waits for: 33 us of a call of 16 groups of
+  // very unequal sizes, 4903 rows in all, into 40 x 648 in one part, 19 in eight
+  const double red = dir == kWeights ? std::min<double>(p.rows, 2.0 * avg) : p.red;
   const double out_rows = dir == kWeights ? static_cast<double>(p.n_groups) * p.out_rows : p.rows;
   const double steps = std::max(1.0, std::ceil(red / step));
   const double matrices = busy * p.w_stride * (el == EL_F32 ? 4 : 2);
@@ -618,8 +623,8 @@ Plan plan(int dir, const GroupGemm& p, int el, int oel) {
       const double tiles = mt * nt * parts / kCus;  // of a CU
       // the one tile of a CU stores its values, and reads some to add, with nothing beside it: 20 GB/s a CU
       const double stores = i == kBig && el != EL_F32 ? h.bm * h.bn * (oel == EL_F32 ? 4 : 2) * 1.5 / 20e3 : 0.0;
-      const double one = std::ceil(steps / parts) * h.alone * used + h.ends + stores;
-      const double full = std::ceil(steps / parts) * h.full * used + h.ends;
+      const double one = std::ceil(steps / parts) * h.alone[dir == kWeights] * used + h.ends + stores;
+      const double full = std::ceil(steps / parts) * h.full[dir == kWeights] * used + h.ends;
       double us = h.call + std::max(one, i == kBig && el != EL_F32 ? std::ceil(tiles) * one : tiles * full);
       if (dir != kWeights) us = std::max(us, matrices / (dir == kForward ? h.forward : h.rows) / 1e6);
       if (parts > 1) us += 2.0 + partial * 2 / 8e6;

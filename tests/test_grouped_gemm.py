@@ -136,6 +136,59 @@ def test_whole_numbers_are_exact_at_the_largest_tiles(dir, out):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dir", DIRS)
+def test_tensors_past_32_bits(dir):
+    """Rows whose first byte, and first element, lie past 2^32: 1.1 million of 4096 values, a few of them not zero."""
+    rows, wide, narrow = (1 << 20) + 70_000, 4096, 8
+    N, K = (wide, narrow) if dir == "weights" else (narrow, wide) if dir == "fwd" else (narrow, wide)
+    counts = [rows - 40, 0, 33]
+    at = offsets_of(counts).tolist()
+    some = torch.tensor([0, 1, 524_287, 524_288, 1_048_575, 1_048_576, rows - 41, rows - 40, rows - 20, rows - 8])
+    c = dict(a=ints((len(some), K), "bf16", 1), d_out=ints((len(some), N), "bf16", 2), w=ints((3, N, K), "bf16", 3))
+    spread = lambda v: torch.zeros(rows, v.shape[1], dtype=v.dtype, device="cuda").index_copy_(0, some.cuda(), v.cuda())  # noqa: E731
+    a = spread(c["a"]) if dir != "rows" else None
+    d_out = spread(c["d_out"]) if dir != "fwd" else None
+    shape = {"fwd": (rows, N), "rows": (rows, K), "weights": (3, N, K)}[dir]
+    out = torch.full(shape, 7.0, dtype=torch.bfloat16, device="cuda")
+    g = moe.make_groups(3, rows, N, K, "bf16", "bf16")
+    call(dir, g, a, d_out, c["w"].cuda(), offsets_of(counts).cuda(), out)
+    of = torch.bucketize(some, torch.tensor(at[1:]), right=True)
+    if dir == "weights":
+        ref = torch.stack([c["d_out"][of == e].double().T @ c["a"][of == e].double() for e in range(3)])
+        assert torch.equal(out.cpu(), ref.bfloat16())
+        return
+    m = c["w"].double()[of]
+    ref = torch.einsum("rk,rnk->rn", c["a"].double(), m) if dir == "fwd" else torch.einsum("rn,rnk->rk", c["d_out"].double(), m)
+    assert torch.equal(out[some.cuda()].cpu(), ref.bfloat16())
+    assert (out[rows - 7:] == 7).all()
+    out[rows - 7:] = 0
+    out[some.cuda()] = 0
+    assert not out.any()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("dir", DIRS)
+def test_workspace_is_as_large_as_said(dir, dtype):
+    """Reductions in parts: bytes behind the workspace stay, and what it held before does not matter."""
+    for counts, N, K in (([16], 1032, 4104), ([5000], 72, 136), ([700, 0, 41], 264, 2056)):
+        c, shape, rows = case(dir, counts, N, K, dtype, "f32", False, False)
+        gpu = {k: None if v is None else v.cuda() for k, v in c.items()}
+        g = moe.make_groups(len(counts), rows, N, K, dtype, "f32")
+        need = moe.grouped_gemm_workspace(g).nbytes
+        ref = reference(dir, counts, c["a"], c["d_out"], c["w"], None, None, rows)
+        for fill in (0, 255):
+            ws = torch.full((need + 4096,), fill, dtype=torch.uint8, device="cuda")
+            ws[need:] = 171
+            got = torch.full(shape, 777.0, device="cuda")
+            call(dir, g, gpu["a"], gpu["d_out"], gpu["w"], offsets_of(counts).cuda(), got, ws=ws[:need])
+            assert (ws[need:] == 171).all()
+            keep = slice(None) if dir == "weights" else slice(0, sum(counts))
+            assert torch.equal(got.cpu()[keep].double(), ref[keep])
+            assert dir == "weights" or (got[sum(counts):] == 777).all()
+
+
+@pytest.mark.gpu
 def test_a_slice_of_the_groups():
     """Offsets that start behind the first row: rows of the groups before and after stay, a reduction in parts, too."""
     counts, N, K = [70, 5003, 40], 264, 264

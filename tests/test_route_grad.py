@@ -152,6 +152,69 @@ def test_tokens_without_a_finite_key(renorm):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("E", [40, 512, 1000])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_a_counted_token_that_is_not_finite(E, bad):
+    """NaN, or an infinity's NaN, reaches the losses and that token's gradient, and no other token's."""
+    for whole_row in (False, True):
+        c = Case(6, E, 2, False, False, False)
+        ref = c.reference()
+        c.logits[2, slice(None) if whole_row else E - 1] = bad
+        loss, load, d = c.run()
+        assert loss.isnan().all() and d[2].isnan().all() and torch.equal(load.long(), ref[1])
+        c.mask = torch.tensor([1, 1, 0, 1, 1, 1], dtype=torch.uint8)
+        loss, load, d = c.run("f32", False, True)
+        ref = c.reference(False, True)
+        others = [0, 1, 3, 4, 5]
+        assert loss.isfinite().all() and not d[2].any()
+        assert ((d.double() - ref[2]).abs() <= ref[3] + U * ref[2].abs())[others].all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("low", [-1e4, -1e30, torch.finfo(torch.float32).min])
+@pytest.mark.parametrize("renorm", [True, False])
+def test_keys_of_the_lowest_value(renorm, low):
+    """Experts masked by a large negative number instead of -inf have probability 0, a token of nothing else equal ones.
+
+    Its lse is low + log E, whose log E fp32 drops at the larger two: the z loss of that token is left out of the comparison.
+    """
+    c = Case(8, 96, 4, renorm, False, False)
+    free = torch.ones(8, 96, dtype=torch.bool).scatter_(1, c.ids, False)
+    c.logits[free] = low
+    c.logits[5] = low
+    c.key = c.logits
+    top = torch.gather(c.logits.double(), 1, c.ids)
+    c.w = torch.softmax(top, 1).float()
+    if not renorm:
+        c.w[5] = 1 / 96
+    c.d_loss = torch.tensor([0.5, 0.0])
+    _, ref_load, ref, err = c.reference()
+    loss, load, d = c.run()
+    on = torch.tensor([0, 1, 2, 3, 4, 6, 7])
+    assert torch.equal(load.long(), ref_load) and d.isfinite().all()
+    assert ((d.double() - ref).abs() <= err + U * ref.abs()).all()
+    assert not d[on][free[on]].any()
+
+
+@pytest.mark.gpu
+def test_workspace_is_as_large_as_said():
+    """Bytes behind the workspace stay, and what it held before does not matter."""
+    for T, E in ((1, 8), (17, 63), (3000, 512)):
+        c = Case(T, E, 2, True, False, False)
+        logits, bias, packed, mask = c.on_gpu()
+        need = moe.route_loss_workspace(c.dims).nbytes
+        results = []
+        for fill in (0, 255):
+            ws = torch.full((need + 4096,), fill, dtype=torch.uint8, device="cuda")
+            ws[need:] = 171
+            loss, load = torch.empty(2, device="cuda"), torch.empty(E + 1, dtype=torch.int32, device="cuda")
+            moe.moe_route_loss(c.dims, logits, bias, packed, loss, load, mask=mask, ws=ws[:need])
+            assert (ws[need:] == 171).all()
+            results.append((loss, load))
+        assert torch.equal(results[0][0], results[1][0]) and torch.equal(results[0][1], results[1][1])
+
+
+@pytest.mark.gpu
 def test_an_expert_named_twice():
     """Gradients of slots with one id add up at that expert."""
     c = Case(4, 32, 4, True, False, False)
