@@ -6,11 +6,16 @@
 // offset (64 bits), so that the mask of an element depends on the seed, the offset and the element's place only, and
 // whoever asks again, the backward pass, a replayed graph, another launch shape, gets the same.  Element i of
 // the block owns 16 of the 128 bits; it is dropped where they are below low = round(65536 p).  16 bits an
-// element halve the generator's work against 32 (see below for what it costs) and move p by up to 2^-17; the factor of
-// the kept elements is 65536 / (65536 - low), by the p that is really applied.
+// element halve the generator's work against 32 and move p by up to 2^-17; the factor of the kept elements is
+// 65536 / (65536 - low), by the p that is really applied.
 //
 // A dropped element's result is chosen, not multiplied, to be zero: what its inputs hold, infinities and NaN too,
 // does not reach it.
+//
+// Bound by memory: a thread has one block of 8 elements, 16 bytes of each tensor, and all accesses go past the caches'
+// replacement.  The activation's gradient reads three bf16 tensors and writes three, 403 MB for 32768 rows of 1024, in 66 us
+// (6.1 TB/s); the activation 201 MB, and the residual sum as much for 8192 rows of 4096, in 33 us each.  The generator's ten rounds, 20 wide
+// products a block, hide behind the memory: with p = 0, which skips them, the three calls take as long.
 #include <algorithm>
 #include <type_traits>
 

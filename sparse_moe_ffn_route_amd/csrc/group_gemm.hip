@@ -9,7 +9,24 @@
 // is contiguous in memory: the reduction's (P and Q of kForward, P of kRows), or the tile's ("across": Q of
 // kRows, both of kWeights).  Either way the tile goes from memory straight into LDS as it lies, 16 bytes per
 // lane, and only the read from LDS differs: 16 bytes of 8 consecutive reduction indexes, or two transposing
-// reads that each hand 16 lanes the four reduction indexes of their own column.
+// reads that each hand 16 lanes the four reduction indexes of their own column.  The exclusive-or orders below leave the
+// larger tiles no bank conflicts (counted) in either.
+//
+// What bounds them.  10 rows of each of 64 groups, 1024 x 4096: the matrices' 537 MB, read in 86 us (6.3 TB/s; a read
+// of memory alone reaches 6.6).  512 rows a group: 275 GFLOP and 0.9 to 2.5 GB, in 330 us (kForward), 363 (kRows, with a
+// tensor added), 508 (kWeights, fp32 sums added to sums: 2.5 GB at 4.9 TB/s).  One 4096^3 product: products alone 77 us, loads
+// alone 51 to 71, LDS reads 30; they hide behind each other only in part: 102, 105, 112 us (1.35, 1.31, 1.23 PFLOP/s).
+//   - Two halves of a workgroup's waves in turn (TURNS), one reads LDS and asks for loads while the other multiplies:
+//     102 us against 118 to 128 with all waves in step.
+//   - A ring of five steps of 64 bytes against two of 128 (one group of 32768 rows, 1024 x 4096, matrices from
+//     memory): 235 against 258 us.  kWeights keeps two of 128: its rows are whole lines either way.
+//   - Smaller tiles at two or three workgroups a CU fill each other's gaps instead and cover each other's stores, with
+//     more to load a product; waves that multiply go first (kRows kWide 375 -> 365 us, kForward 355 -> 344, few rows of many
+//     groups 830 -> 773).  kWeights, which mostly waits for transposing reads, loses by it (506 -> 520) and has none.
+//   - A reduction that is long for the tiles there are is split into parts (16 x 4096 x 4096 kForward 22 -> 12.5 us, 8192
+//     rows into 512 x 512 49 -> 18), summed in order by a second launch: no atomics, the same bits every time.
+//   - A matrix that one tile row reads bypasses the caches' replacement (10 rows a group: 104 -> 86 us), as do
+//     kWeights' results (631 -> 606 us in kBig, with what they add to).
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -21,7 +38,7 @@ namespace moe {
 
 namespace {
 
-// LDS address of tile columns that a lane reads, typed for the transposing read.
+// What a lane has of a transposing read: four values of 16 bits.
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
 constexpr uint32_t kOut = 0x80000000u;  // a lane offset past every range: reads zeros, touches no memory
@@ -61,8 +78,9 @@ __device__ __forceinline__ void load16_to_lds(const u32x4& r, uint32_t lds_at, u
 // One operand's tile of W tile-index values by a step of RB reduction bytes (along) or RB / ES reduction
 // rows (across), in LDS, and how a workgroup of NT threads fills it.  16-byte chunks are stored in an order that
 // spreads the rows read together over the banks:
-//   along: W rows of RB bytes, chunk c of row r at c ^ swizzle(r), so that the 8 lanes of a read's cycle, 8
-//     consecutive rows at one chunk, take 8 different 16-byte slots of the 64 banks' 256 bytes;
+//   along: W rows of RB bytes, chunk c of row r at c ^ turn(r), so that the lanes of a read's cycle, consecutive rows at
+//     one chunk, take different 16-byte slots of the 64 banks' 256 bytes (of 256-byte rows two lanes share a slot: kFew
+//     waits for memory, and is no faster with all sixteen apart);
 //   across: RB / ES rows of W values.  A transposing read's half wave touches 32 bytes of each of the rows 0..3 and
 //     8..11 (of 16-bit values; a 32-bit read 64 bytes of the rows 0, 4, 8, 12): the run of 16 values is moved by an
 //     exclusive or that tells those rows apart.
@@ -369,7 +387,8 @@ __global__ __launch_bounds__(WM * WN * 64, MINB) void group_gemm_kernel(GroupGem
   uint32_t p_at[PP], q_at[QP];
   P::template places<WM>(wm, p_at);
   Q::template places<1>(wn * NF, q_at);
-  // Row fragments are dealt to the waves in turn, and those behind the tile's last row are left out.
+  // Row fragments are dealt to the waves in turn, and those behind the tile's last row are left out: every wave has its
+  // share of a tile that is not full.
   const int live = (tile_rows + 15) / 16 > wm ? ((tile_rows + 15) / 16 - wm + WM - 1) / WM : 0;
   f32x4 acc[MF][NF];
 #pragma unroll
@@ -429,7 +448,9 @@ __global__ __launch_bounds__(WM * WN * 64, MINB) void group_gemm_kernel(GroupGem
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks) {
         read(ks);
+        if (DIR != kWeights) __builtin_amdgcn_s_setprio(1);
         multiply();
+        if (DIR != kWeights) __builtin_amdgcn_s_setprio(0);
       }
       turn_buffers();
     }
@@ -544,22 +565,25 @@ __global__ __launch_bounds__(256) void join_kernel(const float* __restrict__ par
 
 // Tile shapes, and what a call of each is expected to take, in us, as measured over sizes from one tile to thousands:
 // `call` once; per tile and CU `ends` (first loads, last products, stores) and, per 64 indexes of a bf16 reduction (32
-// of an fp32 one), [0] `alone` where a CU has one tile at a time and `full` where its other tiles fill the gaps ([1]: of
-// kWeights, both of whose operands are read across); and no less than the matrices at the TB/s that kForward and kRows
-// stream them with.
+// of an fp32 one), `alone` where a CU has one tile at a time and `full` where its other tiles fill the gaps, of kForward,
+// kRows and kWeights, which read none, one and both of their operands across; and no less than the matrices at the
+// TB/s that kForward and kRows stream them with.  Over 150 calls drawn from one row to 2^28 weights the shape and parts chosen
+// here take 4 % longer than the best of all, as a geometric mean.  Two calls as examples, 64 groups of 512 rows, 1024
+// x 4096: kForward kWide 342, kBig 316 us; kRows, whose many short tiles leave kBig's stores uncovered, 363 and 390.
 struct Shape {
   int bm, bn;
-  double call, ends, alone[2], full[2], forward, rows;
+  double call, ends, alone[3], full[3], forward, rows;
 };
 enum : int { kSmall, kNarrow, kMiddle, kWide, kBig, kFew, kShapes };
-constexpr Shape kBf16Shapes[kShapes] = {{64, 64, 4.0, 0.9, {0.26, 0.34}, {0.21, 0.21}, 5.5, 5.4},
-                                        {64, 128, 4.5, 1.2, {0.38, 0.49}, {0.34, 0.30}, 5.2, 5.9},
-                                        {128, 128, 5.0, 2.0, {0.53, 0.65}, {0.55, 0.42}, 4.4, 5.5},
-                                        {128, 256, 5.0, 3.0, {0.66, 1.00}, {1.05, 0.80}, 4.2, 6.6},
-                                        {256, 256, 6.0, 3.0, {1.40, 1.47}, {1.40, 1.47}, 4.1, 5.2},
-                                        {32, 64, 4.0, 0.9, {0.21, 0.21}, {0.19, 0.19}, 6.3, 5.5}};
-constexpr Shape kF32Shapes[2] = {{64, 64, 4.0, 1.0, {0.55, 0.55}, {0.50, 0.50}, 5.5, 5.4},
-                                 {64, 128, 4.5, 1.5, {1.00, 1.00}, {0.95, 0.95}, 5.2, 5.9}};
+constexpr Shape kBf16Shapes[kShapes] = {
+    {64, 64, 4.0, 0.9, {0.26, 0.26, 0.34}, {0.21, 0.21, 0.21}, 5.5, 5.4},
+    {64, 128, 4.5, 1.2, {0.38, 0.38, 0.49}, {0.34, 0.34, 0.30}, 5.2, 5.9},
+    {128, 128, 5.0, 2.0, {0.53, 0.53, 0.65}, {0.55, 0.55, 0.42}, 4.4, 5.5},
+    {128, 256, 5.0, 3.0, {0.66, 0.66, 1.00}, {1.05, 1.05, 0.80}, 4.2, 6.6},
+    {256, 256, 6.0, 3.0, {1.40, 1.44, 1.47}, {1.40, 1.44, 1.47}, 4.1, 5.2},
+    {32, 64, 4.0, 0.9, {0.21, 0.21, 0.21}, {0.19, 0.19, 0.19}, 6.3, 5.5}};
+constexpr Shape kF32Shapes[2] = {{64, 64, 4.0, 1.0, {0.55, 0.55, 0.55}, {0.50, 0.50, 0.50}, 5.5, 5.4},
+                                 {64, 128, 4.5, 1.5, {1.00, 1.00, 1.00}, {0.95, 0.95, 0.95}, 5.2, 5.9}};
 
 template <int EL, int OEL, int DIR, int BM, int BN, int RB, int WM, int WN, int ST, int MINB, bool TURNS>
 void launch(const GroupGemm& p, int blocks, hipStream_t s) {
@@ -600,7 +624,7 @@ constexpr int64_t kPartialBytes = 64 << 20;  // most that the parts of a call ta
 // where groups share the rows evenly, whole or in parts that a second launch adds up.
 Plan plan(int dir, const GroupGemm& p, int el, int oel) {
   const int shapes = el == EL_F32 ? 2 : dir == kWeights ? kFew : kShapes;
-  const int step = el == EL_F32 ? 32 : 64;
+  const int step = el == EL_F32 ? 32 : 64, order = dir == kForward ? 0 : dir == kRows ? 1 : 2;
   const double busy = std::max(1.0, std::min<double>(p.n_groups, p.rows)), avg = p.rows / busy;
   // groups are seldom of one size, and the largest one's sum is what a call waits for: 33 us of a call of 16 groups of
   // very unequal sizes, 4903 rows in all, into 40 x 648 in one part, 19 in eight
@@ -623,8 +647,8 @@ Plan plan(int dir, const GroupGemm& p, int el, int oel) {
       const double tiles = mt * nt * parts / kCus;  // of a CU
       // the one tile of a CU stores its values, and reads some to add, with nothing beside it: 20 GB/s a CU
       const double stores = i == kBig && el != EL_F32 ? h.bm * h.bn * (oel == EL_F32 ? 4 : 2) * 1.5 / 20e3 : 0.0;
-      const double one = std::ceil(steps / parts) * h.alone[dir == kWeights] * used + h.ends + stores;
-      const double full = std::ceil(steps / parts) * h.full[dir == kWeights] * used + h.ends;
+      const double one = std::ceil(steps / parts) * h.alone[order] * used + h.ends + stores;
+      const double full = std::ceil(steps / parts) * h.full[order] * used + h.ends;
       double us = h.call + std::max(one, i == kBig && el != EL_F32 ? std::ceil(tiles) * one : tiles * full);
       if (dir != kWeights) us = std::max(us, matrices / (dir == kForward ? h.forward : h.rows) / 1e6);
       if (parts > 1) us += 2.0 + partial * 2 / 8e6;

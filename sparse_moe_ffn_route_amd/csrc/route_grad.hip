@@ -11,6 +11,11 @@
 // A wave takes one token at a time, its E <= 1024 keys in registers (up to 16 a lane), so each pass reads the logits
 // once.  The losses need sums over tokens: waves add up the p of their own tokens in registers, workgroups in
 // LDS, and one last workgroup adds the workgroups' sums in their order: no floating-point atomics.
+//
+// 8192 tokens of 512 experts read 17 MB twice and write 8: 9 us at memory's rate, but each token also costs three
+// passes over its registers and three sums over the wave, and there are three launches of 3 us at least: 32 us in
+// all, 10.8 the sums over tokens, 6.6 their joining, 11.6 the gradient.  Fewer workgroups of the first pass leave the
+// CUs idle, more make the joining longer; 128 of 16 waves was the least of both.  64 tokens of 16 experts: 10 us.
 #include <algorithm>
 #include <type_traits>
 
