@@ -6,9 +6,9 @@
 // for dy[t], which the token's waves, next to each other on one XCD, read from its L2.  The dot product is fp32: each
 // lane's own columns in order, then the lanes pairwise.
 //
-// Bound by memory: 8192 tokens of 10 slots, D = 4096, bf16, move 1.41 GB, rows and gradients once each and past the caches'
-// replacement, in 268 us (5.3 TB/s; a copy reaches 5.1).  Four waves a workgroup 268 us, two 272, eight 281; a workgroup
-// per token, dy read once into registers, 313 to 350: too little of it under way.
+// Bound by memory: 8192 tokens of 10 slots, D = 4096, bf16, move 1.41 GB, rows and gradients once each and past the
+// caches' replacement, in 268 us (5.3 TB/s; a copy reaches 5.1).  Four waves a workgroup 268 us, two 272, eight 281;
+// a workgroup per token, dy read once into registers, 313 to 350: too little of it under way.
 #include <algorithm>
 
 #include "common.hpp"

@@ -12,10 +12,11 @@
 // A dropped element's result is chosen, not multiplied, to be zero: what its inputs hold, infinities and NaN too,
 // does not reach it.
 //
-// Bound by memory: a thread has one block of 8 elements, 16 bytes of each tensor, and all accesses go past the caches'
-// replacement.  The activation's gradient reads three bf16 tensors and writes three, 403 MB for 32768 rows of 1024, in 66 us
-// (6.1 TB/s); the activation 201 MB, and the residual sum as much for 8192 rows of 4096, in 33 us each.  The generator's ten rounds, 20 wide
-// products a block, hide behind the memory: with p = 0, which skips them, the three calls take as long.
+// Bound by memory: a thread has one block of 8 elements, 16 bytes of each tensor, and all accesses go past the
+// caches' replacement.  The activation's gradient reads three bf16 tensors and writes three, 403 MB for 32768 rows of
+// 1024, in 66 us (6.1 TB/s); the activation 201 MB, and the residual sum as much for 8192 rows of 4096, in 33 us
+// each.  The generator's ten rounds, 20 wide products a block, hide behind the memory: with p = 0, which skips them,
+// the three calls take as long.
 #include <algorithm>
 #include <type_traits>
 

@@ -13,18 +13,19 @@
 // larger tiles no bank conflicts (counted) in either.
 //
 // What bounds them.  10 rows of each of 64 groups, 1024 x 4096: the matrices' 537 MB, read in 86 us (6.3 TB/s; a read
-// of memory alone reaches 6.6).  512 rows a group: 275 GFLOP and 0.9 to 2.5 GB, in 330 us (kForward), 363 (kRows, with a
-// tensor added), 508 (kWeights, fp32 sums added to sums: 2.5 GB at 4.9 TB/s).  One 4096^3 product: products alone 77 us, loads
-// alone 51 to 71, LDS reads 30; they hide behind each other only in part: 102, 105, 112 us (1.35, 1.31, 1.23 PFLOP/s).
+// of memory alone reaches 6.6).  512 rows a group: 275 GFLOP and 0.9 to 2.5 GB, in 320 us (kForward), 355 (kRows,
+// with a tensor added), 508 (kWeights, fp32 sums added to sums: 2.5 GB at 4.9 TB/s).  One 4096^3 product: products
+// alone 77 us, loads alone 51 to 71, LDS reads 30; they hide behind each other only in part: 102, 105, 112 us (1.35,
+// 1.31, 1.23 PFLOP/s).
 //   - Two halves of a workgroup's waves in turn (TURNS), one reads LDS and asks for loads while the other multiplies:
 //     102 us against 118 to 128 with all waves in step.
 //   - A ring of five steps of 64 bytes against two of 128 (one group of 32768 rows, 1024 x 4096, matrices from
 //     memory): 235 against 258 us.  kWeights keeps two of 128: its rows are whole lines either way.
-//   - Smaller tiles at two or three workgroups a CU fill each other's gaps instead and cover each other's stores, with
-//     more to load a product; waves that multiply go first (kRows kWide 375 -> 365 us, kForward 355 -> 344, few rows of many
-//     groups 830 -> 773).  kWeights, which mostly waits for transposing reads, loses by it (506 -> 520) and has none.
-//   - A reduction that is long for the tiles there are is split into parts (16 x 4096 x 4096 kForward 22 -> 12.5 us, 8192
-//     rows into 512 x 512 49 -> 18), summed in order by a second launch: no atomics, the same bits every time.
+//   - Smaller tiles at two or three workgroups a CU fill each other's gaps instead and cover each other's stores,
+//     with more to load a product; waves that multiply go first (512 rows a group: kRows in kWide 375 -> 365 us,
+//     kForward in kWide 355 -> 344, in kFew 830 -> 773).  kWeights loses by that (506 -> 520) and has none of it.
+//   - A reduction that is long for the tiles there are is split into parts (16 x 4096 x 4096 kForward 22 -> 12.5 us,
+//     8192 rows into 512 x 512 49 -> 18), summed in order by a second launch: no atomics, the same bits every time.
 //   - A matrix that one tile row reads bypasses the caches' replacement (10 rows a group: 104 -> 86 us), as do
 //     kWeights' results (631 -> 606 us in kBig, with what they add to).
 #include <algorithm>
@@ -488,7 +489,8 @@ __global__ __launch_bounds__(WM * WN * 64, MINB) void group_gemm_kernel(GroupGem
 #pragma unroll
       for (int x = 0; x < kPieces; ++x) {
         const int row = row_of(m0, x);
-        to[x] = here && row < tile_rows ? __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(static_cast<const uint8_t*>(p.add) + place(row) * (16 / V))) : u32x4{};
+        const auto* from = static_cast<const uint8_t*>(p.add) + place(row) * (16 / V);
+        to[x] = here && row < tile_rows ? __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(from)) : u32x4{};
       }
     };
     fetch(0, more[0]);
@@ -567,9 +569,9 @@ __global__ __launch_bounds__(256) void join_kernel(const float* __restrict__ par
 // `call` once; per tile and CU `ends` (first loads, last products, stores) and, per 64 indexes of a bf16 reduction (32
 // of an fp32 one), `alone` where a CU has one tile at a time and `full` where its other tiles fill the gaps, of kForward,
 // kRows and kWeights, which read none, one and both of their operands across; and no less than the matrices at the
-// TB/s that kForward and kRows stream them with.  Over 150 calls drawn from one row to 2^28 weights the shape and parts chosen
-// here take 4 % longer than the best of all, as a geometric mean.  Two calls as examples, 64 groups of 512 rows, 1024
-// x 4096: kForward kWide 342, kBig 316 us; kRows, whose many short tiles leave kBig's stores uncovered, 363 and 390.
+// TB/s that kForward and kRows stream them with.  Over 150 calls, from one row to 2^28 weights, the shape and parts
+// chosen here take 4 % longer than the best of all, as a geometric mean.  Two calls as examples, 64 groups of 512 rows,
+// 1024 x 4096: kForward kWide 342, kBig 316 us; kRows, whose many short tiles leave kBig's stores uncovered, 363, 390.
 struct Shape {
   int bm, bn;
   double call, ends, alone[3], full[3], forward, rows;
@@ -640,7 +642,8 @@ Plan plan(int dir, const GroupGemm& p, int el, int oel) {
     // a group's rows end inside a tile
     const double mt = dir == kWeights ? p.n_groups * std::ceil(static_cast<double>(p.out_rows) / h.bm)
                       : busy == 1 || avg <= h.bm * 0.75 ? busy * std::ceil(avg / h.bm) : busy * (avg / h.bm + 0.5);
-    const double used = dir == kWeights ? 1.0 : 0.6 + 0.4 * std::min(1.0, avg / h.bm);  // rows that are not there are not read
+    // rows that are not there are neither read nor multiplied
+    const double used = dir == kWeights ? 1.0 : 0.6 + 0.4 * std::min(1.0, avg / h.bm);
     for (int parts = 1; parts <= 16; parts *= 2) {
       const double partial = out_rows * p.cols * 4 * parts;
       if (parts > 1 && (steps / parts < 4 || partial > kPartialBytes)) break;

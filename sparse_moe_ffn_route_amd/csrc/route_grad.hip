@@ -260,7 +260,8 @@ __global__ __launch_bounds__(kFinish) void loss_finish_kernel(RouteGrad p, const
 template <int OEL, int NC, bool VEC>
 __global__ __launch_bounds__(kGradWaves* kWave) void route_grad_kernel(RouteGrad p) {
   const int lane = lane_id();
-  const int64_t t = (static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x) * kGradWaves + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int64_t t = (static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x) * kGradWaves +
+                    __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   if (t >= p.T) return;
   const bool losses = p.d_loss != nullptr, soft = losses || !p.renormalize;
   // everything is asked for before anything is used
