@@ -551,8 +551,10 @@ int moe_permute_backward(const moe_dims* dims, const void* d_x_perm, const int32
  * dims' T, E, top_k and renormalize are used (all E experts, whatever the local slice).
  *
  *   logits     [T][E] fp32 as moe_route wrote or took them;  logit_bias [E] fp32 or NULL.  -inf keys have probability 0;
- *              a token whose keys are all -inf adds nothing, one with a NaN or +inf key makes the losses and its own
- *              gradient NaN.  Masked tokens' logits are not used by the losses
+ *              a token whose keys are all -inf adds nothing to the losses and has a gradient of zeros, where its
+ *              routing weights are the NaN of such keys' softmax or 0.  One with a NaN or +inf key makes the losses NaN,
+ *              and its own gradient from them and, renormalize = 0, from the weights; renormalised weights' gradient
+ *              takes the weights as they are.  Masked tokens' logits are not used by the losses
  *   packed     [T][2][top_k] int32, the routing (ids outside [0, E) count for no expert)
  *   mask       [T] bytes, 0 = not counted (padding), or NULL: all tokens
  *   loss       [2] fp32 out;  load [E + 1] int32 out: the loads, then n.  To balance over several devices' tokens, add up

@@ -297,6 +297,13 @@ __global__ __launch_bounds__(kGradWaves* kWave) void route_grad_kernel(RouteGrad
     lse = softmax<NC>(v);
   }
   if (p.d_w) {
+    if (__ballot(w != w)) {
+      // Keys that are all -inf have NaN for weights and take no gradient from them; any other NaN goes on.
+      bool some = false;
+      for (int e = lane; e < p.E; e += kWave)
+        some |= !(p.logits[t * p.E + e] + (p.bias ? p.bias[e] : 0.0f) == -INFINITY);
+      if (!__ballot(some)) w = dw = 0.0f;
+    }
     const float mean = sum_of(w * dw);
     // of a slot: what is added at its expert
     const float mine = p.renormalize ? w * (dw - mean) : dw;

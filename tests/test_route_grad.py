@@ -152,6 +152,31 @@ def test_tokens_without_a_finite_key(renorm):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("weight", [float("nan"), 0.0])
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("E", [40, 63, 512, 1000])
+def test_no_gradient_from_the_weights_of_a_token_without_a_finite_key(E, renorm, weight):
+    """All keys -inf: no gradient from weights that are their softmax's NaN, or 0."""
+    for parts in ((True, False), (True, True)):
+        c = Case(6, E, 2, renorm, False, False)
+        c.bias = torch.linspace(-1, 1, E)
+        c.key = c.logits + c.bias
+        top, ids = c.key.double().sort(dim=1, descending=True, stable=True)
+        c.ids, w = ids[:, :2], torch.softmax(top, 1)[:, :2]
+        c.w = (w / w.sum(1, keepdim=True) if renorm else w).float()
+        on = torch.tensor([1, 1, 0, 1, 1, 1], dtype=torch.uint8)
+        c.mask = on
+        _, _, ref, err = c.reference(*parts)   # of the other tokens, with token 2 outside the losses
+        c.logits[2] = -float("inf")
+        c.w[2] = weight
+        for c.mask in (on, None):
+            loss, load, d = c.run("f32", *parts)
+            assert loss.isfinite().all() and not d[2].any()
+            if c.mask is not None or not parts[1]:
+                assert ((d.double() - ref).abs() <= err + U * ref.abs())[on != 0].all()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("E", [40, 512, 1000])
 @pytest.mark.parametrize("bad", [float("nan"), float("inf")])
 def test_a_counted_token_that_is_not_finite(E, bad):
