@@ -14,6 +14,8 @@
 // slots are taken in batches of 8: all of a batch's row loads (and the shared row) are
 // issued before the first is summed, so a wave keeps up to 9 row pieces in flight; the
 // sum itself still runs in slot order.
+#include <algorithm>
+
 #include "common.hpp"
 #include "kernels.hpp"
 
@@ -136,15 +138,23 @@ __global__ __launch_bounds__(256) void combine_kernel(const void* __restrict__ o
 
 hipError_t launch_combine(int out_el, const void* out_rows, const int32_t* packed, const int32_t* inv_pos,
                           const void* shared_out, int T, int D, int k, void* y, hipStream_t stream) {
-  if (T == 0) return hipSuccess;
   const int chunks = (D + 511) / 512;
-  const int waves = T * chunks;
-  dim3 grid((waves + 3) / 4);
-  auto launch = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, grid, dim3(256), 0, stream, out_rows, packed, inv_pos, shared_out, T, D, k, chunks, y);
-  };
-  if (out_el == EL_BF16) packed ? launch(combine_kernel<EL_BF16, false>) : launch(combine_kernel<EL_BF16, true>);
-  else packed ? launch(combine_kernel<EL_F32, false>) : launch(combine_kernel<EL_F32, true>);
+  // A grid dimension holds less than 2^32 threads, which is 2^26 waves: tokens in slices of 2^24 waves, as many
+  // launches.
+  const int per = std::max(1, (1 << 24) / chunks);
+  const size_t row_bytes = static_cast<size_t>(D) * (out_el == EL_BF16 ? 2 : 4);
+  for (int64_t t0 = 0; t0 < T; t0 += per) {
+    const int n = static_cast<int>(std::min<int64_t>(per, T - t0));
+    const int32_t* blob = packed ? packed + t0 * 2 * k : nullptr;
+    const void* more = shared_out ? static_cast<const uint8_t*>(shared_out) + t0 * row_bytes : nullptr;
+    void* out = static_cast<uint8_t*>(y) + t0 * row_bytes;
+    const dim3 grid((n * chunks + 3) / 4);
+    auto launch = [&](auto kernel) {
+      hipLaunchKernelGGL(kernel, grid, dim3(256), 0, stream, out_rows, blob, inv_pos + t0 * k, more, n, D, k, chunks, out);
+    };
+    if (out_el == EL_BF16) packed ? launch(combine_kernel<EL_BF16, false>) : launch(combine_kernel<EL_BF16, true>);
+    else packed ? launch(combine_kernel<EL_F32, false>) : launch(combine_kernel<EL_F32, true>);
+  }
   return hipGetLastError();
 }
 

@@ -79,6 +79,29 @@ def test_permute_backward(T, D, E, k, local, act):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("T,D", [((1 << 26) + 3, 64), ((1 << 25) + 3, 576)])
+def test_more_tokens_than_a_grid_dimension_holds(T, D):
+    """2^26 waves and more, which are 2^32 threads: the permutation's gradient and the combine itself, every row."""
+    d = moe.make_dims(T, D, 2, 1, 64)
+    rows = torch.empty(T, D, dtype=torch.bfloat16, device="cuda").random_(-8, 9)
+    inv = torch.arange(T, device="cuda", dtype=torch.int32).flip(0).contiguous()
+    inv[::7] = -1
+    packed = torch.zeros(T, 2, 1, dtype=torch.int32, device="cuda")
+    packed[:, 1] = torch.tensor(2.0).view(torch.int32).item()
+    out = torch.empty_like(rows)
+    for weight, call in ((1, lambda: moe.moe_permute_backward(d, rows, inv, out)),
+                         (2, lambda: moe.moe_unpermute_combine(d, rows, packed, inv, None, out))):
+        out.fill_(777.0)
+        call()
+        for t in range(0, T, 1 << 21):
+            at = inv[t:t + (1 << 21), None].long()
+            want = torch.where(at >= 0, rows[at[:, 0].clamp_min(0)] * weight, 0)
+            assert torch.equal(out[t:t + (1 << 21)], want), (weight, t)
+    del rows, inv, packed, out, want
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.gpu
 def test_combine_backward_random_values():
     """Random weights and rows: a product and its rounding per row value; dots of D exact products and as many sums."""
     T, D, E, k = 40, 1024, 32, 6
