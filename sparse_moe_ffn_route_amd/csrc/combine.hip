@@ -71,13 +71,14 @@ __device__ __forceinline__ void store8(void* base, size_t idx, const float v[8])
   }
 }
 
-// UNIT: every weight is one and packed is not read (the gradient of the permutation).
+// UNIT: every weight is one and packed is not read (the gradient of the permutation).  y may be shared_out: a lane reads
+// the columns that it writes, before it writes them, and no others.
 template <int OUT, bool UNIT>
 __global__ __launch_bounds__(256) void combine_kernel(const void* __restrict__ out_rows,
                                                       const int32_t* __restrict__ packed,
                                                       const int32_t* __restrict__ inv_pos,
-                                                      const void* __restrict__ shared_out, int T, int D, int k,
-                                                      int chunks, void* __restrict__ y) {
+                                                      const void* shared_out, int T, int D, int k, int chunks,
+                                                      void* y) {
   constexpr int kBatch = 8;
   // wave-uniform by construction; readfirstlane lets the slot metadata load as scalars
   const int wid = __builtin_amdgcn_readfirstlane(blockIdx.x * 4 + threadIdx.x / kWave);

@@ -79,6 +79,23 @@ def test_permute_backward(T, D, E, k, local, act):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("act", list(DT))
+@pytest.mark.parametrize("T,D,k", [(1, 64, 1), (700, 576, 10), (4096, 1024, 32)])
+def test_adding_in_place_gives_the_same_bits(T, D, k, act):
+    """d_x = add's own memory, call after call, against d_x apart from it."""
+    g = torch.Generator(device="cuda").manual_seed(T)
+    d = moe.make_dims(T, D, 32, k, 64, act=act, w=act, out=act)
+    rows = torch.randn(T * k, D, generator=g, device="cuda").to(DT[act])
+    inv = torch.randperm(T * k, generator=g, device="cuda").int().reshape(T, k)
+    inv[::3, k // 2] = -1
+    here, apart = torch.randn(T, D, generator=g, device="cuda").to(DT[act]), torch.empty(T, D, dtype=DT[act], device="cuda")
+    for _ in range(3):
+        moe.moe_permute_backward(d, rows, inv, apart, add=here)
+        moe.moe_permute_backward(d, rows, inv, here, add=here)
+        assert torch.equal(here, apart)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("T,D", [((1 << 26) + 3, 64), ((1 << 25) + 3, 576)])
 def test_more_tokens_than_a_grid_dimension_holds(T, D):
     """2^26 waves and more, which are 2^32 threads: the permutation's gradient and the combine itself, every row."""
