@@ -62,7 +62,7 @@ __device__ __forceinline__ void wait_step() {
 // buffer_load16_to_lds with the LDS address as a number, as an instruction that the compiler does not count: told of it,
 // the compiler waits for all such loads before every transposing read, which it cannot tell apart from them, and
 // with that for the step that was only just asked for.  The kernel waits for its steps itself.  The first wait is
-// for the scalars' writers, the second for m0's.
+// for the scalars' writers, the second for m0's; no other instruction of the kernels here takes m0.
 template <bool NT = false>
 __device__ __forceinline__ void load16_to_lds(const u32x4& r, uint32_t lds_at, uint32_t voff, uint32_t soff) {
   auto scalar = [](uint32_t v) { return static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(v)); };
@@ -70,10 +70,10 @@ __device__ __forceinline__ void load16_to_lds(const u32x4& r, uint32_t lds_at, u
   const u32x4 rs{scalar(r[0]), scalar(r[1]), scalar(r[2]), scalar(r[3])};
   if constexpr (NT)
     asm volatile("s_nop 4\n\ts_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen nt lds"
-                 :: "s"(lds), "v"(voff), "s"(rs), "s"(s) : "memory", "m0");
+                 :: "s"(lds), "v"(voff), "s"(rs), "s"(s) : "memory");
   else
     asm volatile("s_nop 4\n\ts_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
-                 :: "s"(lds), "v"(voff), "s"(rs), "s"(s) : "memory", "m0");
+                 :: "s"(lds), "v"(voff), "s"(rs), "s"(s) : "memory");
 }
 
 // One operand's tile of W tile-index values by a step of RB reduction bytes (along) or RB / ES reduction
