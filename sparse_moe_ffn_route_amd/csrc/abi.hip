@@ -481,12 +481,13 @@ int check_groups(const moe_groups* g) {
 
 GroupGemm group_problem(const moe_groups& g, int dir) {
   GroupGemm p{};
-  p.n_groups = g.n_groups;
-  p.rows = g.rows;
-  p.w_stride = static_cast<int64_t>(g.N) * g.K;
-  p.cols = dir == kForward ? g.N : g.K;
-  p.red = dir == kForward ? g.K : g.N;
-  p.out_rows = g.N;
+  const GroupSizes s = group_sizes(dir, g.n_groups, g.rows, g.N, g.K);
+  p.n_groups = s.n_groups;
+  p.rows = s.rows;
+  p.w_stride = s.w_stride;
+  p.cols = s.cols;
+  p.red = s.red;
+  p.out_rows = s.out_rows;
   p.ldp = dir == kForward ? g.K : g.N;
   p.ldq = g.K;
   return p;

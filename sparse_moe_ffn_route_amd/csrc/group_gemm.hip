@@ -29,13 +29,14 @@
 //   - A matrix that one tile row reads bypasses the caches' replacement (10 rows a group: 104 -> 86 us), as do
 //     kWeights' results (631 -> 606 us in kBig, with what they add to).
 #include <algorithm>
-#include <cmath>
 #include <type_traits>
 
 #include "common.hpp"
 #include "kernels.hpp"
 
 namespace moe {
+
+using namespace groups;  // group_plan.hpp
 
 namespace {
 
@@ -565,28 +566,6 @@ __global__ __launch_bounds__(256) void join_kernel(const float* __restrict__ par
   }
 }
 
-// Tile shapes, and what a call of each is expected to take, in us, as measured over sizes from one tile to thousands:
-// `call` once; per tile and CU `ends` (first loads, last products, stores) and, per 64 indexes of a bf16 reduction (32
-// of an fp32 one), `alone` where a CU has one tile at a time and `full` where its other tiles fill the gaps, of kForward,
-// kRows and kWeights, which read none, one and both of their operands across; and no less than the matrices at the
-// TB/s that kForward and kRows stream them with.  Over 150 calls, from one row to 2^28 weights, the shape and parts
-// chosen here take 4 % longer than the best of all, as a geometric mean.  Two calls as examples, 64 groups of 512 rows,
-// 1024 x 4096: kForward kWide 342, kBig 316 us; kRows, whose many short tiles leave kBig's stores uncovered, 363, 390.
-struct Shape {
-  int bm, bn;
-  double call, ends, alone[3], full[3], forward, rows;
-};
-enum : int { kSmall, kNarrow, kMiddle, kWide, kBig, kFew, kShapes };
-constexpr Shape kBf16Shapes[kShapes] = {
-    {64, 64, 4.0, 0.9, {0.26, 0.26, 0.34}, {0.21, 0.21, 0.21}, 5.5, 5.4},
-    {64, 128, 4.5, 1.2, {0.38, 0.38, 0.49}, {0.34, 0.34, 0.30}, 5.2, 5.9},
-    {128, 128, 5.0, 2.0, {0.53, 0.53, 0.65}, {0.55, 0.55, 0.42}, 4.4, 5.5},
-    {128, 256, 5.0, 3.0, {0.66, 0.66, 1.00}, {1.05, 1.05, 0.80}, 4.2, 6.6},
-    {256, 256, 6.0, 3.0, {1.40, 1.44, 1.47}, {1.40, 1.44, 1.47}, 4.1, 5.2},
-    {32, 64, 4.0, 0.9, {0.21, 0.21, 0.21}, {0.19, 0.19, 0.19}, 6.3, 5.5}};
-constexpr Shape kF32Shapes[2] = {{64, 64, 4.0, 1.0, {0.55, 0.55, 0.55}, {0.50, 0.50, 0.50}, 5.5, 5.4},
-                                 {64, 128, 4.5, 1.5, {1.00, 1.00, 1.00}, {0.95, 0.95, 0.95}, 5.2, 5.9}};
-
 template <int EL, int OEL, int DIR, int BM, int BN, int RB, int WM, int WN, int ST, int MINB, bool TURNS>
 void launch(const GroupGemm& p, int blocks, hipStream_t s) {
   hipLaunchKernelGGL((group_gemm_kernel<EL, OEL, DIR, BM, BN, RB, WM, WN, ST, MINB, TURNS>), dim3(blocks),
@@ -614,78 +593,24 @@ void launch_types(int el, int oel, int shape, const GroupGemm& p, int blocks, hi
   else launch_shape<EL_BF16, EL_BF16, DIR>(shape, p, blocks, s);
 }
 
-struct Plan {
-  int shape, parts, high;
-  int64_t blocks;
-};
-
-constexpr double kCus = 256;
-constexpr int64_t kPartialBytes = 64 << 20;  // most that the parts of a call take of a workspace
-
-// Shape, parts of the reduction and most workgroups of a call: the least of what the shapes are expected to take,
-// where groups share the rows evenly, whole or in parts that a second launch adds up.
-Plan plan(int dir, const GroupGemm& p, int el, int oel) {
-  const int shapes = el == EL_F32 ? 2 : dir == kWeights ? kFew : kShapes;
-  const int step = el == EL_F32 ? 32 : 64, order = dir == kForward ? 0 : dir == kRows ? 1 : 2;
-  const double busy = std::max(1.0, std::min<double>(p.n_groups, p.rows)), avg = p.rows / busy;
-  // groups are seldom of one size, and the largest one's sum is what a call waits for: 33 us of a call of 16 groups of
-  // very unequal sizes, 4903 rows in all, into 40 x 648 in one part, 19 in eight
-  const double red = dir == kWeights ? std::min<double>(p.rows, 2.0 * avg) : p.red;
-  const double out_rows = dir == kWeights ? static_cast<double>(p.n_groups) * p.out_rows : p.rows;
-  const double steps = std::max(1.0, std::ceil(red / step));
-  const double matrices = busy * p.w_stride * (el == EL_F32 ? 4 : 2);
-  Plan best{};
-  double least = 0;
-  for (int i = 0; i < shapes; ++i) {
-    const Shape& h = el == EL_F32 ? kF32Shapes[i] : kBf16Shapes[i];
-    const double nt = std::ceil(static_cast<double>(p.cols) / h.bn);
-    // a group's rows end inside a tile
-    const double mt = dir == kWeights ? p.n_groups * std::ceil(static_cast<double>(p.out_rows) / h.bm)
-                      : busy == 1 || avg <= h.bm * 0.75 ? busy * std::ceil(avg / h.bm) : busy * (avg / h.bm + 0.5);
-    // rows that are not there are neither read nor multiplied
-    const double used = dir == kWeights ? 1.0 : 0.6 + 0.4 * std::min(1.0, avg / h.bm);
-    for (int parts = 1; parts <= 16; parts *= 2) {
-      const double partial = out_rows * p.cols * 4 * parts;
-      if (parts > 1 && (steps / parts < 4 || partial > kPartialBytes)) break;
-      const double tiles = mt * nt * parts / kCus;  // of a CU
-      // the one tile of a CU stores its values, and reads some to add, with nothing beside it: 20 GB/s a CU
-      const double stores = i == kBig && el != EL_F32 ? h.bm * h.bn * (oel == EL_F32 ? 4 : 2) * 1.5 / 20e3 : 0.0;
-      const double one = std::ceil(steps / parts) * h.alone[order] * used + h.ends + stores;
-      const double full = std::ceil(steps / parts) * h.full[order] * used + h.ends;
-      double us = h.call + std::max(one, i == kBig && el != EL_F32 ? std::ceil(tiles) * one : tiles * full);
-      if (dir != kWeights) us = std::max(us, matrices / (dir == kForward ? h.forward : h.rows) / 1e6);
-      if (parts > 1) us += 2.0 + partial * 2 / 8e6;
-      if (best.parts == 0 || us < least) {
-        least = us;
-        best.shape = i;
-        best.parts = parts;
-      }
-    }
-  }
-  const Shape& h = el == EL_F32 ? kF32Shapes[best.shape] : kBf16Shapes[best.shape];
-  const int64_t nt = (p.cols + h.bn - 1) / h.bn;
-  const int64_t mt = dir == kWeights
-                         ? static_cast<int64_t>(p.n_groups) * ((p.out_rows + h.bm - 1) / h.bm)
-                         : (static_cast<int64_t>(p.rows) + static_cast<int64_t>(p.n_groups) * (h.bm - 1)) / h.bm;
-  best.high = h.bm;
-  best.blocks = mt * nt * best.parts;
-  return best;
+Plan plan_of(int dir, int el, int oel, const GroupGemm& p) {
+  return plan(dir, GroupSizes{p.n_groups, p.rows, p.w_stride, p.cols, p.red, p.out_rows}, el == EL_F32, oel == EL_F32);
 }
 
 }  // namespace
 
 size_t group_gemm_workspace(int dir, int el, int oel, const GroupGemm& p) {
-  const Plan r = plan(dir, p, el, oel);
+  const Plan r = plan_of(dir, el, oel, p);
   const int64_t rows = dir == kWeights ? static_cast<int64_t>(p.n_groups) * p.out_rows : p.rows;
   return r.parts > 1 ? static_cast<size_t>(rows) * p.cols * r.parts * 4 : 0;
 }
 
 bool group_gemm_fits(int dir, int el, int oel, const GroupGemm& p) {
-  return plan(dir, p, el, oel).blocks < (1ll << 32) / 512;  // of threads, which a grid dimension counts
+  return plan_of(dir, el, oel, p).blocks < (1ll << 32) / 512;  // of threads, which a grid dimension counts
 }
 
 hipError_t launch_group_gemm(int dir, int el, int oel, GroupGemm p, void* ws, hipStream_t s) {
-  const Plan r = plan(dir, p, el, oel);
+  const Plan r = plan_of(dir, el, oel, p);
   if (r.blocks == 0) return hipSuccess;
   const int64_t rows = dir == kWeights ? static_cast<int64_t>(p.n_groups) * p.out_rows : p.rows;
   p.parts = r.parts;

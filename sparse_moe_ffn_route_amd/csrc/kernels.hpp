@@ -5,6 +5,7 @@
 #include <stdint.h>
 
 #include "gemm.hpp"
+#include "group_plan.hpp"
 
 namespace moe {
 
@@ -185,9 +186,7 @@ struct BlockNorm {
 };
 hipError_t launch_block_norm(int el, int y_el, const BlockNorm& p, hipStream_t stream);
 
-// Products grouped by expert and their gradients (see group_gemm.hip).  Output tile rows are rows of the groups
-// (kForward, kRows) or of the weight matrices (kWeights).
-enum : int { kForward = 0, kRows = 1, kWeights = 2 };
+// Products grouped by expert and their gradients (see group_gemm.hip; directions: group_plan.hpp).
 struct GroupGemm {
   const void* p;           // operand of the output's rows: a, d_out, d_out
   const void* q;           // operand of its columns: w, w, a
