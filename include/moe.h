@@ -441,7 +441,7 @@ int moe_block_forward(const moe_dims* dims, const moe_weights* weights, const vo
 typedef struct moe_groups {
   int32_t n_groups;  /* 1 .. 1024 */
   int32_t rows;      /* rows that the grouped tensors hold, at most 2^30 */
-  int32_t N, K;      /* multiples of 8, at most 2^20 */
+  int32_t N, K;      /* multiples of 8, at most 2^20; no tensor of more than 2^40 elements */
   int32_t in_dtype;  /* of operands: MOE_F32 or MOE_BF16 */
   int32_t out_dtype; /* of the result: MOE_F32, or MOE_BF16 with in_dtype MOE_BF16 */
 } moe_groups;

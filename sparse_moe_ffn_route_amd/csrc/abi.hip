@@ -469,11 +469,14 @@ BlockLayout block_layout(const moe_dims& d) {
 
 // Products grouped by expert: rows and matrices are addressed from 64-bit bases with 32-bit offsets inside a tile.
 constexpr int32_t kGroupMaxWidth = 1 << 20;
+constexpr int64_t kGroupMaxElements = 1ll << 40;  // of a tensor: its tiles, of 32 x 64 at least, are counted in 32 bits
 int check_groups(const moe_groups* g) {
   if (!g) return MOE_ERR_NULL_ARG;
   if (g->n_groups < 1 || g->rows < 0 || g->N < 1 || g->K < 1) return MOE_ERR_BAD_DIMS;
   if (g->n_groups > kMaxLocalExperts || g->rows > (1 << 30)) return MOE_ERR_UNSUPPORTED;
   if (g->N % 8 || g->K % 8 || g->N > kGroupMaxWidth || g->K > kGroupMaxWidth) return MOE_ERR_UNSUPPORTED;
+  const int64_t rows = g->rows, N = g->N, K = g->K;
+  if (std::max({rows * N, rows * K, g->n_groups * N * K}) > kGroupMaxElements) return MOE_ERR_UNSUPPORTED;
   const bool f32 = g->in_dtype == MOE_F32 && g->out_dtype == MOE_F32;
   const bool bf16 = g->in_dtype == MOE_BF16 && (g->out_dtype == MOE_BF16 || g->out_dtype == MOE_F32);
   return f32 || bf16 ? MOE_OK : MOE_ERR_UNSUPPORTED;
@@ -510,7 +513,6 @@ int grouped_gemm(const moe_groups* g, int dir, const void* p, const void* q, int
   if (need && !ws) return MOE_ERR_NULL_ARG;
   if (ws_bytes < need) return MOE_ERR_WORKSPACE;
   m.p = p; m.q = q; m.out = out; m.add = add; m.offsets = offsets; m.index = index; m.src_rows = src_rows;
-  if (!group_gemm_fits(dir, g->in_dtype, g->out_dtype, m)) return MOE_ERR_UNSUPPORTED;
   return hip_status(launch_group_gemm(dir, g->in_dtype, g->out_dtype, m, ws, static_cast<hipStream_t>(stream)));
 }
 

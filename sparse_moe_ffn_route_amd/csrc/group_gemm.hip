@@ -186,7 +186,7 @@ __device__ __forceinline__ bool find_rows(const GroupGemm& p, int n_tiles, int b
     const int2 v = group_rows(p, min(g, p.n_groups - 1));
     if (i == 0) r = v;
     if (g < p.n_groups) mine += tiles_of(v);
-    mine = min(mine, 1 << 24);  // more than any launch has: offsets that overlap must not overflow
+    mine = min(mine, kMaxTileRows);  // more than any call has: offsets that overlap must not overflow
   }
   int upto = mine;
 #pragma unroll
@@ -240,7 +240,7 @@ __global__ __launch_bounds__(WM * WN * 64, MINB) void group_gemm_kernel(GroupGem
   Place at;
   if constexpr (DIR == kWeights) {
     const int m_tiles = (p.out_rows + BM - 1) / BM;
-    int L = xcd_remap(blockIdx.x, gridDim.x);
+    int L = xcd_remap(p.first + blockIdx.x, p.blocks);
     at.part = L % p.parts;
     L /= p.parts;
     at.g = L / (m_tiles * n_tiles);
@@ -251,7 +251,7 @@ __global__ __launch_bounds__(WM * WN * 64, MINB) void group_gemm_kernel(GroupGem
     at.begin = __builtin_amdgcn_readfirstlane(r.x);
     at.end = __builtin_amdgcn_readfirstlane(r.y);
   } else {
-    if (!find_rows(p, n_tiles, blockIdx.x, at)) return;
+    if (!find_rows(p, n_tiles, p.first + blockIdx.x, at)) return;
   }
   at.col0 *= BN;
   const int tile_rows = min(at.high, (DIR == kWeights ? p.out_rows : at.end - at.begin) - at.row0);
@@ -566,31 +566,35 @@ __global__ __launch_bounds__(256) void join_kernel(const float* __restrict__ par
   }
 }
 
+// Workgroups of a launch: a grid dimension holds less than 2^32 threads, and larger calls are several launches.
+constexpr int kMaxLaunch = 1 << 22;
+
 template <int EL, int OEL, int DIR, int BM, int BN, int RB, int WM, int WN, int ST, int MINB, bool TURNS>
-void launch(const GroupGemm& p, int blocks, hipStream_t s) {
-  hipLaunchKernelGGL((group_gemm_kernel<EL, OEL, DIR, BM, BN, RB, WM, WN, ST, MINB, TURNS>), dim3(blocks),
-                     dim3(WM * WN * 64), 0, s, p);
+void launch(GroupGemm p, hipStream_t s) {
+  for (p.first = 0; p.first < p.blocks; p.first += kMaxLaunch)
+    hipLaunchKernelGGL((group_gemm_kernel<EL, OEL, DIR, BM, BN, RB, WM, WN, ST, MINB, TURNS>),
+                       dim3(std::min(kMaxLaunch, p.blocks - p.first)), dim3(WM * WN * 64), 0, s, p);
 }
 
 template <int EL, int OEL, int DIR>
-void launch_shape(int shape, const GroupGemm& p, int blocks, hipStream_t s) {
-  if (shape == kSmall) return launch<EL, OEL, DIR, 64, 64, 128, 2, 2, 3, 3, false>(p, blocks, s);
-  if (shape == kNarrow) return launch<EL, OEL, DIR, 64, 128, 128, 2, 2, 3, 2, false>(p, blocks, s);
+void launch_shape(int shape, const GroupGemm& p, hipStream_t s) {
+  if (shape == kSmall) return launch<EL, OEL, DIR, 64, 64, 128, 2, 2, 3, 3, false>(p, s);
+  if (shape == kNarrow) return launch<EL, OEL, DIR, 64, 128, 128, 2, 2, 3, 2, false>(p, s);
   if constexpr (EL == EL_BF16) {
     if constexpr (DIR != kWeights)
-      if (shape == kFew) return launch<EL, OEL, DIR, 32, 64, 256, 1, 4, 3, 2, false>(p, blocks, s);
-    if (shape == kMiddle) return launch<EL, OEL, DIR, 128, 128, 128, 2, 2, 2, 2, false>(p, blocks, s);
-    if (shape == kWide) return launch<EL, OEL, DIR, 128, 256, 64, 2, 4, 3, 2, false>(p, blocks, s);
-    if (DIR == kWeights) return launch<EL, OEL, DIR, 256, 256, 128, 2, 4, 2, 1, true>(p, blocks, s);
-    return launch<EL, OEL, DIR, 256, 256, 64, 2, 4, 5, 1, true>(p, blocks, s);
+      if (shape == kFew) return launch<EL, OEL, DIR, 32, 64, 256, 1, 4, 3, 2, false>(p, s);
+    if (shape == kMiddle) return launch<EL, OEL, DIR, 128, 128, 128, 2, 2, 2, 2, false>(p, s);
+    if (shape == kWide) return launch<EL, OEL, DIR, 128, 256, 64, 2, 4, 3, 2, false>(p, s);
+    if (DIR == kWeights) return launch<EL, OEL, DIR, 256, 256, 128, 2, 4, 2, 1, true>(p, s);
+    return launch<EL, OEL, DIR, 256, 256, 64, 2, 4, 5, 1, true>(p, s);
   }
 }
 
 template <int DIR>
-void launch_types(int el, int oel, int shape, const GroupGemm& p, int blocks, hipStream_t s) {
-  if (el == EL_F32) launch_shape<EL_F32, EL_F32, DIR>(shape, p, blocks, s);
-  else if (oel == EL_F32) launch_shape<EL_BF16, EL_F32, DIR>(shape, p, blocks, s);
-  else launch_shape<EL_BF16, EL_BF16, DIR>(shape, p, blocks, s);
+void launch_types(int el, int oel, int shape, const GroupGemm& p, hipStream_t s) {
+  if (el == EL_F32) launch_shape<EL_F32, EL_F32, DIR>(shape, p, s);
+  else if (oel == EL_F32) launch_shape<EL_BF16, EL_F32, DIR>(shape, p, s);
+  else launch_shape<EL_BF16, EL_BF16, DIR>(shape, p, s);
 }
 
 Plan plan_of(int dir, int el, int oel, const GroupGemm& p) {
@@ -605,10 +609,6 @@ size_t group_gemm_workspace(int dir, int el, int oel, const GroupGemm& p) {
   return r.parts > 1 ? static_cast<size_t>(rows) * p.cols * r.parts * 4 : 0;
 }
 
-bool group_gemm_fits(int dir, int el, int oel, const GroupGemm& p) {
-  return plan_of(dir, el, oel, p).blocks < (1ll << 32) / 512;  // of threads, which a grid dimension counts
-}
-
 hipError_t launch_group_gemm(int dir, int el, int oel, GroupGemm p, void* ws, hipStream_t s) {
   const Plan r = plan_of(dir, el, oel, p);
   if (r.blocks == 0) return hipSuccess;
@@ -617,10 +617,10 @@ hipError_t launch_group_gemm(int dir, int el, int oel, GroupGemm p, void* ws, hi
   p.high = r.high;
   p.partial = static_cast<float*>(ws);
   p.part_stride = rows * p.cols;
-  const int blocks = static_cast<int>(r.blocks);
-  if (dir == kForward) launch_types<kForward>(el, oel, r.shape, p, blocks, s);
-  else if (dir == kRows) launch_types<kRows>(el, oel, r.shape, p, blocks, s);
-  else launch_types<kWeights>(el, oel, r.shape, p, blocks, s);
+  p.blocks = static_cast<int>(r.blocks);
+  if (dir == kForward) launch_types<kForward>(el, oel, r.shape, p, s);
+  else if (dir == kRows) launch_types<kRows>(el, oel, r.shape, p, s);
+  else launch_types<kWeights>(el, oel, r.shape, p, s);
   if (r.parts > 1) {
     const int64_t n4 = rows * p.cols / 4;
     const dim3 grid(static_cast<unsigned>(std::min<int64_t>((n4 + 255) / 256, 4096)));

@@ -60,6 +60,7 @@ struct Plan {
 };
 
 constexpr double kCus = 256;
+constexpr int kMaxTileRows = (1 << 25) - 1;  // of kForward and kRows: 64 lanes' counts add up in 32 bits
 constexpr int64_t kPartialBytes = 64 << 20;  // most that the parts of a call take of a workspace
 
 // Shape, parts of the reduction and most workgroups of a call: the least of what the shapes are expected to take,
@@ -78,6 +79,7 @@ inline Plan plan(int dir, const GroupSizes& p, bool f32, bool out_f32) {
   double least = 0;
   for (int i = 0; i < shapes; ++i) {
     const Shape& h = f32 ? kF32Shapes[i] : kBf16Shapes[i];
+    if (dir != kWeights && p.rows / h.bm + p.n_groups > kMaxTileRows) continue;  // 2^30 rows in the shortest tiles
     const double nt = std::ceil(static_cast<double>(p.cols) / h.bn);
     // a group's rows end inside a tile
     const double mt = dir == kWeights ? p.n_groups * std::ceil(static_cast<double>(p.out_rows) / h.bm)

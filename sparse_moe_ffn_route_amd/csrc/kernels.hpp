@@ -204,9 +204,9 @@ struct GroupGemm {
   int64_t part_stride;
   int parts;
   int high;                // set by the launcher: most rows of a tile (kForward, kRows)
+  int first, blocks;       // set by the launcher: workgroups before this launch, and of the call
 };
 size_t group_gemm_workspace(int dir, int el, int out_el, const GroupGemm& p);
-bool group_gemm_fits(int dir, int el, int out_el, const GroupGemm& p);  // one launch holds the call's tiles
 hipError_t launch_group_gemm(int dir, int el, int out_el, GroupGemm p, void* ws, hipStream_t stream);
 
 // SwiGLU with dropout, its gradient, and dropout on a residual branch (see dropout.hip).

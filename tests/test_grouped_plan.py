@@ -93,7 +93,7 @@ int main() {
   int dir, n, rows, N, K, f32, out_f32;
   while (std::scanf("%d %d %d %d %d %d %d", &dir, &n, &rows, &N, &K, &f32, &out_f32) == 7) {
     const moe::groups::Plan p = moe::groups::plan(dir, moe::group_sizes(dir, n, rows, N, K), f32, out_f32);
-    std::printf("%d %d\\n", p.shape, p.parts);
+    std::printf("%d %d %d %lld\\n", p.shape, p.parts, p.high, static_cast<long long>(p.blocks));
   }
 }
 """
@@ -105,17 +105,18 @@ def results_of(dtype):
 
 @pytest.fixture(scope="module")
 def plans(tmp_path_factory):
-    """Shape and parts of calls, asked of the library's own decision, compiled for the host alone."""
+    """Shape and parts (and a tile's rows and the workgroups) of calls, by the library's own choice, compiled for the host."""
     at = tmp_path_factory.mktemp("plan")
     (at / "ask.cpp").write_text(ASK)
     cc = shutil.which("g++") or os.path.join(os.path.dirname(build._hipcc()), "amdclang++")
     subprocess.run([cc, "-O1", "-std=c++17", "-I", build.CSRC, str(at / "ask.cpp"), "-o", str(at / "ask")], check=True)
 
-    def ask(calls):
+    def ask(calls, counts=False):
         lines = "\n".join(f"{DIRS.index(d)} {n} {rows} {N} {K} {int(t == 'f32')} {int(o == 'f32')}"
                           for d, n, rows, N, K, t, o in calls)
         got = subprocess.run([str(at / "ask")], input=lines, text=True, check=True, capture_output=True).stdout.split()
-        return [(SHAPES[int(s)], int(p)) for s, p in zip(got[::2], got[1::2])]
+        return [(SHAPES[int(s)], int(p)) + ((int(h), int(b)) if counts else ())
+                for s, p, h, b in zip(*(got[i::4] for i in range(4)))]
 
     return ask
 
@@ -138,6 +139,31 @@ def test_cases_take_the_shapes_they_are_for(plans):
 def test_slices_are_split(plans):
     assert plans([(dir, 1, sum(counts) + SPARE, N, K, t, o) for dir, counts, N, K, t, o, _, _ in SLICES]) == \
         [s[6:] for s in SLICES]
+
+
+def test_counts_of_the_largest_calls_fit(plans):
+    """Workgroups in 31 bits and tile rows in 25, up to the sizes that are refused."""
+    sizes = [(n, rows, N, K) for n in (1, 3, 1000, 1024) for rows in (0, 1, 1024, 1 << 20, (1 << 30) - 1, 1 << 30)
+             for N in (8, 1024, 8192, 1 << 20) for K in (8, 1024, 8192, 1 << 20)]
+    types = [("bf16", "bf16"), ("bf16", "f32"), ("f32", "f32")]
+    fit = [s for s in sizes if max(s[1] * s[2], s[1] * s[3], s[0] * s[2] * s[3]) <= 1 << 40]
+    calls = [(dir, *s, t, o) for s in fit for dir in DIRS for t, o in types]
+    for (dir, n, rows, *_), (_, _, high, blocks) in zip(calls, plans(calls, True)):
+        assert blocks < 1 << 31 and (dir == "weights" or rows // high + n < 1 << 25)
+    for n, rows, N, K in sizes:
+        for t, o in types:
+            need = moe.library().moe_grouped_gemm_workspace_bytes(moe.make_groups(n, rows, N, K, t, o))
+            assert (need > 0) == ((n, rows, N, K) in fit)
+
+
+def test_refusal_of_more_than_2_to_the_40_elements():
+    lib, fake = moe.library(), 256
+    for n, rows, N, K in ((1024, 8, 1 << 20, 1032), (1, 1 << 30, 1032, 8), (1, 1 << 30, 8, 1032)):
+        g = moe.make_groups(n, rows, N, K)
+        got = {lib.moe_grouped_gemm(g, fake, 0, None, fake, fake, None, fake, fake, 1 << 40, None),
+               lib.moe_grouped_gemm_backward_rows(g, fake, fake, fake, None, fake, fake, 1 << 40, None),
+               lib.moe_grouped_gemm_backward_weights(g, fake, fake, 0, None, fake, None, fake, fake, 1 << 40, None)}
+        assert got == {moe.ERR_UNSUPPORTED}
 
 
 def whole(shape, dtype, seed):
@@ -215,3 +241,52 @@ def test_a_slice_of_the_groups_in_parts(dir, counts, N, K, dtype, out, shape, pa
         c = Call(dir, counts, N, K, dtype, out, False, add, seed=K)
         rows = sum(counts) + SPARE
         c.check(c.offsets[1:3].clone(), moe.make_groups(1, rows, N, K, dtype, out), c.at[1:3], c.w[1:2])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dir,rows,n,dtype,gather", [
+    ("fwd", 1 << 29, 3, "f32", False), ("rows", 1 << 29, 100, "f32", False), ("fwd", 1 << 30, 100, "bf16", False),
+    ("rows", 1 << 30, 3, "bf16", False), ("fwd", (1 << 29) + 77, 1024, "bf16", True)])
+def test_more_tile_rows_than_a_grid_dimension_holds(dir, rows, n, dtype, gather):
+    """2^23 tiles and more, whose threads are 2^31 and more: every row of 8 values, in several launches."""
+    N = K = 8
+    counts = torch.randint(0, 2 * (rows // n), (n,), generator=torch.Generator().manual_seed(n))
+    counts[n // 2] = 0
+    while counts.sum() > rows - 50:
+        counts //= 2
+    counts[-1] += rows - 50 - counts.sum()
+    offsets = torch.zeros(n + 1, dtype=torch.int64)
+    offsets[1:] = counts.cumsum(0)
+    src = 1000 if gather else rows
+    a, w = torch.empty(src, 8, dtype=DT[dtype], device="cuda").random_(-3, 4), whole((n, N, K), dtype, 1)
+    index = torch.empty(rows, dtype=torch.int32, device="cuda").random_(0, src) if gather else None
+    out = torch.full((rows, 8), 777.0, dtype=DT[dtype], device="cuda")
+    call(dir, moe.make_groups(n, rows, N, K, dtype), a, a, w, offsets.int().cuda(), out, index)
+    at, m = offsets.tolist(), w.float()
+    for e, (b, t) in enumerate(zip(at, at[1:])):
+        for r in range(b, t, 1 << 24):
+            r = slice(r, min(t, r + (1 << 24)))
+            x = (a[index[r].long()] if gather else a[r]).float()
+            assert torch.equal(out[r], (x @ (m[e].T if dir == "fwd" else m[e])).to(DT[dtype])), (e, r)
+    assert (out[at[-1]:] == 777).all()
+    del a, index, out, x
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+def test_more_tiles_of_weights_than_a_grid_dimension_holds(out):
+    """2^23 tiles of the weights' gradient, 8 x 2^20 in each of 1024 groups."""
+    n, rows, N, K = 1024, 100, 8, 1 << 20
+    d_out, a = whole((rows, N), "bf16", 1), whole((rows, K), "bf16", 2)
+    at = [0] * 300 + [40] * 500 + [99] * 225
+    got = torch.full((n, N, K), 777.0, dtype=DT[out], device="cuda")
+    call("weights", moe.make_groups(n, rows, N, K, "bf16", out), a, d_out, None,
+         torch.tensor(at, dtype=torch.int32, device="cuda"), got)
+    for e in (299, 799):
+        b, t = at[e:e + 2]
+        assert torch.equal(got[e], (d_out[b:t].float().T @ a[b:t].float()).to(DT[out]))
+        got[e] = 0
+    assert not any(got[e:e + 64].any() for e in range(0, n, 64))
+    del got
+    torch.cuda.empty_cache()
