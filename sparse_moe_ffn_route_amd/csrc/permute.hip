@@ -67,12 +67,12 @@ __global__ __launch_bounds__(256) void perm_rank_kernel(const int32_t* __restric
                                                         uint8_t* __restrict__ qdst, float* __restrict__ qscale) {
   __shared__ int32_t run[kWavesPerBlock][kMaxLocalExperts];
   const int w = threadIdx.x / kWave, lane = lane_id();
-  if (static_cast<int>(blockIdx.x) >= rank_blocks) {
-    const int r = (static_cast<int>(blockIdx.x) - rank_blocks) * kWavesPerBlock + w;
+  if (wide_block() >= rank_blocks) {
+    const int r = (wide_block() - rank_blocks) * kWavesPerBlock + w;
     if (r < qrows) quant_row<EL_BF16>(qsrc, r, qcols, lane, qdst, qscale);
     return;
   }
-  const int u = blockIdx.x * kWavesPerBlock + w;
+  const int u = wide_block() * kWavesPerBlock + w;
   if (u >= n_units) return;  // whole wave leaves together; waves use disjoint LDS rows
   const int base_i = u * kPermUnit;
   int pe[kUnitSteps];
@@ -340,7 +340,7 @@ __global__ __launch_bounds__(256) void gather_rows_kernel(const uint8_t* __restr
                                                           const int32_t* __restrict__ n_rows_dev,
                                                           int row_bytes, uint8_t* __restrict__ dst,
                                                           float* __restrict__ dst_scale) {
-  const int r = blockIdx.x;
+  const int r = wide_block();
   if (r >= *n_rows_dev) return;
   const int t = perm_token[r];
   const uint4* s = reinterpret_cast<const uint4*>(src + static_cast<size_t>(t) * row_bytes);
@@ -472,7 +472,7 @@ __global__ __launch_bounds__(256) void quant_rows_kernel(const void* __restrict_
                                                          const int32_t* __restrict__ n_rows_dev, int cols,
                                                          uint8_t* __restrict__ dst, float* __restrict__ scale,
                                                          const int32_t* __restrict__ skip_inv, int skip_k) {
-  const int r = blockIdx.x * kWavesPerBlock + threadIdx.x / kWave;
+  const int r = wide_block() * kWavesPerBlock + threadIdx.x / kWave;
   const int lane = lane_id();
   const int n = n_rows_dev ? *n_rows_dev : rows;
   if (r >= n) return;
@@ -537,7 +537,7 @@ hipError_t launch_permute(const int32_t* packed, int T, int k, int E, int e_begi
   const int n_units = perm_units(T, k);
   const int blocks = (n_units + kWavesPerBlock - 1) / kWavesPerBlock;
   const int q_blocks = xq_src ? (T + kWavesPerBlock - 1) / kWavesPerBlock : 0;
-  hipLaunchKernelGGL(perm_rank_kernel, dim3(blocks + q_blocks), dim3(256), 0, stream, packed, n_pairs, k, e_begin,
+  hipLaunchKernelGGL(perm_rank_kernel, wide_grid(blocks + q_blocks), dim3(256), 0, stream, packed, n_pairs, k, e_begin,
                      n_local, E, n_bits, n_units, rank, hist, bad, blocks, xq_src, xq_src ? T : 0, xq_cols,
                      static_cast<uint8_t*>(xq_dst), xq_scale);
   hipLaunchKernelGGL(perm_scan_kernel, dim3(1), dim3(1024), 0, stream, hist, n_local, n_units, bm0, bm1, base,
@@ -551,7 +551,7 @@ hipError_t launch_gather_rows(const void* src, const float* src_scale, const int
                               const int32_t* n_rows_dev, int max_rows, int row_bytes, void* dst, float* dst_scale,
                               hipStream_t stream) {
   if (max_rows == 0) return hipSuccess;
-  hipLaunchKernelGGL(gather_rows_kernel, dim3(max_rows), dim3(256), 0, stream,
+  hipLaunchKernelGGL(gather_rows_kernel, wide_grid(max_rows), dim3(256), 0, stream,
                      static_cast<const uint8_t*>(src), src_scale, perm_token, n_rows_dev, row_bytes,
                      static_cast<uint8_t*>(dst), dst_scale);
   return hipGetLastError();
@@ -560,7 +560,7 @@ hipError_t launch_gather_rows(const void* src, const float* src_scale, const int
 hipError_t launch_quant_rows(int in_el, const void* src, int rows, const int32_t* n_rows_dev, int cols, void* dst,
                              float* scale, hipStream_t stream, const int32_t* skip_inv, int skip_k) {
   if (rows == 0) return hipSuccess;
-  dim3 grid((rows + kWavesPerBlock - 1) / kWavesPerBlock);
+  const dim3 grid = wide_grid((rows + kWavesPerBlock - 1) / kWavesPerBlock);
   if (in_el == EL_BF16)
     hipLaunchKernelGGL(quant_rows_kernel<EL_BF16>, grid, dim3(256), 0, stream, src, rows, n_rows_dev, cols,
                        static_cast<uint8_t*>(dst), scale, skip_inv, skip_k);
