@@ -22,7 +22,7 @@ __global__ __launch_bounds__(256) void route_kernel(const float* __restrict__ pa
                                                     int T, int E, int k, int renormalize,
                                                     int32_t* __restrict__ packed) {
   const int lane = lane_id();
-  const int t = blockIdx.x * (blockDim.x / kWave) + threadIdx.x / kWave;
+  const int t = wide_block() * (blockDim.x / kWave) + threadIdx.x / kWave;
   if (t >= T) return;
   const size_t part_stride = static_cast<size_t>(T) * E;
   const float* row = (SPLIT ? parts : logits) + static_cast<size_t>(t) * E;
@@ -73,7 +73,7 @@ hipError_t launch_route(const float* parts, int n_parts, float* logits, const fl
                         int renormalize, int32_t* packed, hipStream_t stream) {
   if (T == 0) return hipSuccess;
   const int waves_per_block = 4;
-  dim3 grid((T + waves_per_block - 1) / waves_per_block);
+  const dim3 grid = wide_grid((T + waves_per_block - 1) / waves_per_block);
   const dim3 block(waves_per_block * kWave);
   // keys per lane: 8 cover up to 512 experts, kMaxKeysPerLane the largest E accepted
   if (E <= 8 * kWave) {

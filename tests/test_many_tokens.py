@@ -1,4 +1,4 @@
-"""Grouping of more tokens than one grid dimension holds threads for (a launch of more drops what is over)."""
+"""Routing and grouping of more tokens than one grid dimension holds threads for (a launch of more drops what is over)."""
 
 import pytest
 import torch
@@ -59,3 +59,16 @@ def test_every_token_is_quantised():
     del x, perm, x_perm, scale
     torch.cuda.empty_cache()
 
+
+def test_every_token_is_routed():
+    T, E, k = (1 << 26) + 5, 4, 2
+    d = moe.make_dims(T, 64, E, k, 64)
+    logits, packed = gpu(T, E, dtype=torch.float32).normal_(), gpu(T, 2, k).fill_(-7)
+    moe.moe_route(d, None, None, logits, None, packed)
+    for t in range(0, T, STEP):
+        top, ids = logits[t:t + STEP].sort(dim=1, descending=True, stable=True)
+        assert torch.equal(packed[t:t + STEP, 0], ids[:, :k].int()), t
+        w = packed[t:t + STEP, 1].contiguous().view(torch.float32)
+        assert (w - torch.softmax(top[:, :k], 1)).abs().max() <= 16 * 2.0 ** -24, t
+    del logits, packed, top, ids, w
+    torch.cuda.empty_cache()
