@@ -434,6 +434,10 @@ int moe_block_forward(const moe_dims* dims, const moe_weights* weights, const vo
  *   moe_permute_backward             rows' gradients -> d_x
  *   moe_route_backward               d_weights and the router's losses -> d_logits, which goes through
  *                                    the two products with one group (the router's matrix)
+ * Those two take an E that is a multiple of 8 (the products' N).  With another E, train over the next multiple, P: the
+ * router's matrix with P - E rows of zeros behind it, logit_bias with -inf there, dims' E = P and n_local = E.  The
+ * experts that are closed so have probability 0, no token (top_k <= E) and zeros in d_logits; load balance is then P / E
+ * times as large, and d_loss[0] times E / P gives the gradient for E experts.
  * Tensors of at least 16-byte alignment where a call says so (else MOE_ERR_UNSUPPORTED).
  */
 
