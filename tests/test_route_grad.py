@@ -115,6 +115,24 @@ def test_losses_and_gradient(T, E, k, renorm, mask, bias):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("mask,bias", [(False, False), (True, True)])
+@pytest.mark.parametrize("T,E,k", CASES + [(5000, 64, 4), (9000, 512, 10)])
+def test_losses_are_sums_of_few_steps(T, E, k, mask, bias):
+    """The losses to the steps that their sums have.  Tokens go round 128 workgroups of 16 waves: a wave adds up its own
+    ceil(T / 2048), a workgroup its 16 waves, the join b / f workgroups and f such sums, with f = 1024 over the experts'
+    next power of two (64 at least), then over a wave in 6 and 16 of those; and up to 8 products and quotients.  The
+    log of a sum that is off by P is off by P, and rounded with the largest key, U of each."""
+    c = Case(T, E, k, True, mask, bias)
+    (bal, z), _, _, _ = c.reference(False, True)
+    loss, _, _ = c.run("f32", False, True)
+    blocks, f = min(128, -(-T // 16)), 1024 // max(64, 1 << (E - 1).bit_length())
+    steps = -(-T // 2048) + 16 + -(-blocks // f) + f + 6 + 16 + 8
+    top = float(c.key[c.key.isfinite()].abs().max())
+    assert abs(loss[0] - bal) <= (steps * U + P) * bal
+    assert abs(loss[1] - z) <= steps * U * z + 2 * z.sqrt() * (P + 2 * U * (top + 8))
+
+
+@pytest.mark.gpu
 def test_calls_repeat_bit_for_bit():
     c = Case(3000, 512, 10, True, True, True)
     a, b = c.run(), c.run()
