@@ -23,7 +23,8 @@
 //     memory): 235 against 258 us.  kWeights keeps two of 128: its rows are whole lines either way.
 //   - Smaller tiles at two or three workgroups a CU fill each other's gaps instead and cover each other's stores,
 //     with more to load a product; waves that multiply go first (512 rows a group: kRows in kWide 375 -> 365 us,
-//     kForward in kWide 355 -> 344, in kFew 830 -> 773).  kWeights loses by that (506 -> 520) and has none of it.
+//     kForward in kWide 355 -> 344, in kFew 830 -> 773).  kWeights loses by that (506 -> 520) and has it only where a
+//     workgroup's halves take turns (kBig).
 //   - A reduction that is long for the tiles there are is split into parts (16 x 4096 x 4096 kForward 22 -> 12.5 us,
 //     8192 rows into 512 x 512 49 -> 18), summed in order by a second launch: no atomics, the same bits every time.
 //   - A matrix that one tile row reads bypasses the caches' replacement (10 rows a group: 104 -> 86 us), as do
