@@ -16,6 +16,7 @@
 //   * beyond: rank within 1024-pair units (one wave each), one-workgroup scan over
 //     experts, then one thread per pair places it.
 #include "common.hpp"
+#include "grid.hpp"
 #include "kernels.hpp"
 
 namespace moe {

@@ -7,6 +7,7 @@
 //
 // One wave64 per token; the selection itself is select_topk (topk.hpp).
 #include "common.hpp"
+#include "grid.hpp"
 #include "kernels.hpp"
 #include "topk.hpp"
 

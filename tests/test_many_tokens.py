@@ -1,4 +1,4 @@
-"""Routing and grouping of more tokens than one grid dimension holds threads for (a launch of more drops what is over)."""
+"""Routing and grouping of more tokens than one grid dimension holds threads for (a launch of more runs in part, without an error)."""
 
 import pytest
 import torch
